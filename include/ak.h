@@ -18,6 +18,12 @@
  *                   ones (tile-scan PR #202, first paragraph and paragraph
  *                   "Alternatives").
  *
+ * Four more carry the same scans and folds into sequence models: the
+ * layout of a batch from its request lengths (ak_batch_layout), linear
+ * attention with a decay for each head (ak_linear_attention, its gradients
+ * and its single-token step), and the verification of drafted tokens
+ * (ak_verify_drafts).
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Pointers. Arrays (src, dst, workspace) are DEVICE pointers to memory of the
@@ -357,6 +363,150 @@ ak_status ak_reduce_noalloc(const void* src, int64_t n, ak_dtype in, ak_map f, a
 ak_status ak_dims_select(int64_t inner, int64_t red_len, int64_t outer, int elem_bytes,
                          int vec_elems, int sm_count, int forced_shape, int32_t* shape_out,
                          int32_t* tile_outputs, int32_t* row_groups, int32_t* split);
+
+/* ---------------------------------------------------------------------------
+ * ak_batch_layout: block tables, slot maps and packed offsets of a batch,
+ * from its requests' lengths, without the lengths ever reaching the host.
+ * With ctx_r tokens of request r in a paged cache of blocks of b tokens and
+ * new_r tokens to run:
+ *   offsets[r] = new_0 + ... + new_{r-1}           (exclusive scan, nreq + 1 values)
+ *   blocks ceil(ctx_r / b) .. ceil((ctx_r + new_r) / b) - 1 of request r are
+ *     taken from free_blocks, front to back, in request order, and entered
+ *     in its row of block_table (other entries stay as they are)
+ *   token t of request r: positions[t] = ctx_r + t - offsets[r],
+ *     requests[t] = r, slots[t] = block_table[r][pos / b] * b + pos % b
+ *
+ *   ctx_lens, new_lens  device, nreq int32 (negative values count as 0)
+ *   block_table  device, nreq rows of table_width int32, table_stride apart
+ *   free_blocks  device, nfree int32; not changed: counts[1] of them are used
+ *   offsets      device, nreq + 1 int32
+ *   slots        device, max_tokens int64; positions, requests: max_tokens
+ *                int32. Entries past the batch's last token get slot -1,
+ *                position 0 and request -1.
+ *   counts       device, 2 int32: tokens of the batch, blocks it takes
+ * What does not fit is never written: tokens past max_tokens are left out, a
+ * block past the free list enters as -1, and a token in such a block or past
+ * the table's width (or in a block whose entry is negative) gets slot -1;
+ * the caller compares counts with max_tokens and nfree. The sums of tokens
+ * and of blocks must stay below 2^31.
+ * ------------------------------------------------------------------------- */
+ak_status ak_batch_layout_workspace_size(int64_t nreq, const ak_opts* opts, size_t* bytes);
+ak_status ak_batch_layout(const int32_t* ctx_lens, const int32_t* new_lens, int64_t nreq, int32_t* block_table,
+                          int64_t table_stride, int32_t table_width, const int32_t* free_blocks, int64_t nfree,
+                          int32_t block_size, int64_t max_tokens, int32_t* offsets, int64_t* slots,
+                          int32_t* positions, int32_t* requests, int32_t* counts, void* workspace,
+                          size_t workspace_bytes, const ak_opts* opts, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ak_verify_drafts: how many of its drafted tokens each request keeps, and
+ * the token after them, from given random numbers. Request r drafted tokens
+ * d_0 .. d_{m-1} (m = draft_counts[r], or k) from distributions q_j; the
+ * target's are p_0 .. p_m. With
+ *   a = the first j < m for which u_j * q_j(d_j) < p_j(d_j) is false, or m
+ * accepted[r] = a and tokens[r] = d_0 .. d_{a-1}, x, -1, -1, ... with
+ *   x = argmax_v max(p_a(v) - q_a(v), 0) / e_v   if a < m
+ *   x = argmax_v p_a(v) / e_v                    if a = m
+ * (ties: the lowest v), which, for u uniform in [0, 1) and e exponential,
+ * leaves the emitted tokens distributed as the target's own.
+ *
+ *   target_probs  device, element (r, j, v) at r*target_req + j*target_row + v,
+ *                 j <= k; AK_F32 or AK_BF16, as are the draft's
+ *   draft_probs   device, likewise with j < k; NULL: each draft was certain
+ *                 (q_j is 1 at d_j and 0 elsewhere)
+ *   draft_tokens  device, nreq * k int32; a token outside [0, vocab) is
+ *                 refused
+ *   draft_counts  device, nreq int32, clamped to [0, k]; NULL: all k
+ *   uniform       device, nreq * k float
+ *   noise         device, one row of vocab float > 0 for each request,
+ *                 noise_stride apart
+ *   tokens        device, nreq * (k + 1) int32
+ *   accepted      device, nreq int32
+ * Differences and quotients are rounded to float32. Candidates need a weight
+ * above zero; scores that are NaN are passed over. If the difference leaves
+ * no candidate (p = q up to rounding), p alone decides; if that leaves none,
+ * x is -1. k may be 0. No workspace.
+ * ------------------------------------------------------------------------- */
+ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t target_row, const void* draft_probs,
+                           int64_t draft_req, int64_t draft_row, ak_dtype dtype, const int32_t* draft_tokens,
+                           const int32_t* draft_counts, const float* uniform, const float* noise,
+                           int64_t noise_stride, int64_t nreq, int32_t k, int64_t vocab, int32_t* tokens,
+                           int32_t* accepted, const ak_opts* opts, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the scan whose state is a
+ * matrix. For each head h and sequence, with g = exp(log_decay[h]):
+ *   S_t = g * S_{t-1} + k_t v_t^T      (dk x dv, float32)
+ *   o_t = scale * S_t^T q_t            (the token itself included)
+ * Sequences are packed along the token axis: sequence n holds tokens
+ * offsets[n] .. offsets[n+1]-1 (the offsets of ak_batch_layout), some may be
+ * empty. S starts from state_in, or zero.
+ *
+ * ak_heads describes one [tokens][heads][dim] array: element (t, h, i) at
+ * t*token_stride + h*head_stride + i (strides in elements, >= 0; a head
+ * stride of 0 shares one head among all in an input).
+ *
+ * ak_linattn, the shape of a call:
+ *   dtype     AK_F32 or AK_BF16: of q, k, v, o and their gradients; products
+ *             are summed in float32, and states are float32 throughout
+ *   tokens, seqs, heads; dk, dv in 1 .. 256
+ *   max_len   a bound on the longest sequence, or 0 (unknown); it only
+ *             guides how the token axis is cut
+ *   scale     finite
+ *
+ *   log_decay  device, heads float, normally <= 0; -infinity: no memory
+ *   offsets    device, seqs + 1 int32, non-decreasing; NULL: one sequence of
+ *              all tokens (seqs = 1). Values are clamped to [0, tokens].
+ *              Output rows of tokens outside every sequence are set to 0.
+ *   state_in   device, seqs*heads matrices, dk x dv with dv contiguous, or NULL
+ *   state_out  device, the states after each sequence's last token, or NULL;
+ *              may be state_in
+ * Within the types' rounding the order of summation is fixed by the shape:
+ * equal calls give equal bits. In bf16 calls weighted scores and the state
+ * are rounded to bf16 where they enter a product with q or v. A NaN or
+ * infinity reaches the later tokens of its sequence and head, and may reach
+ * up to 127 earlier ones.
+ *
+ * ak_linear_attention_backward: the gradients of sum(o * do) +
+ * sum(state_out * dstate_out), from the forward call's inputs; dq, dk, dv as
+ * q, k, v are described; dstate_in (may be NULL) receives the gradient of
+ * state_in. log_decay and scale are constants of the model and get none.
+ * dstate_in may be dstate_out.
+ *
+ * ak_linear_attention_step: one token for each of `tokens` requests (seqs,
+ * offsets and max_len unused), the state updated in place. Request b uses
+ * matrices slots[b] of nslots in `state` (slots NULL: b). An index outside
+ * [0, nslots) marks padding: its output is 0. Indices must not repeat.
+ *
+ * opts->target_blocks: windows the token axis is cut into (0 = automatic).
+ * ------------------------------------------------------------------------- */
+typedef struct ak_heads {
+    void* data;
+    int64_t token_stride, head_stride;
+} ak_heads;
+
+typedef struct ak_linattn {
+    int64_t tokens, seqs, max_len;
+    int32_t heads, dk, dv;
+    int32_t dtype; /* ak_dtype */
+    float scale;
+    int32_t reserved; /* must be 0 */
+} ak_linattn;
+
+/* Enough for the forward and the backward pass of a shape. */
+ak_status ak_linear_attention_workspace_size(const ak_linattn* shape, const ak_opts* opts, size_t* bytes);
+ak_status ak_linear_attention(const ak_linattn* shape, const ak_heads* q, const ak_heads* k, const ak_heads* v,
+                              const float* log_decay, const int32_t* offsets, const float* state_in,
+                              const ak_heads* o, float* state_out, void* workspace, size_t workspace_bytes,
+                              const ak_opts* opts, void* stream);
+ak_status ak_linear_attention_backward(const ak_linattn* shape, const ak_heads* d_o, const ak_heads* q,
+                                       const ak_heads* k, const ak_heads* v, const float* log_decay,
+                                       const int32_t* offsets, const float* state_in, const float* dstate_out,
+                                       const ak_heads* dq, const ak_heads* dk, const ak_heads* dv,
+                                       float* dstate_in, void* workspace, size_t workspace_bytes,
+                                       const ak_opts* opts, void* stream);
+ak_status ak_linear_attention_step(const ak_linattn* shape, const ak_heads* q, const ak_heads* k, const ak_heads* v,
+                                   const float* log_decay, float* state, const int32_t* slots, int64_t nslots,
+                                   const ak_heads* o, const ak_opts* opts, void* stream);
 
 #ifdef __cplusplus
 }

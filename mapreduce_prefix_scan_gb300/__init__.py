@@ -20,11 +20,16 @@ import torch
 
 from . import _abi
 from ._abi import DTYPES, MAPS, MAPS2, OPS, SHAPES, STORES
+from .sequence import (BatchLayout, ak_batch_layout, ak_batch_layout_workspace_size, ak_linear_attention,
+                       ak_linear_attention_backward, ak_linear_attention_step, ak_linear_attention_workspace_size,
+                       ak_verify_drafts)
 
 __all__ = ["AkError", "ak_reduce", "ak_reduce2", "ak_reduce_dims", "ak_accumulate", "ak_reduce_workspace_size",
            "ak_reduce_dims_workspace_size", "ak_accumulate_workspace_size", "ak_status_string",
            "ak_kernel_launch_count", "ak_dims_select", "ak_scan_status", "ak_findall",
-           "ak_findall_workspace_size", "make_opts", "lib"]
+           "ak_findall_workspace_size", "make_opts", "lib", "BatchLayout", "ak_batch_layout",
+           "ak_batch_layout_workspace_size", "ak_verify_drafts", "ak_linear_attention",
+           "ak_linear_attention_backward", "ak_linear_attention_step", "ak_linear_attention_workspace_size"]
 
 _TORCH = {torch.float32: "f32", torch.float64: "f64", torch.bfloat16: "bf16", torch.int32: "i32",
           torch.int64: "i64", torch.uint8: "u8", torch.bool: "u8"}

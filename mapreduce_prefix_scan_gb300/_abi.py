@@ -27,7 +27,9 @@ EXPORTS = ("ak_opts_default", "ak_status_string", "ak_dtype_size", "ak_last_cuda
            "ak_kernel_launch_count", "ak_reduce_workspace_size", "ak_reduce", "ak_reduce2",
            "ak_reduce_dims_workspace_size", "ak_reduce_dims", "ak_accumulate_workspace_size",
            "ak_accumulate", "ak_scan_status", "ak_findall_workspace_size", "ak_findall", "ak_dims_select",
-           "ak_reduce_noalloc")
+           "ak_reduce_noalloc", "ak_batch_layout_workspace_size", "ak_batch_layout", "ak_verify_drafts",
+           "ak_linear_attention_workspace_size", "ak_linear_attention", "ak_linear_attention_backward",
+           "ak_linear_attention_step")
 
 
 class ak_opts(ctypes.Structure):
@@ -36,6 +38,16 @@ class ak_opts(ctypes.Structure):
                 ("check", ctypes.c_int32), ("flags", ctypes.c_int32),
                 ("exclusive", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("wait_limit_ns", ctypes.c_int64), ("debug_skip_publish_tile", ctypes.c_int64)]
+
+
+class ak_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class ak_linattn(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int64), ("max_len", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -80,9 +92,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.ak_findall.argtypes = [P, I64, I32, P, P, P, P, SZ, PO, P]
     L.ak_dims_select.argtypes = [I64, I64, I64, I32, I32, I32, I32, PI32, PI32, PI32, PI32]
     L.ak_reduce_noalloc.argtypes = [P, I64, I32, I32, I32, I32, I32, P, I32, P, P, PO, P]
+    PH, PL = ctypes.POINTER(ak_heads), ctypes.POINTER(ak_linattn)
+    L.ak_batch_layout_workspace_size.argtypes = [I64, PO, PSZ]
+    L.ak_batch_layout.argtypes = [P, P, I64, P, I64, I32, P, I64, I32, I64, P, P, P, P, P, P, SZ, PO, P]
+    L.ak_verify_drafts.argtypes = [P, I64, I64, P, I64, I64, I32, P, P, P, P, I64, I64, I32, I64, P, P, PO, P]
+    L.ak_linear_attention_workspace_size.argtypes = [PL, PO, PSZ]
+    L.ak_linear_attention.argtypes = [PL, PH, PH, PH, P, P, P, PH, P, P, SZ, PO, P]
+    L.ak_linear_attention_backward.argtypes = [PL, PH, PH, PH, PH, P, P, P, P, PH, PH, PH, P, P, SZ, PO, P]
+    L.ak_linear_attention_step.argtypes = [PL, PH, PH, PH, P, P, P, I64, PH, PO, P]
     for f in ("ak_reduce_workspace_size", "ak_reduce", "ak_reduce2", "ak_reduce_dims_workspace_size", "ak_reduce_dims",
               "ak_accumulate_workspace_size", "ak_accumulate", "ak_scan_status", "ak_findall_workspace_size",
-              "ak_findall", "ak_dims_select", "ak_reduce_noalloc"):
+              "ak_findall", "ak_dims_select", "ak_reduce_noalloc", "ak_batch_layout_workspace_size",
+              "ak_batch_layout", "ak_verify_drafts", "ak_linear_attention_workspace_size", "ak_linear_attention",
+              "ak_linear_attention_backward", "ak_linear_attention_step"):
         getattr(L, f).restype = I32
     if path == LIB_PATH:
         _lib = L

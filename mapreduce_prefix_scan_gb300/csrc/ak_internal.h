@@ -285,4 +285,81 @@ ak_status run_findall(const void* src, int64_t n, ak_dtype in, int64_t* idx, int
                       int64_t ntiles, size_t ws_bytes, uint64_t epoch, int64_t wait_limit_ns, int64_t skip_tile,
                       int target_blocks, cudaStream_t stream);
 
+// ---------------------------------------------------------------------------
+// sequence operators (sequence_api.cu validates, the named files launch)
+// ---------------------------------------------------------------------------
+
+// batch_layout.cu
+struct LayoutCall {
+    const int32_t *ctx_lens, *new_lens;
+    int64_t nreq;
+    int32_t* table;
+    int64_t table_stride;
+    int32_t table_width;
+    const int32_t* free_blocks;
+    int64_t nfree;
+    int32_t block_size;
+    int32_t block_shift;  // log2 of block_size, or -1
+    int64_t max_tokens;
+    int32_t* offsets;
+    int64_t* slots;
+    int32_t *positions, *requests, *counts;
+    bool vec;  // slots, positions and requests are 16-byte aligned
+    // filled in by run_layout
+    int64_t tokens_per_block;
+    uint64_t* tile_sums;
+    int32_t* base;
+};
+size_t layout_workspace(int64_t nreq);
+ak_status run_layout(LayoutCall c, void* ws, cudaStream_t stream);
+
+// verify_drafts.cu
+struct VerifyCall {
+    const void *p, *q;  // q may be null
+    ak_dtype dtype;
+    int64_t p_req, p_row, q_req, q_row;  // element strides
+    const int32_t* drafts;   // [nreq][k]
+    const int32_t* counts;   // [nreq] or null
+    const float* uniform;    // [nreq][k]
+    const float* noise;
+    int64_t noise_stride;
+    int64_t nreq, vocab;
+    int32_t k;
+    int32_t* tokens;    // [nreq][k + 1]
+    int32_t* accepted;  // [nreq]
+};
+ak_status run_verify(const VerifyCall& c, cudaStream_t stream);
+
+// linattn.cu
+struct LinattnCall {
+    ak_dtype dtype;
+    int64_t tokens, seqs, max_len;
+    int heads, dk, dv;
+    float scale;
+    int64_t windows;  // 0 = automatic
+    ak_heads q, k, v, o;  // o: the output, or its gradient in the backward pass
+    ak_heads dq, dk_out, dvv;
+    const float* log_decay;
+    const int32_t* offsets;
+    const float* state_in;
+    float* state_out;
+    const float* dstate_out;  // gradient of the final state, or null
+    float* dstate_in;         // gradient of the initial state, or null
+    cudaStream_t stream;
+};
+size_t linattn_workspace(const LinattnCall& c, const DeviceInfo& dev);
+ak_status run_linattn(const LinattnCall& c, void* ws, cudaStream_t stream);
+ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stream);
+ak_status run_linattn_step(const LinattnCall& c, float* state, const int32_t* slots, int64_t nslots,
+                           cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// helpers of the entry points (api.cu)
+// ---------------------------------------------------------------------------
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+ak_opts resolve_opts(const ak_opts* o);
+bool log_on();
+void log_call(const char* fmt, ...);
+ak_status sync_and_check(cudaStream_t s);
+
 }  // namespace ak

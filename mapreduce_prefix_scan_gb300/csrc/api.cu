@@ -95,9 +95,7 @@ static ak_status check_types(ak_dtype in, ak_map f, ak_op op, ak_dtype acc, ak_d
     return dispatch_types(in, acc, out, [](auto, auto, auto) { return AK_OK; });
 }
 
-static bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-static ak_opts resolve_opts(const ak_opts* o) {
+ak_opts resolve_opts(const ak_opts* o) {
     ak_opts r;
     ak_opts_default(&r);
     if (o) r = *o;
@@ -178,12 +176,12 @@ static ak_status host_finish(const void* bare, ak_dtype in, ak_dtype acc, ak_dty
 // AK_LOG set (and not "0") in the environment: one line per call on stderr
 // naming the path the call takes -- kernel, grid or tile count, dims shape.
 // The variable is read on every call, so it can be switched at run time.
-static bool log_on() {
+bool log_on() {
     const char* v = getenv("AK_LOG");
     return v && *v && strcmp(v, "0") != 0;
 }
 
-static void log_call(const char* fmt, ...) {
+void log_call(const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     char line[256];
@@ -202,7 +200,7 @@ static const char* op_name(ak_op op) {
     return (int)op >= 0 && (int)op < 5 ? names[op] : "?";
 }
 
-static ak_status sync_and_check(cudaStream_t s) {
+ak_status sync_and_check(cudaStream_t s) {
     cudaError_t e = cudaStreamSynchronize(s);
     return e == cudaSuccess ? AK_OK : cuda_fail(e);
 }

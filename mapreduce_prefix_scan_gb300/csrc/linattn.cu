@@ -1,0 +1,461 @@
+// linattn.cu -- linear attention with a decay for each head: the token-by-
+// token kernel for every type and head size, the join of window states, the
+// single-token step and the choice between the kernels (linattn.cuh has the
+// mathematics; linattn_mma.cu the chunked tensor-core kernel).
+#include <algorithm>
+
+#include "linattn.cuh"
+
+namespace ak {
+namespace la {
+
+__device__ __forceinline__ float as_f(float v) { return v; }
+__device__ __forceinline__ float as_f(bf16 v) { return __bfloat162float(v); }
+template <class T>
+__device__ __forceinline__ T from_f(float v) {
+    if constexpr (std::is_same_v<T, bf16>) return __float2bfloat16_rn(v);
+    else return v;
+}
+
+// ---------------------------------------------------------------------------
+// token by token
+// ---------------------------------------------------------------------------
+// A block holds 32 columns of the state of one head: 4 groups of DK / 4 rows
+// x 32 columns, a column's rows of a group in one thread's registers, so the
+// state is read and written once a sequence piece. k, q and v of kTile tokens
+// are staged in shared memory (k and q are read as 16-byte broadcasts); the
+// groups' parts of each output are added in shared memory once a tile.
+//
+// The decay leaves the inner loop: with X = g S before a block of b tokens,
+//   S_e = g^e (X + sum_{j<=e} g^-j k_j v_j^T),  e = 0 .. b - 1,
+// so v enters scaled by g^-j, o leaves scaled by g^e, and the state is scaled
+// once a block (by a two-float factor). b is the largest power of two up to
+// kTile that keeps g^-j below e^40. That is 2 DK fused operations a column
+// and token: bound by the FMA pipe for long inputs and by the chain of tokens
+// for few heads (hence the windows).
+constexpr int kTile = 16;
+constexpr int kGroups = 4;
+constexpr int kThreads = 32 * kGroups;
+
+template <class T, int DK, bool FOLD>
+__global__ void __launch_bounds__(kThreads) k_tokens(const Args a) {
+    constexpr int R = DK / kGroups;
+    __shared__ alignas(16) float s_k[kTile][DK]; __shared__ alignas(16) float s_q[FOLD ? 1 : kTile][FOLD ? 4 : DK];
+    __shared__ float s_v[kTile][32];
+    __shared__ float s_w[kTile];  // g^e of each token, times the output's scale
+    __shared__ float s_o[FOLD ? 1 : kTile][kGroups][32];
+    __shared__ int64_t s_count;
+    const int col = threadIdx.x % 32, grp = threadIdx.x / 32;
+    const int64_t w = blockIdx.x;
+    const int h = blockIdx.y;
+    const int c0 = blockIdx.z * 32;
+    const bool live = c0 + col < a.dv;
+    const int64_t t0 = w * a.window, t1 = w == a.windows - 1 ? a.tokens : t0 + a.window;
+    const float ld = a.log_decay[h];
+    int block = kTile;
+    while (block > 1 && !(fabsf(ld) * block <= 40.0f)) block /= 2;
+    const Factor whole = decay_factor(ld, block);
+    const T* q = static_cast<const T*>(a.q) + h * a.q_head;
+    const T* k = static_cast<const T*>(a.k) + h * a.k_head;
+    const T* v = static_cast<const T*>(a.v) + h * a.v_head;
+    T* o = static_cast<T*>(a.o) + h * a.o_head;
+    const int64_t ssize = (int64_t)a.dk * a.dv;
+    float s[R];
+
+    auto addr = [&](int64_t t) { return a.reverse ? a.tokens - 1 - t : t; };
+    // tokens of no sequence get zeros
+    auto blank = [&](int64_t from, int64_t to) {
+        if (FOLD) return;
+        for (int64_t t = from + grp; t < to; t += kGroups)
+            if (live) o[addr(t) * a.o_tok + c0 + col] = from_f<T>(0.0f);
+    };
+    auto load_state = [&](const float* src, bool transposed) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = grp * R + i;
+            s[i] = 0.0f;
+            if (src && live && r < a.dk)
+                s[i] = transposed ? src[(int64_t)(c0 + col) * a.dk + r] : src[(int64_t)r * a.dv + c0 + col];
+        }
+    };
+    auto store_state = [&](float* dst) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = grp * R + i;
+            if (live && r < a.dk) dst[(int64_t)r * a.dv + c0 + col] = s[i];
+        }
+    };
+    auto seq_state = [&](int64_t n) {
+        const int64_t m = a.reverse ? a.seqs - 1 - n : n;
+        return (m * a.heads + h) * ssize;
+    };
+    // tokens [from, to) of one sequence
+    auto walk = [&](int64_t from, int64_t to) {
+        if (!a.reverse) {
+            const Factor one = decay_factor(ld, 1);
+#pragma unroll
+            for (int i = 0; i < R; ++i) s[i] = s[i] * one;
+        }
+        for (int64_t tb = from; tb < to; tb += kTile) {
+            const int m = (int)(to - tb < kTile ? to - tb : kTile);
+            __syncthreads();
+            for (int i = threadIdx.x; i < kTile * DK; i += kThreads) {
+                const int t = i / DK, r = i % DK;
+                const bool in = t < m && r < a.dk;
+                s_k[t][r] = in ? as_f(k[addr(tb + t) * a.k_tok + r]) : 0.0f;
+                if (!FOLD) s_q[t][r] = in ? as_f(q[addr(tb + t) * a.q_tok + r]) : 0.0f;
+            }
+            for (int i = threadIdx.x; i < kTile * 32; i += kThreads) {
+                const int t = i / 32, c = i % 32;
+                s_v[t][c] = t < m && c0 + c < a.dv
+                                ? as_f(v[addr(tb + t) * a.v_tok + c0 + c]) * (a.in_scale * decay_pow(ld, -(t & (block - 1))))
+                                : 0.0f;
+            }
+            if (threadIdx.x < kTile) s_w[threadIdx.x] = decay_pow(ld, threadIdx.x & (block - 1)) * a.out_scale;
+            __syncthreads();
+            for (int t = 0; t < m; ++t) {
+                const float vv = s_v[t][col];
+                float acc = 0.0f;
+#pragma unroll
+                for (int i = 0; i < R; i += 4) {
+                    const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][grp * R + i]);
+                    s[i] = fmaf(kk.x, vv, s[i]), s[i + 1] = fmaf(kk.y, vv, s[i + 1]);
+                    s[i + 2] = fmaf(kk.z, vv, s[i + 2]), s[i + 3] = fmaf(kk.w, vv, s[i + 3]);
+                    if (!FOLD) {
+                        const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][grp * R + i]);
+                        acc = fmaf(qq.x, s[i], acc), acc = fmaf(qq.y, s[i + 1], acc);
+                        acc = fmaf(qq.z, s[i + 2], acc), acc = fmaf(qq.w, s[i + 3], acc);
+                    }
+                }
+                if (!FOLD) s_o[t][grp][col] = acc;
+                const int e = t & (block - 1);
+                const bool last = tb + t == to - 1;
+                if (last || e == block - 1) {
+                    // after the last token a forward state is S, not g S
+                    const int power = last && !a.reverse ? e : e + 1;
+                    const Factor f = power == block ? whole : Factor{decay_pow(ld, power), 0.0f};
+#pragma unroll
+                    for (int i = 0; i < R; ++i) s[i] = s[i] * f;
+                }
+            }
+            if (!FOLD) {
+                __syncthreads();
+                for (int t = grp; t < m; t += kGroups) {
+                    const float x = (s_o[t][0][col] + s_o[t][1][col]) + (s_o[t][2][col] + s_o[t][3][col]);
+                    if (live) o[addr(tb + t) * a.o_tok + c0 + col] = from_f<T>(x * s_w[t]);
+                }
+            }
+        }
+    };
+
+    int64_t n = first_sequence<kThreads>(a, t0, &s_count);
+    if (FOLD) {
+        // the sequence that crosses the window's end
+        while (n < a.seqs && offset_at(a, n + 1) <= t1) ++n;
+        const int64_t begin = n < a.seqs ? offset_at(a, n) : t1;
+        const int32_t kind = begin >= t1 ? kNone : (begin >= t0 ? kFresh : kThrough);
+        if (threadIdx.x == 0 && h == 0 && blockIdx.z == 0) a.tail[w] = kind;
+        if (kind == kNone) return;
+        load_state(kind == kFresh && a.s_in ? a.s_in + seq_state(n) : nullptr, a.s_in_t);
+        walk(begin > t0 ? begin : t0, t1);
+        store_state(a.carry + (w * a.heads + h) * ssize);
+        return;
+    }
+    int64_t at = t0;
+    for (; n < a.seqs; ++n) {
+        const int64_t begin = offset_at(a, n), end = offset_at(a, n + 1);
+        if (begin >= t1 && w != a.windows - 1) break;
+        if (begin > at) blank(at, begin < t1 ? begin : t1);
+        const bool before = begin < t0;
+        const int64_t from = before ? t0 : begin, to = end < t1 ? end : t1;
+        if (before) load_state(a.carry + (w * a.heads + h) * ssize, false);
+        else load_state(a.s_in ? a.s_in + seq_state(n) : nullptr, a.s_in_t);
+        if (from < to) walk(from, to);
+        if (end <= t1 && a.s_out) store_state(a.s_out + seq_state(n));
+        if (to > at) at = to;
+        if (end > t1) break;
+    }
+    if (at < t1) blank(at, t1);
+}
+
+// ---------------------------------------------------------------------------
+// join of the windows' states
+// ---------------------------------------------------------------------------
+// carry[w] holds window w's last piece folded from its own start (or zero);
+// on return it holds the state before window w. One thread takes E values of
+// the state and walks the windows; kAhead loads are in flight before the
+// chain needs them.
+constexpr int kAhead = 8;
+
+template <int E>
+__global__ void __launch_bounds__(128) k_join(const Args a, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t per_head = (int64_t)a.dk * a.dv / E;
+    const Factor g = decay_factor(a.log_decay[i / per_head], (int)a.window);
+    Raw<4 * E>* c = reinterpret_cast<Raw<4 * E>*>(a.carry) + i;
+    Raw<4 * E> run = {};
+    for (int64_t w0 = 0; w0 < a.windows; w0 += kAhead) {
+        Raw<4 * E> u[kAhead];
+        int32_t kind[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            kind[j] = w0 + j < a.windows ? a.tail[w0 + j] : (int32_t)kNone;
+            if (kind[j] != kNone) u[j] = c[(w0 + j) * n];
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (w0 + j < a.windows) c[(w0 + j) * n] = run;
+            if (kind[j] == kFresh) run = u[j];
+            if (kind[j] == kThrough)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    run.w[e] = __float_as_uint(__uint_as_float(run.w[e]) * g + __uint_as_float(u[j].w[e]));
+        }
+    }
+}
+
+ak_status launch_join(const Args& a, cudaStream_t stream) {
+    const int64_t n = (int64_t)a.heads * a.dk * a.dv;
+    if ((int64_t)a.dk * a.dv % 4 == 0) k_join<4><<<(unsigned)((n / 4 + 127) / 128), 128, 0, stream>>>(a, n / 4);
+    else k_join<1><<<(unsigned)((n + 127) / 128), 128, 0, stream>>>(a, n);
+    count_launches(1);
+    return check_launch();
+}
+
+template <class T, int DK>
+ak_status launch_tokens(const Args& a, cudaStream_t stream) {
+    const dim3 grid((unsigned)a.windows, (unsigned)a.heads, (unsigned)((a.dv + 31) / 32));
+    if (a.windows > 1) {
+        k_tokens<T, DK, true><<<grid, kThreads, 0, stream>>>(a);
+        count_launches(1);
+        ak_status s = check_launch();
+        if (s == AK_OK) s = launch_join(a, stream);
+        if (s != AK_OK) return s;
+    }
+    k_tokens<T, DK, false><<<grid, kThreads, 0, stream>>>(a);
+    count_launches(1);
+    return check_launch();
+}
+
+template <class T>
+ak_status launch_tokens_of(const Args& a, cudaStream_t stream) {
+    if (a.dk <= 32) return launch_tokens<T, 32>(a, stream);
+    if (a.dk <= 64) return launch_tokens<T, 64>(a, stream);
+    if (a.dk <= 128) return launch_tokens<T, 128>(a, stream);
+    return launch_tokens<T, 256>(a, stream);
+}
+
+// ---------------------------------------------------------------------------
+// one token
+// ---------------------------------------------------------------------------
+// S = g S + k v^T; o = scale S^T q, the state updated in place: it is read
+// and written once, which is all the traffic that counts. A block takes a
+// request, a head and `cols` columns; a warp's lanes take four columns each
+// of kRows rows in flight, and the rows' parts of o meet in shared memory.
+constexpr int kStepThreads = 256;
+constexpr int kStepRows = 8;  // rows a thread has in flight
+
+struct StepArgs {
+    const void *q, *k, *v;
+    int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, o_tok, o_head;
+    void* o;
+    const float* log_decay;
+    float* state;
+    const int32_t* slots;
+    int64_t nslots;
+    int heads, dk, dv, cols;
+    float scale;
+};
+
+// VEC: dv is a multiple of 4 and the state 16-byte aligned.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kStepThreads) k_step(const StepArgs a) {
+    constexpr int E = VEC ? 4 : 1;
+    extern __shared__ float s_part[];  // [groups][cols], then k[dk], q[dk]
+    const int64_t b = blockIdx.x;
+    const int h = blockIdx.y;
+    const int c0 = blockIdx.z * a.cols;
+    const int cols = min(a.cols, a.dv - c0);
+    const int lanes = a.cols / E;              // threads across the columns
+    const int groups = kStepThreads / lanes;   // rows side by side
+    float* s_k = s_part + groups * a.cols;
+    float* s_q = s_k + a.dk;
+    const int64_t slot = a.slots ? (int64_t)a.slots[b] : b;
+    const int x = threadIdx.x % lanes, g = threadIdx.x / lanes;
+    T* o = static_cast<T*>(a.o) + b * a.o_tok + h * a.o_head + c0;
+    if (slot < 0 || slot >= a.nslots) {  // a padding entry
+        for (int i = threadIdx.x; i < cols; i += kStepThreads) o[i] = from_f<T>(0.0f);
+        return;
+    }
+    const bool live = g < groups && x * E < cols;
+    float* s = a.state + (slot * a.heads + h) * ((int64_t)a.dk * a.dv) + c0 + x * E;
+    const Factor w = decay_factor(a.log_decay[h], 1);
+    float st[kStepRows][E];
+    // the first rows are in flight while k, q and v arrive
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kStepRows; ++i) {
+            const int r = r0 + i * groups;
+            if (live && r < a.dk) {
+                if constexpr (VEC) *reinterpret_cast<float4*>(st[i]) = *reinterpret_cast<const float4*>(s + (int64_t)r * a.dv);
+                else st[i][0] = s[(int64_t)r * a.dv];
+            }
+        }
+    };
+    load(g);
+    const T* q = static_cast<const T*>(a.q) + b * a.q_tok + h * a.q_head;
+    const T* k = static_cast<const T*>(a.k) + b * a.k_tok + h * a.k_head;
+    const T* v = static_cast<const T*>(a.v) + b * a.v_tok + h * a.v_head + c0;
+    for (int i = threadIdx.x; i < a.dk; i += kStepThreads) {
+        s_k[i] = as_f(k[i]);
+        s_q[i] = as_f(q[i]);
+    }
+    float vv[E], acc[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        vv[j] = live ? as_f(v[x * E + j]) : 0.0f;
+        acc[j] = 0.0f;
+    }
+    __syncthreads();
+    for (int r0 = g; r0 < a.dk; r0 += groups * kStepRows) {
+        if (r0 != g) load(r0);
+#pragma unroll
+        for (int i = 0; i < kStepRows; ++i) {
+            const int r = r0 + i * groups;
+            if (live && r < a.dk) {
+                const float kk = s_k[r], qq = s_q[r];
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    st[i][j] = fmaf(st[i][j], w.hi, fmaf(st[i][j], w.lo, kk * vv[j]));
+                    acc[j] = fmaf(qq, st[i][j], acc[j]);
+                }
+                if constexpr (VEC) *reinterpret_cast<float4*>(s + (int64_t)r * a.dv) = *reinterpret_cast<const float4*>(st[i]);
+                else s[(int64_t)r * a.dv] = st[i][0];
+            }
+        }
+    }
+    if (g < groups) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) s_part[g * a.cols + x * E + j] = acc[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < cols; i += kStepThreads) {
+        float r = 0.0f;
+        for (int j = 0; j < groups; ++j) r += s_part[j * a.cols + i];
+        o[i] = from_f<T>(r * a.scale);
+    }
+}
+
+template <class T>
+ak_status launch_step(const StepArgs& a, int64_t batch, bool vec, cudaStream_t stream) {
+    const int lanes = a.cols / (vec ? 4 : 1);
+    const size_t smem = ((size_t)(kStepThreads / lanes) * a.cols + 2 * (size_t)a.dk) * 4;
+    const dim3 grid((unsigned)batch, (unsigned)a.heads, (unsigned)((a.dv + a.cols - 1) / a.cols));
+    if (vec) k_step<T, true><<<grid, kStepThreads, smem, stream>>>(a);
+    else k_step<T, false><<<grid, kStepThreads, smem, stream>>>(a);
+    count_launches(1);
+    return check_launch();
+}
+
+}  // namespace la
+
+// Windows of the packed axis. One window needs neither the fold pass nor the
+// join; more of them fill the device where heads alone do not.
+static int64_t plan_windows(const LinattnCall& c, const DeviceInfo& dev, int64_t* window) {
+    const int64_t unit = 64;
+    int64_t want = c.windows > 0 ? c.windows : (4 * dev.sm_count + c.heads - 1) / c.heads;
+    const int64_t units = std::max<int64_t>(1, (c.tokens + unit - 1) / unit);
+    want = std::max<int64_t>(1, std::min(want, units));
+    const int64_t per = (units + want - 1) / want;
+    *window = per * unit;
+    return std::max<int64_t>(1, (c.tokens + *window - 1) / *window);
+}
+
+size_t linattn_workspace(const LinattnCall& c, const DeviceInfo& dev) {
+    int64_t window;
+    const int64_t w = plan_windows(c, dev, &window);
+    if (w == 1) return kWsHeader;
+    const size_t state = (size_t)c.heads * c.dk * c.dv * 4;
+    return kWsHeader + align_up((size_t)w * 4, 256) + align_up((size_t)w * state, 256);
+}
+
+static la::Args args_of(const LinattnCall& c, const DeviceInfo& dev, void* ws) {
+    la::Args a = {};
+    a.log_decay = c.log_decay;
+    a.offsets = c.offsets;
+    a.tokens = c.tokens;
+    a.seqs = c.seqs;
+    a.heads = c.heads;
+    a.windows = plan_windows(c, dev, &a.window);
+    char* w = static_cast<char*>(ws) + kWsHeader;
+    a.tail = reinterpret_cast<int32_t*>(w);
+    a.carry = reinterpret_cast<float*>(w + align_up((size_t)a.windows * 4, 256));
+    return a;
+}
+
+static void roles(la::Args& a, const ak_heads& q, const ak_heads& k, const ak_heads& v, const ak_heads& o, int dk, int dv) {
+    a.q = q.data, a.q_tok = q.token_stride, a.q_head = q.head_stride;
+    a.k = k.data, a.k_tok = k.token_stride, a.k_head = k.head_stride;
+    a.v = v.data, a.v_tok = v.token_stride, a.v_head = v.head_stride;
+    a.o = o.data, a.o_tok = o.token_stride, a.o_head = o.head_stride;
+    a.dk = dk, a.dv = dv;
+}
+
+static ak_status run_one(const la::Args& a, ak_dtype dtype, cudaStream_t s) {
+    return dtype == AK_F32 ? la::launch_tokens_of<float>(a, s) : la::launch_tokens_of<bf16>(a, s);
+}
+
+ak_status run_linattn(const LinattnCall& c, void* ws, cudaStream_t stream) {
+    DeviceInfo dev;
+    if (!current_device(&dev)) return AK_ERR_CUDA;
+    la::Args a = args_of(c, dev, ws);
+    roles(a, c.q, c.k, c.v, c.o, c.dk, c.dv);
+    a.s_in = c.state_in, a.s_out = c.state_out;
+    a.out_scale = c.scale, a.in_scale = 1.0f;
+    return run_one(a, c.dtype, stream);
+}
+
+ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stream) {
+    DeviceInfo dev;
+    if (!current_device(&dev)) return AK_ERR_CUDA;
+    la::Args a = args_of(c, dev, ws);
+    // dq = F(do, v, k) from the transposed initial state
+    roles(a, c.o, c.v, c.k, c.dq, c.dv, c.dk);
+    a.s_in = c.state_in, a.s_in_t = true, a.s_out = nullptr;
+    a.out_scale = c.scale, a.in_scale = 1.0f;
+    ak_status s = run_one(a, c.dtype, stream);
+    if (s != AK_OK) return s;
+    a.reverse = true, a.out_scale = 1.0f, a.in_scale = c.scale;
+    // dv = R(k, q, do) from dS_T, leaving dS_0
+    roles(a, c.k, c.q, c.o, c.dvv, c.dk, c.dv);
+    a.s_in = c.dstate_out, a.s_in_t = false, a.s_out = c.dstate_in;
+    if ((s = run_one(a, c.dtype, stream)) != AK_OK) return s;
+    // dk = R(v, do, q) from dS_T transposed
+    roles(a, c.v, c.o, c.q, c.dk_out, c.dv, c.dk);
+    a.s_in_t = true, a.s_out = nullptr;
+    return run_one(a, c.dtype, stream);
+}
+
+ak_status run_linattn_step(const LinattnCall& c, float* state, const int32_t* slots, int64_t nslots,
+                           cudaStream_t stream) {
+    DeviceInfo dev;
+    if (!current_device(&dev)) return AK_ERR_CUDA;
+    la::StepArgs a = {};
+    a.q = c.q.data, a.q_tok = c.q.token_stride, a.q_head = c.q.head_stride;
+    a.k = c.k.data, a.k_tok = c.k.token_stride, a.k_head = c.k.head_stride;
+    a.v = c.v.data, a.v_tok = c.v.token_stride, a.v_head = c.v.head_stride;
+    a.o = c.o.data, a.o_tok = c.o.token_stride, a.o_head = c.o.head_stride;
+    a.log_decay = c.log_decay;
+    a.state = state, a.slots = slots, a.nslots = nslots;
+    a.heads = c.heads, a.dk = c.dk, a.dv = c.dv, a.scale = c.scale;
+    const bool vec = c.dv % 4 == 0 && reinterpret_cast<uintptr_t>(state) % 16 == 0;
+    a.cols = 32;
+    while (a.cols < c.dv && a.cols < 256) a.cols *= 2;
+    // fewer blocks than SMs: narrower column slices (128 bytes a row at least)
+    while (a.cols > 32 && c.tokens * c.heads * ((c.dv + a.cols - 1) / a.cols) < 2 * dev.sm_count) a.cols /= 2;
+    return c.dtype == AK_F32 ? la::launch_step<float>(a, c.tokens, vec, stream)
+                             : la::launch_step<bf16>(a, c.tokens, vec, stream);
+}
+
+}  // namespace ak

@@ -1,0 +1,321 @@
+"""The sequence operators over torch tensors: the layout of a batch from its
+request lengths, the verification of drafted tokens, and linear attention
+with a decay for each head (packed prompts, gradients, single tokens).
+
+Like the rest of the binding these functions only marshal arguments; include/ak.h
+states the mathematics and the rules of every argument. Tensors here are
+plain row-major: ``[tokens, heads, dim]`` (any token and head stride, the last
+dimension contiguous) and states ``[sequences, heads, dk, dv]``.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import _abi
+from ._abi import DTYPES, ak_heads, ak_linattn
+
+_FLOAT = {torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"]}
+
+
+class BatchLayout(NamedTuple):
+    """What ak_batch_layout fills in; ``counts`` holds the batch's tokens and the free blocks it takes."""
+    offsets: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    requests: torch.Tensor
+    counts: torch.Tensor
+
+
+def _stream_of(stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _keep(stream, *tensors):
+    """Memory allocated here for a call on another stream than the current one is not handed out again before
+    that stream is done with it."""
+    if stream is None:
+        return
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def _opts(opts):
+    if opts is None:
+        return None
+    from . import make_opts
+    return ctypes.byref(make_opts(**opts) if isinstance(opts, dict) else opts)
+
+
+def _check(status: int, where: str) -> None:
+    if status != _abi.AK_OK:
+        from . import AkError
+        raise AkError(status, where)
+
+
+def _need(cond, message):
+    if not cond:
+        raise ValueError(message)
+
+
+def _flat(t, dtype, numel, name):
+    """Pointer of a contiguous CUDA tensor of `numel` elements of `dtype`."""
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() == numel):
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {numel} {dtype} values is needed, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _dense_rows(t):
+    """Whether the last dimension is contiguous (strides of empty and one-element dimensions mean nothing)."""
+    return t.stride(-1) == 1 or t.shape[-1] <= 1 or t.numel() == 0
+
+
+def _workspace_ptr(nbytes, device, workspace, stream):
+    if workspace is not None:
+        size = workspace.numel() * workspace.element_size()
+        _need(size >= nbytes, "workspace too small")
+        return workspace.data_ptr(), size
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _keep(stream, ws)
+    return ws.data_ptr(), nbytes
+
+
+# ---------------------------------------------------------------------------
+# ak_batch_layout
+# ---------------------------------------------------------------------------
+
+def ak_batch_layout_workspace_size(nreq: int, opts=None) -> int:
+    b = ctypes.c_size_t()
+    _check(_abi.load().ak_batch_layout_workspace_size(int(nreq), _opts(opts), ctypes.byref(b)),
+           "ak_batch_layout_workspace_size")
+    return b.value
+
+
+def ak_batch_layout(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                    free_blocks: torch.Tensor, *, block_size: int, max_tokens: int, offsets=None, slots=None,
+                    positions=None, requests=None, counts=None, workspace=None, opts=None,
+                    stream=None) -> BatchLayout:
+    """Packed offsets, slot map, positions and request ids of a batch from its
+    requests' int32 lengths (``ctx_lens`` cached, ``new_lens`` to run), and the
+    new entries of ``block_table`` ([requests, width] int32, in place) taken in
+    order from ``free_blocks``. Token arrays hold ``max_tokens`` entries, -1 / 0
+    / -1 past the batch's end."""
+    n = ctx_lens.numel()
+    dev = ctx_lens.device
+    _need(block_table.is_cuda and block_table.dtype == torch.int32 and block_table.dim() == 2 and
+          block_table.shape[0] == n and _dense_rows(block_table),
+          "block_table: a [requests, width] int32 CUDA tensor with contiguous rows is needed")
+    if offsets is None:
+        offsets = torch.empty(n + 1, dtype=torch.int32, device=dev)
+        _keep(stream, offsets)
+    if slots is None:
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        _keep(stream, slots)
+    if positions is None:
+        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        _keep(stream, positions)
+    if requests is None:
+        requests = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        _keep(stream, requests)
+    if counts is None:
+        counts = torch.empty(2, dtype=torch.int32, device=dev)
+        _keep(stream, counts)
+    L = _abi.load()
+    size = ak_batch_layout_workspace_size(n) if n > 4096 else 0
+    wp, wb = _workspace_ptr(size, dev, workspace, stream) if size or workspace is not None else (None, 0)
+    _check(L.ak_batch_layout(
+        _flat(ctx_lens, torch.int32, n, "ctx_lens"), _flat(new_lens, torch.int32, n, "new_lens"), n,
+        block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
+        _flat(free_blocks, torch.int32, free_blocks.numel(), "free_blocks"), free_blocks.numel(), int(block_size),
+        int(max_tokens), _flat(offsets, torch.int32, n + 1, "offsets"), _flat(slots, torch.int64, max_tokens, "slots"),
+        _flat(positions, torch.int32, max_tokens, "positions"), _flat(requests, torch.int32, max_tokens, "requests"),
+        _flat(counts, torch.int32, 2, "counts"), wp, wb, _opts(opts), _stream_of(stream)), "ak_batch_layout")
+    return BatchLayout(offsets, slots, positions, requests, counts)
+
+
+# ---------------------------------------------------------------------------
+# ak_verify_drafts
+# ---------------------------------------------------------------------------
+
+def ak_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform: torch.Tensor,
+                     noise: torch.Tensor, *, draft_probs: torch.Tensor | None = None,
+                     draft_counts: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                     accepted: torch.Tensor | None = None, opts=None, stream=None):
+    """Verify ``draft_tokens`` [requests, k] int32 against ``target_probs``
+    [requests, k + 1, vocab] (float32 or bfloat16) with ``uniform`` [requests, k]
+    and exponential ``noise`` [requests, vocab]; ``draft_probs`` [requests, k,
+    vocab] or None where each draft was certain. Returns ``(tokens, accepted)``:
+    [requests, k + 1] int32, the kept drafts, then the token after them, then -1;
+    and how many drafts were kept."""
+    n, k = draft_tokens.shape
+    vocab = target_probs.shape[-1]
+    dev = target_probs.device
+    dt = target_probs.dtype
+    _need(dt in _FLOAT, "probabilities are float32 or bfloat16")
+    _need(target_probs.is_cuda and target_probs.shape == (n, k + 1, vocab) and _dense_rows(target_probs),
+          "target_probs: a [requests, k + 1, vocab] CUDA tensor with contiguous rows is needed")
+    _need(noise.is_cuda and noise.dtype == torch.float32 and noise.shape == (n, vocab) and _dense_rows(noise),
+          "noise: a [requests, vocab] float32 CUDA tensor with contiguous rows is needed")
+    q, qs = None, (0, 0)
+    if draft_probs is not None:
+        _need(draft_probs.is_cuda and draft_probs.dtype == dt and draft_probs.shape == (n, k, vocab) and
+              _dense_rows(draft_probs),
+              "draft_probs: a [requests, k, vocab] CUDA tensor of the target's type with contiguous rows is needed")
+        q, qs = (draft_probs.data_ptr() if k else None), draft_probs.stride()
+    if tokens is None:
+        tokens = torch.empty(n, k + 1, dtype=torch.int32, device=dev)
+        _keep(stream, tokens)
+    if accepted is None:
+        accepted = torch.empty(n, dtype=torch.int32, device=dev)
+        _keep(stream, accepted)
+    ps = target_probs.stride()
+    _check(_abi.load().ak_verify_drafts(
+        target_probs.data_ptr(), ps[0], ps[1], q, qs[0], qs[1], _FLOAT[dt],
+        _flat(draft_tokens, torch.int32, n * k, "draft_tokens"),
+        None if draft_counts is None else _flat(draft_counts, torch.int32, n, "draft_counts"),
+        _flat(uniform, torch.float32, n * k, "uniform"), noise.data_ptr(), noise.stride(0), n, k, vocab,
+        _flat(tokens, torch.int32, n * (k + 1), "tokens"), _flat(accepted, torch.int32, n, "accepted"), _opts(opts),
+        _stream_of(stream)), "ak_verify_drafts")
+    return tokens, accepted
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay for each head
+# ---------------------------------------------------------------------------
+
+def _heads(t: torch.Tensor, shape, dtype, name) -> ak_heads:
+    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and (t.stride(2) == 1 or shape[2] == 1)):
+        raise ValueError(f"{name}: a {list(shape)} {dtype} CUDA tensor with a contiguous last dimension is needed, "
+                         f"got {list(t.shape)} {t.dtype} with strides {list(t.stride())} on {t.device}")
+    s = t.stride()
+    return ak_heads(t.data_ptr(), s[0], s[1])
+
+
+def _state_ptr(t, shape, name):
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype == torch.float32 and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {list(shape)} float32 CUDA tensor is needed, got {list(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def _geometry(q, k, v, log_decay, offsets, scale, max_len):
+    _need(q.dim() == 3 and v.dim() == 3, "q, k and v are [tokens, heads, dim] tensors")
+    t, h, dk = q.shape
+    dv = v.shape[2]
+    dt = q.dtype
+    _need(dt in _FLOAT, "q, k and v are float32 or bfloat16")
+    n = 1 if offsets is None else offsets.numel() - 1
+    _need(n >= 0, "offsets: at least one value is needed")
+    a = ak_linattn(t, n, int(max_len or 0), h, dk, dv, _FLOAT[dt], scale, 0)
+    ld = _flat(log_decay, torch.float32, h, "log_decay")
+    off = None if offsets is None else _flat(offsets, torch.int32, n + 1, "offsets")
+    return a, (t, h, dk), (t, h, dv), (n, h, dk, dv), dt, ld, off
+
+
+def ak_linear_attention_workspace_size(tokens: int, heads: int, dk: int, dv: int, *, seqs: int = 1, max_len=None,
+                                       dtype: str = "bf16", opts=None) -> int:
+    b = ctypes.c_size_t()
+    a = ak_linattn(tokens, seqs, int(max_len or 0), heads, dk, dv, DTYPES[dtype], 1.0, 0)
+    _check(_abi.load().ak_linear_attention_workspace_size(ctypes.byref(a), _opts(opts), ctypes.byref(b)),
+           "ak_linear_attention_workspace_size")
+    return b.value
+
+
+def _workspace(a, device, workspace, opts, stream):
+    b = ctypes.c_size_t()
+    _check(_abi.load().ak_linear_attention_workspace_size(ctypes.byref(a), opts, ctypes.byref(b)),
+           "ak_linear_attention_workspace_size")
+    return _workspace_ptr(b.value, device, workspace, stream)
+
+
+def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
+                        offsets: torch.Tensor | None = None, state: torch.Tensor | None = None, scale: float = 1.0,
+                        max_len: int | None = None, out: torch.Tensor | None = None,
+                        state_out: torch.Tensor | None = None, final_state: bool = False, workspace=None, opts=None,
+                        stream=None):
+    """``S_t = exp(log_decay) S_{t-1} + k_t v_t^T``, ``o_t = scale S_t^T q_t`` for
+    every head over packed sequences (``offsets`` int32, None: one sequence),
+    from ``state`` [sequences, heads, dk, dv] float32 or zero. Returns ``(out,
+    state_out)``, the latter None unless given or asked for by ``final_state``."""
+    a, sk, sv, ss, dt, ld, off = _geometry(q, k, v, log_decay, offsets, scale, max_len)
+    if out is None:
+        out = torch.empty(sv, dtype=dt, device=q.device)
+        _keep(stream, out)
+    if state_out is None and final_state:
+        state_out = torch.empty(ss, dtype=torch.float32, device=q.device)
+        _keep(stream, state_out)
+    op = _opts(opts)
+    hq, hk, hv, ho = _heads(q, sk, dt, "q"), _heads(k, sk, dt, "k"), _heads(v, sv, dt, "v"), _heads(out, sv, dt, "out")
+    s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(state_out, ss, "state_out")
+    wp, wb = _workspace(a, q.device, workspace, op, stream)
+    _check(_abi.load().ak_linear_attention(ctypes.byref(a), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), ld,
+                                           off, s0, ctypes.byref(ho), s1, wp, wb, op, _stream_of(stream)),
+           "ak_linear_attention")
+    return out, state_out
+
+
+def ak_linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                 log_decay: torch.Tensor, *, offsets: torch.Tensor | None = None,
+                                 state: torch.Tensor | None = None, dstate_out: torch.Tensor | None = None,
+                                 scale: float = 1.0, max_len: int | None = None, dq: torch.Tensor | None = None,
+                                 dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                                 dstate: torch.Tensor | None = None, workspace=None, opts=None, stream=None):
+    """Gradients of ak_linear_attention with respect to q, k, v and the initial
+    state, from the output's gradient ``do`` and the final state's
+    ``dstate_out`` (or None). Returns ``(dq, dk, dv, dstate)``; ``dstate`` is
+    None where the forward call had no ``state`` and none is given."""
+    a, sk, sv, ss, dt, ld, off = _geometry(q, k, v, log_decay, offsets, scale, max_len)
+    dev = q.device
+    if dq is None:
+        dq = torch.empty(sk, dtype=dt, device=dev)
+        _keep(stream, dq)
+    if dk is None:
+        dk = torch.empty(sk, dtype=dt, device=dev)
+        _keep(stream, dk)
+    if dv is None:
+        dv = torch.empty(sv, dtype=dt, device=dev)
+        _keep(stream, dv)
+    if dstate is None and state is not None:
+        dstate = torch.empty(ss, dtype=torch.float32, device=dev)
+        _keep(stream, dstate)
+    op = _opts(opts)
+    hs = [_heads(x, s, dt, n) for x, s, n in ((do, sv, "do"), (q, sk, "q"), (k, sk, "k"), (v, sv, "v"),
+                                              (dq, sk, "dq"), (dk, sk, "dk"), (dv, sv, "dv"))]
+    hdo, hq, hk, hv, hdq, hdk, hdv = [ctypes.byref(x) for x in hs]
+    s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(dstate_out, ss, "dstate_out")
+    s2 = _state_ptr(dstate, ss, "dstate")
+    wp, wb = _workspace(a, dev, workspace, op, stream)
+    _check(_abi.load().ak_linear_attention_backward(ctypes.byref(a), hdo, hq, hk, hv, ld, off, s0, s1, hdq, hdk, hdv,
+                                                    s2, wp, wb, op, _stream_of(stream)),
+           "ak_linear_attention_backward")
+    return dq, dk, dv, dstate
+
+
+def ak_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                             state: torch.Tensor, *, slots: torch.Tensor | None = None, scale: float = 1.0,
+                             out: torch.Tensor | None = None, opts=None, stream=None) -> torch.Tensor:
+    """One token of each of ``q.shape[0]`` requests: updates the matrices
+    ``state[slots]`` ([slots, heads, dk, dv] float32; ``slots`` int32, None: request
+    b uses state[b]) in place and returns the outputs. Slots outside the pool
+    mark padding and give zeros."""
+    a, sk, sv, ss, dt, ld, _ = _geometry(q, k, v, log_decay, None, scale, None)
+    if out is None:
+        out = torch.empty(sv, dtype=dt, device=q.device)
+        _keep(stream, out)
+    hq, hk, hv, ho = _heads(q, sk, dt, "q"), _heads(k, sk, dt, "k"), _heads(v, sv, dt, "v"), _heads(out, sv, dt, "out")
+    pool = state.shape[0]
+    sp = _state_ptr(state, (pool,) + ss[1:], "state")
+    at = None if slots is None else _flat(slots, torch.int32, sk[0], "slots")
+    _need(slots is not None or pool >= sk[0], "state: one matrix for each request and head is needed")
+    _check(_abi.load().ak_linear_attention_step(ctypes.byref(a), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
+                                                ld, sp, at, pool, ctypes.byref(ho), _opts(opts), _stream_of(stream)),
+           "ak_linear_attention_step")
+    return out
