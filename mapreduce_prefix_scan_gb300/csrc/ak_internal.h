@@ -345,7 +345,8 @@ struct LinattnCall {
     float* state_out;
     const float* dstate_out;  // gradient of the final state, or null
     float* dstate_in;         // gradient of the initial state, or null
-    cudaStream_t stream;
+    uint64_t epoch;           // written to the workspace's first word by a kernel that gave up waiting
+    int64_t wait_limit_ns;
 };
 size_t linattn_workspace(const LinattnCall& c, const DeviceInfo& dev);
 ak_status run_linattn(const LinattnCall& c, void* ws, cudaStream_t stream);

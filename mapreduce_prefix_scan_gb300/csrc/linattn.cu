@@ -402,8 +402,12 @@ static void roles(la::Args& a, const ak_heads& q, const ak_heads& k, const ak_he
     a.dk = dk, a.dv = dv;
 }
 
-static ak_status run_one(const la::Args& a, ak_dtype dtype, cudaStream_t s) {
-    return dtype == AK_F32 ? la::launch_tokens_of<float>(a, s) : la::launch_tokens_of<bf16>(a, s);
+static ak_status run_one(const la::Args& a, const LinattnCall& c, void* ws, cudaStream_t s) {
+    if (la::mma_takes(a, c.dtype)) {
+        const ak_status r = la::launch_chunks(a, static_cast<uint64_t*>(ws), c.epoch, (uint64_t)c.wait_limit_ns, s);
+        if (r != AK_ERR_UNSUPPORTED) return r;
+    }
+    return c.dtype == AK_F32 ? la::launch_tokens_of<float>(a, s) : la::launch_tokens_of<bf16>(a, s);
 }
 
 ak_status run_linattn(const LinattnCall& c, void* ws, cudaStream_t stream) {
@@ -413,7 +417,7 @@ ak_status run_linattn(const LinattnCall& c, void* ws, cudaStream_t stream) {
     roles(a, c.q, c.k, c.v, c.o, c.dk, c.dv);
     a.s_in = c.state_in, a.s_out = c.state_out;
     a.out_scale = c.scale, a.in_scale = 1.0f;
-    return run_one(a, c.dtype, stream);
+    return run_one(a, c, ws, stream);
 }
 
 ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stream) {
@@ -424,17 +428,17 @@ ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stre
     roles(a, c.o, c.v, c.k, c.dq, c.dv, c.dk);
     a.s_in = c.state_in, a.s_in_t = true, a.s_out = nullptr;
     a.out_scale = c.scale, a.in_scale = 1.0f;
-    ak_status s = run_one(a, c.dtype, stream);
+    ak_status s = run_one(a, c, ws, stream);
     if (s != AK_OK) return s;
     a.reverse = true, a.out_scale = 1.0f, a.in_scale = c.scale;
     // dv = R(k, q, do) from dS_T, leaving dS_0
     roles(a, c.k, c.q, c.o, c.dvv, c.dk, c.dv);
     a.s_in = c.dstate_out, a.s_in_t = false, a.s_out = c.dstate_in;
-    if ((s = run_one(a, c.dtype, stream)) != AK_OK) return s;
+    if ((s = run_one(a, c, ws, stream)) != AK_OK) return s;
     // dk = R(v, do, q) from dS_T transposed
     roles(a, c.v, c.o, c.q, c.dk_out, c.dv, c.dk);
     a.s_in_t = true, a.s_out = nullptr;
-    return run_one(a, c.dtype, stream);
+    return run_one(a, c, ws, stream);
 }
 
 ak_status run_linattn_step(const LinattnCall& c, float* state, const int32_t* slots, int64_t nslots,

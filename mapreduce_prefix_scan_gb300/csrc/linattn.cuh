@@ -101,5 +101,12 @@ __device__ __forceinline__ int64_t first_sequence(const Args& a, int64_t t0, int
     return *s_count;
 }
 
+// linattn.cu
+ak_status launch_join(const Args& a, cudaStream_t stream);
+// linattn_mma.cu
+bool mma_takes(const Args& a, ak_dtype dtype);
+ak_status launch_chunks(const Args& a, uint64_t* error_word, uint64_t epoch, uint64_t wait_limit_ns,
+                        cudaStream_t stream);
+
 }  // namespace la
 }  // namespace ak

@@ -131,6 +131,8 @@ static LinattnCall call_of(const ak_linattn* a, const ak_opts& o) {
     c.heads = a->heads, c.dk = a->dk, c.dv = a->dv;
     c.scale = a->scale;
     c.windows = o.target_blocks > 0 ? o.target_blocks : 0;
+    c.epoch = next_epoch();
+    c.wait_limit_ns = o.wait_limit_ns;
     return c;
 }
 
@@ -138,7 +140,17 @@ static ak_status check_workspace(const LinattnCall& c, const void* ws, size_t ws
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
     const size_t need = linattn_workspace(c, dev);
-    return need > kWsHeader && (!ws || ws_bytes < need || !aligned(ws, 16)) ? AK_ERR_WORKSPACE : AK_OK;
+    return !ws || ws_bytes < need || !aligned(ws, 16) ? AK_ERR_WORKSPACE : AK_OK;
+}
+
+// With opts->check: waits for the call and reports a wait that ran out.
+static ak_status finish_attention(ak_status s, const LinattnCall& c, const void* ws, const ak_opts* opts, void* stream) {
+    s = finish(s, opts, stream);
+    if (s != AK_OK || !resolve_opts(opts).check) return s;
+    uint64_t word = 0;
+    const cudaError_t e = cudaMemcpy(&word, ws, sizeof word, cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(e);
+    return word == c.epoch ? AK_ERR_TIMEOUT : AK_OK;
 }
 
 extern "C" ak_status ak_linear_attention_workspace_size(const ak_linattn* a, const ak_opts* opts, size_t* bytes) {
@@ -169,7 +181,7 @@ extern "C" ak_status ak_linear_attention(const ak_linattn* a, const ak_heads* q,
     c.q = *q, c.k = *k, c.v = *v, c.o = *o;
     c.log_decay = log_decay, c.offsets = offsets, c.state_in = state_in, c.state_out = state_out;
     if ((s = check_workspace(c, ws, ws_bytes)) != AK_OK) return s;
-    return finish(run_linattn(c, ws, static_cast<cudaStream_t>(stream)), opts, stream);
+    return finish_attention(run_linattn(c, ws, static_cast<cudaStream_t>(stream)), c, ws, opts, stream);
 }
 
 extern "C" ak_status ak_linear_attention_backward(const ak_linattn* a, const ak_heads* d_o, const ak_heads* q,
@@ -194,7 +206,7 @@ extern "C" ak_status ak_linear_attention_backward(const ak_linattn* a, const ak_
     c.log_decay = log_decay, c.offsets = offsets, c.state_in = state_in;
     c.dstate_out = dstate_out, c.dstate_in = dstate_in;
     if ((s = check_workspace(c, ws, ws_bytes)) != AK_OK) return s;
-    return finish(run_linattn_backward(c, ws, static_cast<cudaStream_t>(stream)), opts, stream);
+    return finish_attention(run_linattn_backward(c, ws, static_cast<cudaStream_t>(stream)), c, ws, opts, stream);
 }
 
 extern "C" ak_status ak_linear_attention_step(const ak_linattn* a, const ak_heads* q, const ak_heads* k,
