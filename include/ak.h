@@ -470,7 +470,7 @@ ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t
  * sum(state_out * dstate_out), from the forward call's inputs; dq, dk, dv as
  * q, k, v are described; dstate_in (may be NULL) receives the gradient of
  * state_in. log_decay and scale are constants of the model and get none.
- * dstate_in may be dstate_out.
+ * dstate_in is neither dstate_out nor state_in.
  *
  * ak_linear_attention_step: one token for each of `tokens` requests (seqs,
  * offsets and max_len unused), the state updated in place. Request b uses

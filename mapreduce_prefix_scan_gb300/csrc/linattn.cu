@@ -38,7 +38,7 @@ constexpr int kGroups = 4;
 constexpr int kThreads = 32 * kGroups;
 
 template <class T, int DK, bool FOLD>
-__global__ void __launch_bounds__(kThreads) k_tokens(const Args a) {
+__global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Batch batch) {
     constexpr int R = DK / kGroups;
     __shared__ alignas(16) float s_k[kTile][DK]; __shared__ alignas(16) float s_q[FOLD ? 1 : kTile][FOLD ? 4 : DK];
     __shared__ float s_v[kTile][32];
@@ -48,9 +48,12 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const Args a) {
     const int col = threadIdx.x % 32, grp = threadIdx.x / 32;
     const int64_t w = blockIdx.x;
     const int h = blockIdx.y;
-    const int c0 = blockIdx.z * 32;
+    const Args& a = batch.a[blockIdx.z % batch.count];
+    const int c0 = blockIdx.z / batch.count * 32;
+    if (c0 >= a.dv) return;  // the calls of a batch may differ in dv
     const bool live = c0 + col < a.dv;
-    const int64_t t0 = w * a.window, t1 = w == a.windows - 1 ? a.tokens : t0 + a.window;
+    int64_t t0, t1;
+    block_span(a, w, &t0, &t1);
     const float ld = a.log_decay[h];
     int block = kTile;
     while (block > 1 && !(fabsf(ld) * block <= 40.0f)) block /= 2;
@@ -154,9 +157,10 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const Args a) {
         while (n < a.seqs && offset_at(a, n + 1) <= t1) ++n;
         const int64_t begin = n < a.seqs ? offset_at(a, n) : t1;
         const int32_t kind = begin >= t1 ? kNone : (begin >= t0 ? kFresh : kThrough);
-        if (threadIdx.x == 0 && h == 0 && blockIdx.z == 0) a.tail[w] = kind;
+        if (threadIdx.x == 0 && h == 0 && c0 == 0) a.tail[w] = kind;
         if (kind == kNone) return;
         load_state(kind == kFresh && a.s_in ? a.s_in + seq_state(n) : nullptr, a.s_in_t);
+        if (a.stash && kind == kFresh) store_state(a.stash + (w * a.heads + h) * ssize);
         walk(begin > t0 ? begin : t0, t1);
         store_state(a.carry + (w * a.heads + h) * ssize);
         return;
@@ -164,11 +168,12 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const Args a) {
     int64_t at = t0;
     for (; n < a.seqs; ++n) {
         const int64_t begin = offset_at(a, n), end = offset_at(a, n + 1);
-        if (begin >= t1 && w != a.windows - 1) break;
+        if (a.by_seq ? n > w : begin >= t1 && w != a.windows - 1) break;
         if (begin > at) blank(at, begin < t1 ? begin : t1);
-        const bool before = begin < t0;
+        const bool before = begin < t0;  // never, by sequence
         const int64_t from = before ? t0 : begin, to = end < t1 ? end : t1;
         if (before) load_state(a.carry + (w * a.heads + h) * ssize, false);
+        else if (a.stash && end > t1) load_state(a.stash + (w * a.heads + h) * ssize, false);
         else load_state(a.s_in ? a.s_in + seq_state(n) : nullptr, a.s_in_t);
         if (from < to) walk(from, to);
         if (end <= t1 && a.s_out) store_state(a.s_out + seq_state(n));
@@ -188,13 +193,15 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const Args a) {
 constexpr int kAhead = 8;
 
 template <int E>
-__global__ void __launch_bounds__(128) k_join(const Args a, int64_t n) {
+__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Batch batch, int64_t n) {
+    const Args& a = batch.a[blockIdx.y];
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
     if (i >= n) return;
     const int64_t per_head = (int64_t)a.dk * a.dv / E;
     const Factor g = decay_factor(a.log_decay[i / per_head], (int)a.window);
     Raw<4 * E>* c = reinterpret_cast<Raw<4 * E>*>(a.carry) + i;
     Raw<4 * E> run = {};
+    int32_t before = kNone;  // tail of the window before: kNone, and nothing reads the window's state
     for (int64_t w0 = 0; w0 < a.windows; w0 += kAhead) {
         Raw<4 * E> u[kAhead];
         int32_t kind[kAhead];
@@ -205,7 +212,8 @@ __global__ void __launch_bounds__(128) k_join(const Args a, int64_t n) {
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (w0 + j < a.windows) c[(w0 + j) * n] = run;
+            if (before != kNone) c[(w0 + j) * n] = run;
+            before = kind[j];
             if (kind[j] == kFresh) run = u[j];
             if (kind[j] == kThrough)
 #pragma unroll
@@ -215,35 +223,41 @@ __global__ void __launch_bounds__(128) k_join(const Args a, int64_t n) {
     }
 }
 
-ak_status launch_join(const Args& a, cudaStream_t stream) {
+ak_status launch_join(const Batch& b, cudaStream_t stream) {
+    const Args& a = b.a[0];
     const int64_t n = (int64_t)a.heads * a.dk * a.dv;
-    if ((int64_t)a.dk * a.dv % 4 == 0) k_join<4><<<(unsigned)((n / 4 + 127) / 128), 128, 0, stream>>>(a, n / 4);
-    else k_join<1><<<(unsigned)((n + 127) / 128), 128, 0, stream>>>(a, n);
+    const bool four = (int64_t)a.dk * a.dv % 4 == 0;
+    const dim3 grid((unsigned)((n / (four ? 4 : 1) + 127) / 128), (unsigned)b.count);
+    if (four) k_join<4><<<grid, 128, 0, stream>>>(b, n / 4);
+    else k_join<1><<<grid, 128, 0, stream>>>(b, n);
     count_launches(1);
     return check_launch();
 }
 
 template <class T, int DK>
-ak_status launch_tokens(const Args& a, cudaStream_t stream) {
-    const dim3 grid((unsigned)a.windows, (unsigned)a.heads, (unsigned)((a.dv + 31) / 32));
-    if (a.windows > 1) {
-        k_tokens<T, DK, true><<<grid, kThreads, 0, stream>>>(a);
+ak_status launch_tokens(const Batch& b, cudaStream_t stream) {
+    const Args& a = b.a[0];
+    const int dv = std::max(a.dv, b.count > 1 ? a.dk : 0);
+    const dim3 grid((unsigned)a.windows, (unsigned)a.heads, (unsigned)((dv + 31) / 32 * b.count));
+    if (a.windows > 1 && !a.by_seq) {
+        k_tokens<T, DK, true><<<grid, kThreads, 0, stream>>>(b);
         count_launches(1);
         ak_status s = check_launch();
-        if (s == AK_OK) s = launch_join(a, stream);
+        if (s == AK_OK) s = launch_join(b, stream);
         if (s != AK_OK) return s;
     }
-    k_tokens<T, DK, false><<<grid, kThreads, 0, stream>>>(a);
+    k_tokens<T, DK, false><<<grid, kThreads, 0, stream>>>(b);
     count_launches(1);
     return check_launch();
 }
 
 template <class T>
-ak_status launch_tokens_of(const Args& a, cudaStream_t stream) {
-    if (a.dk <= 32) return launch_tokens<T, 32>(a, stream);
-    if (a.dk <= 64) return launch_tokens<T, 64>(a, stream);
-    if (a.dk <= 128) return launch_tokens<T, 128>(a, stream);
-    return launch_tokens<T, 256>(a, stream);
+ak_status launch_tokens_of(const Batch& b, cudaStream_t stream) {
+    const int dk = std::max(b.a[0].dk, b.count > 1 ? b.a[0].dv : 0);
+    if (dk <= 32) return launch_tokens<T, 32>(b, stream);
+    if (dk <= 64) return launch_tokens<T, 64>(b, stream);
+    if (dk <= 128) return launch_tokens<T, 128>(b, stream);
+    return launch_tokens<T, 256>(b, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -360,37 +374,78 @@ ak_status launch_step(const StepArgs& a, int64_t batch, bool vec, cudaStream_t s
 
 }  // namespace la
 
-// Windows of the packed axis. One window needs neither the fold pass nor the
-// join; more of them fill the device where heads alone do not.
-static int64_t plan_windows(const LinattnCall& c, const DeviceInfo& dev, int64_t* window) {
+// How the token axis is divided among blocks.
+struct Division {
+    bool by_seq;
+    int64_t window, windows;
+};
+
+// `slots`: blocks that run at a time; `lanes`: blocks that a window takes
+// (heads, calls of the launch, column slices). One wave of equal windows
+// leaves no block waiting for a last one, and longer windows have fewer
+// states to pass on. By sequence there is no fold of window states and no
+// join (about a third of the main pass), but the longest sequence, or the
+// last ones to start, set the time: that is taken where it ends sooner.
+static Division divide(const LinattnCall& c, int64_t slots, int64_t lanes) {
     const int64_t unit = 64;
-    int64_t want = c.windows > 0 ? c.windows : (4 * dev.sm_count + c.heads - 1) / c.heads;
+    Division d = {};
     const int64_t units = std::max<int64_t>(1, (c.tokens + unit - 1) / unit);
+    int64_t want = c.windows > 0 ? c.windows : slots / lanes;
     want = std::max<int64_t>(1, std::min(want, units));
     const int64_t per = (units + want - 1) / want;
-    *window = per * unit;
-    return std::max<int64_t>(1, (c.tokens + *window - 1) / *window);
+    d.window = per * unit;
+    d.windows = std::max<int64_t>(1, (c.tokens + d.window - 1) / d.window);
+    if (c.windows > 0 || !c.offsets || c.seqs < 2) return d;
+    const double work = (double)(units + c.seqs) * lanes / slots;  // steps of 64 tokens, spread evenly
+    const double longest = (double)((c.max_len + unit - 1) / unit);
+    const double seq_steps = std::max(longest, work + 0.5 * longest);
+    const double window_steps = d.windows == 1 ? (double)(units + c.seqs) * std::max<int64_t>(1, lanes / slots)
+                                               : std::max(1.35 * work, (double)per) + 4;
+    if (seq_steps <= window_steps) {
+        d.by_seq = true;
+        d.windows = c.seqs;
+    }
+    return d;
+}
+
+static int64_t token_slices(int dv) { return (dv + 31) / 32; }
+
+// Divisions of the two kernels (the pointers decide between them later).
+static Division divide_chunks(const LinattnCall& c, const DeviceInfo& dev, int calls) {
+    return divide(c, 2 * dev.sm_count, (int64_t)c.heads * calls);
+}
+static Division divide_tokens(const LinattnCall& c, const DeviceInfo& dev, int calls) {
+    return divide(c, 8 * dev.sm_count, (int64_t)c.heads * calls * token_slices(std::max(c.dk, c.dv)));
+}
+
+static size_t carry_bytes(const LinattnCall& c, const Division& d, int calls) {
+    if (d.by_seq || d.windows == 1) return 0;
+    const size_t state = (size_t)c.heads * c.dk * c.dv * 4;
+    // one call may work in place and keeps its initial states beside the carries
+    return calls * align_up((size_t)d.windows * 4, 256) + (calls == 1 ? 2 : calls) * align_up((size_t)d.windows * state, 256);
 }
 
 size_t linattn_workspace(const LinattnCall& c, const DeviceInfo& dev) {
-    int64_t window;
-    const int64_t w = plan_windows(c, dev, &window);
-    if (w == 1) return kWsHeader;
-    const size_t state = (size_t)c.heads * c.dk * c.dv * 4;
-    return kWsHeader + align_up((size_t)w * 4, 256) + align_up((size_t)w * state, 256);
+    size_t most = 0;
+    LinattnCall x = c;
+    for (int known = 0; known < 2; ++known) {  // the query does not know whether offsets will be given
+        const int32_t one = 0;
+        x.offsets = known ? &one : nullptr;
+        for (int calls = 1; calls <= la::kMaxCalls; calls += 2) {
+            most = std::max(most, carry_bytes(x, divide_chunks(x, dev, calls), calls));
+            most = std::max(most, carry_bytes(x, divide_tokens(x, dev, calls), calls));
+        }
+    }
+    return kWsHeader + most;
 }
 
-static la::Args args_of(const LinattnCall& c, const DeviceInfo& dev, void* ws) {
+static la::Args args_of(const LinattnCall& c) {
     la::Args a = {};
     a.log_decay = c.log_decay;
     a.offsets = c.offsets;
     a.tokens = c.tokens;
     a.seqs = c.seqs;
     a.heads = c.heads;
-    a.windows = plan_windows(c, dev, &a.window);
-    char* w = static_cast<char*>(ws) + kWsHeader;
-    a.tail = reinterpret_cast<int32_t*>(w);
-    a.carry = reinterpret_cast<float*>(w + align_up((size_t)a.windows * 4, 256));
     return a;
 }
 
@@ -402,43 +457,64 @@ static void roles(la::Args& a, const ak_heads& q, const ak_heads& k, const ak_he
     a.dk = dk, a.dv = dv;
 }
 
-static ak_status run_one(const la::Args& a, const LinattnCall& c, void* ws, cudaStream_t s) {
-    if (la::mma_takes(a, c.dtype)) {
-        const ak_status r = la::launch_chunks(a, static_cast<uint64_t*>(ws), c.epoch, (uint64_t)c.wait_limit_ns, s);
+static ak_status run_batch(la::Batch& b, const LinattnCall& c, const DeviceInfo& dev, void* ws, cudaStream_t s) {
+    auto place = [&](const Division& d) {
+        char* w = static_cast<char*>(ws) + kWsHeader;
+        for (int i = 0; i < b.count; ++i) {
+            la::Args& a = b.a[i];
+            a.by_seq = d.by_seq, a.window = d.window, a.windows = d.windows;
+            a.tail = reinterpret_cast<int32_t*>(w);
+            w += align_up((size_t)d.windows * 4, 256);
+            a.carry = reinterpret_cast<float*>(w);
+            w += align_up((size_t)d.windows * c.heads * c.dk * c.dv * 4, 256);
+            a.stash = nullptr;
+        }
+        // the backward pass has room for three carries and never works in place
+        la::Args& a = b.a[0];
+        if (b.count == 1 && a.s_in && a.s_in == a.s_out && !d.by_seq && d.windows > 1) a.stash = reinterpret_cast<float*>(w);
+    };
+    bool chunks = true;
+    for (int i = 0; i < b.count; ++i) chunks = chunks && la::mma_takes(b.a[i], c.dtype);
+    if (chunks) {
+        place(divide_chunks(c, dev, b.count));
+        const ak_status r = la::launch_chunks(b, static_cast<uint64_t*>(ws), c.epoch, (uint64_t)c.wait_limit_ns, s);
         if (r != AK_ERR_UNSUPPORTED) return r;
     }
-    return c.dtype == AK_F32 ? la::launch_tokens_of<float>(a, s) : la::launch_tokens_of<bf16>(a, s);
+    place(divide_tokens(c, dev, b.count));
+    return c.dtype == AK_F32 ? la::launch_tokens_of<float>(b, s) : la::launch_tokens_of<bf16>(b, s);
 }
 
 ak_status run_linattn(const LinattnCall& c, void* ws, cudaStream_t stream) {
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
-    la::Args a = args_of(c, dev, ws);
+    la::Batch b = {};
+    b.count = 1;
+    la::Args& a = b.a[0];
+    a = args_of(c);
     roles(a, c.q, c.k, c.v, c.o, c.dk, c.dv);
     a.s_in = c.state_in, a.s_out = c.state_out;
     a.out_scale = c.scale, a.in_scale = 1.0f;
-    return run_one(a, c, ws, stream);
+    return run_batch(b, c, dev, ws, stream);
 }
 
 ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stream) {
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
-    la::Args a = args_of(c, dev, ws);
+    la::Batch b = {};
+    b.count = 3;
+    for (la::Args& a : b.a) a = args_of(c);
     // dq = F(do, v, k) from the transposed initial state
-    roles(a, c.o, c.v, c.k, c.dq, c.dv, c.dk);
-    a.s_in = c.state_in, a.s_in_t = true, a.s_out = nullptr;
-    a.out_scale = c.scale, a.in_scale = 1.0f;
-    ak_status s = run_one(a, c, ws, stream);
-    if (s != AK_OK) return s;
-    a.reverse = true, a.out_scale = 1.0f, a.in_scale = c.scale;
+    roles(b.a[0], c.o, c.v, c.k, c.dq, c.dv, c.dk);
+    b.a[0].s_in = c.state_in, b.a[0].s_in_t = true;
+    b.a[0].out_scale = c.scale, b.a[0].in_scale = 1.0f;
     // dv = R(k, q, do) from dS_T, leaving dS_0
-    roles(a, c.k, c.q, c.o, c.dvv, c.dk, c.dv);
-    a.s_in = c.dstate_out, a.s_in_t = false, a.s_out = c.dstate_in;
-    if ((s = run_one(a, c, ws, stream)) != AK_OK) return s;
+    roles(b.a[1], c.k, c.q, c.o, c.dvv, c.dk, c.dv);
+    b.a[1].s_in = c.dstate_out, b.a[1].s_out = c.dstate_in;
     // dk = R(v, do, q) from dS_T transposed
-    roles(a, c.v, c.o, c.q, c.dk_out, c.dv, c.dk);
-    a.s_in_t = true, a.s_out = nullptr;
-    return run_one(a, c, ws, stream);
+    roles(b.a[2], c.v, c.o, c.q, c.dk_out, c.dv, c.dk);
+    b.a[2].s_in = c.dstate_out, b.a[2].s_in_t = true;
+    for (int i = 1; i < 3; ++i) b.a[i].reverse = true, b.a[i].out_scale = 1.0f, b.a[i].in_scale = c.scale;
+    return run_batch(b, c, dev, ws, stream);
 }
 
 ak_status run_linattn_step(const LinattnCall& c, float* state, const int32_t* slots, int64_t nslots,

@@ -17,7 +17,10 @@
 // and one head and walks the pieces of sequences in it. With more than one
 // window the scan takes three launches, like this library's long-line scans:
 // a fold of each window's last piece into its state, a join of the windows'
-// states along the axis, and the main pass from the joined states. Positions
+// states along the axis, and the main pass from the joined states. Where the
+// sequences are many and even, a block takes a sequence instead (by_seq), and
+// the main pass is all there is. The backward pass runs its three calls side
+// by side in the same launches (Batch). Positions
 // below are primed: token t' = T - 1 - t and sequence n' = N - 1 - n in a
 // reversed call, so both directions share every line of this logic.
 #pragma once
@@ -47,9 +50,21 @@ struct Args {
     bool s_in_t;
     bool reverse;
     float out_scale, in_scale;
+    bool by_seq;             // block w takes sequence w; windows = seqs
     int64_t window, windows;
     float* carry;            // [windows][H][dk * dv]
     int32_t* tail;           // [windows]
+    // states written in place (s_out == s_in): the fold pass keeps here what
+    // the main pass needs after another block may have overwritten it, the
+    // initial states of sequences that begin in a window and leave it
+    float* stash;            // as carry, or null
+};
+
+// Calls of one launch: the same tokens, heads and windows.
+constexpr int kMaxCalls = 3;
+struct Batch {
+    Args a[kMaxCalls];
+    int count;
 };
 
 __device__ __forceinline__ int64_t offset_at(const Args& a, int64_t n) {
@@ -71,23 +86,37 @@ __device__ __forceinline__ float decay_pow(float ld, int64_t n) {
 
 // g^n as a sum of two floats. A factor that multiplies the state again and
 // again must not carry a rounding of its own: with a slow decay (memory of M
-// factors) a relative error e in it grows to M e in the state.
+// factors) a relative error e in it grows to M e in the state. M is about
+// 1 / |x| with x = ld n, and 1 + expm1(x) is good to |x| 2^-23; a fast decay
+// forgets the error with the rest.
 struct Factor {
     float hi, lo;
 };
 __device__ __forceinline__ Factor decay_factor(float ld, int n) {
-    const double x = n == 0 ? 1.0 : exp((double)ld * n);
+    const float x = n == 0 ? 0.0f : ld * (float)n;
     Factor f;
-    f.hi = (float)x;
-    f.lo = isinf(f.hi) ? 0.0f : (float)(x - (double)f.hi);
+    f.hi = fabsf(x) < 0.5f ? 1.0f : decay_pow(ld, n);
+    f.lo = fabsf(x) < 0.5f ? expm1f(x) : 0.0f;
     return f;
 }
 __device__ __forceinline__ float operator*(float s, Factor f) { return fmaf(s, f.hi, s * f.lo); }
+
+// First and last + 1 token of block w.
+__device__ __forceinline__ void block_span(const Args& a, int64_t w, int64_t* t0, int64_t* t1) {
+    if (a.by_seq) {  // the blocks at the ends also take what lies outside every sequence
+        *t0 = w == 0 ? 0 : offset_at(a, w);
+        *t1 = w == a.windows - 1 ? a.tokens : offset_at(a, w + 1);
+    } else {
+        *t0 = w * a.window;
+        *t1 = w == a.windows - 1 ? a.tokens : *t0 + a.window;
+    }
+}
 
 // The first sequence with tokens at or after t0, or that is empty at or
 // after t0. All threads of the block take part.
 template <int THREADS>
 __device__ __forceinline__ int64_t first_sequence(const Args& a, int64_t t0, int64_t* s_count) {
+    if (a.by_seq) return blockIdx.x;
     if (!a.offsets || t0 == 0) return 0;
     int64_t c = 0;
     for (int64_t n = threadIdx.x; n < a.seqs; n += THREADS)
@@ -102,10 +131,10 @@ __device__ __forceinline__ int64_t first_sequence(const Args& a, int64_t t0, int
 }
 
 // linattn.cu
-ak_status launch_join(const Args& a, cudaStream_t stream);
+ak_status launch_join(const Batch& b, cudaStream_t stream);
 // linattn_mma.cu
 bool mma_takes(const Args& a, ak_dtype dtype);
-ak_status launch_chunks(const Args& a, uint64_t* error_word, uint64_t epoch, uint64_t wait_limit_ns,
+ak_status launch_chunks(const Batch& b, uint64_t* error_word, uint64_t epoch, uint64_t wait_limit_ns,
                         cudaStream_t stream);
 
 }  // namespace la

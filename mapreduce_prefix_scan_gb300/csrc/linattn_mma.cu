@@ -40,6 +40,10 @@ constexpr int kMmaThreads = 256;
 struct Maps {
     CUtensorMap q, k, v;
     int q_h, k_h, v_h;  // 0: one head shared by all
+};
+struct ChunkBatch {
+    Maps maps[kMaxCalls];
+    Batch b;
     uint64_t* error_word;
     uint64_t epoch;
     uint64_t wait_limit_ns;
@@ -71,23 +75,30 @@ struct Chunk {
 };
 
 template <int D, int PARTS, bool FOLD>
-__global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant__ ChunkBatch batch) {
     using P = Plan<D, PARTS, FOLD>;
     extern __shared__ unsigned char s_raw[];
     __shared__ uint64_t s_full, s_mma, s_upd;
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ int64_t s_count;
-    __shared__ float s_pow[kChunk + 1];
+    // g^n at kChunk + n, zeros below; the second table holds g^n in_scale
+    __shared__ float s_pow_raw[2 * kChunk + 1], s_pows_raw[2 * kChunk + 1];
+    float* const s_pow = s_pow_raw + kChunk;
+    float* const s_pows = s_pows_raw + kChunk;
+    const Args& a = batch.b.a[blockIdx.z];
+    const Maps& maps = batch.maps[blockIdx.z];
     unsigned char* sm = s_raw + ((1024 - (smem_addr(s_raw) & 1023)) & 1023);
     const uint32_t sbase = smem_addr(sm);
-    const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
+    const uint32_t leader = lane == 0;  // of warp 0, which issues products and copies
     const int row = (warp % 4) * 32 + lane;  // TMEM lane
     const int half = warp / 4;               // which half of the columns
     const int dv = row % D;                  // state column (copies at D = 64)
     const int64_t w = blockIdx.x;
     const int h = blockIdx.y;
-    const int64_t t0 = w * a.window, t1 = w == a.windows - 1 ? a.tokens : t0 + a.window;
+    int64_t t0, t1;
+    block_span(a, w, &t0, &t1);
     const float ld = a.log_decay[h];
     const bool rev = a.reverse;
     const int64_t ssize = (int64_t)D * D;
@@ -104,12 +115,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
         tma_prefetch_map(&maps.v);
         if (!FOLD) tma_prefetch_map(&maps.q);
     }
-    if (tid <= kChunk) s_pow[tid] = decay_pow(ld, tid);
+    if (tid <= 2 * kChunk) {
+        const float x = tid < kChunk ? 0.0f : decay_pow(ld, tid - kChunk);
+        s_pow_raw[tid] = x;
+        s_pows_raw[tid] = x * a.in_scale;
+    }
     const Factor whole = decay_factor(ld, kChunk);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
 
     // Bounded waits: a block that gives up records it, skips its further
@@ -117,9 +132,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
     uint32_t full_phase = 0, mma_phase = 0, upd_phase = 0;
     auto wait = [&](uint64_t* bar, uint32_t& phase) {
         if (!mbar_try_wait(bar, phase) && !*(volatile int*)&s_failed) {
-            if (!mbar_wait(bar, phase, globaltimer_ns() + maps.wait_limit_ns)) {
+            if (!mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) {
                 *(volatile int*)&s_failed = 1;
-                if (maps.error_word) *(volatile uint64_t*)maps.error_word = maps.epoch;
+                if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
             }
         }
         phase ^= 1;
@@ -168,7 +183,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
         Chunk c = {};
         for (; n < a.seqs; ++n) {
             const int64_t begin = offset_at(a, n), end = offset_at(a, n + 1);
-            if (begin >= t1 && w != a.windows - 1) break;
+            if (a.by_seq ? n > w : begin >= t1 && w != a.windows - 1) break;
             if (begin > covered) blank(covered, begin < t1 ? begin : t1);
             if (begin > covered) covered = begin;
             c = start(n, begin, end);
@@ -231,6 +246,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
             bool tr = false;
             if (begin >= t0) {
                 if (a.s_in) src = a.s_in + seq_state(c.n), tr = a.s_in_t;
+                // another block may already have written this one's result in place
+                if (!FOLD && a.stash && c.end == t1 && offset_at(a, c.n + 1) > t1) src = a.stash + (w * a.heads + h) * ssize;
             } else if (!FOLD) {
                 src = a.carry + (w * a.heads + h) * ssize;
             }
@@ -253,6 +270,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
                         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(src[(int64_t)(k0 + i) * D + dv]);
                     }
                     tmem_st32(tmem + lanes + P::kS + k0, r);
+                    if (FOLD && a.stash && row < D) {
+                        float* keep = a.stash + (w * a.heads + h) * ssize;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) keep[(int64_t)(k0 + i) * D + dv] = __uint_as_float(r[i]);
+                    }
                 }
                 tmem_wait_st();
             }
@@ -272,18 +294,17 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
             fence_async_smem();
             __syncthreads();
         }
-        if (!FOLD && tid == 0) {
+        if (!FOLD && warp == 0) {
             tc_fence_after();
             // P = Q K^T; rows 64..127 of M read on into the next tile and are not used
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
                 const uint32_t off = (s / 4) * 8192 + (s % 4) * 32;
                 mma_ss(tmem + P::kR, smem_desc(sbase + P::kQ + off, 16), smem_desc(sbase + P::kK + off, 16),
-                       mma_idesc(128, 64, false, false), s > 0);
+                       mma_idesc(128, 64, false, false), s > 0, leader);
             }
-            mma_commit(&s_mma);
+            mma_commit(&s_mma, leader);
         }
-        __syncwarp();
         // S^T as a bf16 operand, and scaled by g^m
         if (!zero) {
             const Factor f = m == kChunk ? whole : decay_factor(ld, m);
@@ -315,7 +336,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
             const int r = i / (D / 8), x = i % (D / 8);
             const int off = (x / 8) * 8192 + swz128(r, x % 8);
             const uint4 vv = *reinterpret_cast<const uint4*>(sm + P::kV + off);
-            const float wt = r < m ? s_pow[rev ? r + 1 : m - 1 - r] * a.in_scale : 0.0f;
+            const float wt = s_pows[rev ? r + 1 : m - 1 - r];  // rows past the chunk are zeros
             const uint32_t in[4] = {vv.x, vv.y, vv.z, vv.w};
             uint32_t part[PARTS][4];
 #pragma unroll
@@ -338,23 +359,24 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
             wait(&s_mma, mma_phase);
             tc_fence_after();
             if (row < kChunk) {
-                // a row of scores: weights g^(i-j) where j is not after i
+                // a row of scores, weighted by g^(i-j); later tokens count nothing
                 uint32_t r[32];
                 tmem_ld32(r, tmem + lanes + P::kR + half * 32);
+                const int step = rev ? 1 : -1;
+                const int gap0 = rev ? half * 32 - row : row - half * 32;
+                float wt[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) wt[j] = s_pows[gap0 + step * j];
                 tmem_wait_ld(r);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     uint32_t p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float y[2];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int j = half * 32 + x * 8 + e * 2 + b;
-                            const int gap = rev ? j - row : row - j;
-                            y[b] = gap >= 0 && j < m ? __uint_as_float(r[x * 8 + e * 2 + b]) * (s_pow[gap < 0 ? 0 : gap] * a.in_scale) : 0.0f;
-                        }
-                        const __nv_bfloat162 z = __floats2bfloat162_rn(y[0], y[1]);
+                        const int j = x * 8 + e * 2;
+                        const float lo = gap0 + step * j >= 0 ? __uint_as_float(r[j]) * wt[j] : 0.0f;
+                        const float hi = gap0 + step * (j + 1) >= 0 ? __uint_as_float(r[j + 1]) * wt[j + 1] : 0.0f;
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(lo, hi);
                         memcpy(&p[e], &z, 4);
                     }
                     *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, half * 4 + x)) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -364,27 +386,30 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
         fence_async_smem();
         tc_fence_before();
         __syncthreads();
-        const Chunk c2 = next(c);
         auto update = [&] {  // S^T += (w V)^T K
 #pragma unroll
             for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                 for (int s = 0; s < kChunk / 16; ++s)
                     mma_ss(tmem + P::kS, smem_desc(sbase + P::kW + p * P::kTileBytes + s * 2048, D == 128 ? 8192 : 0),
-                           smem_desc(sbase + P::kK + s * 2048, 8192), mma_idesc(128, D, true, true), !zero || p > 0 || s > 0);
+                           smem_desc(sbase + P::kK + s * 2048, 8192), mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
         };
+        Chunk c2;
         if (!FOLD) {
             uint32_t inter[32];
-            if (!zero) {
-                if (tid == 0) {
+            if (zero) {
+                c2 = next(c);
+            } else {
+                if (warp == 0) {
                     tc_fence_after();
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
                         mma_ts(tmem + P::kR, tmem + P::kB + s * 8,
                                smem_desc(sbase + P::kQ + (s / 4) * 8192 + (s % 4) * 32, 16),
-                               mma_idesc(128, 64, false, false), s > 0);
-                    mma_commit(&s_mma);
+                               mma_idesc(128, 64, false, false), s > 0, leader);
+                    mma_commit(&s_mma, leader);
                 }
+                c2 = next(c);
                 wait(&s_mma, mma_phase);
                 tc_fence_after();
                 if (row < D) {
@@ -394,38 +419,55 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const Args a, const _
                 tc_fence_before();
                 __syncthreads();
             }
-            if (tid == 0) {
+            if (warp == 0) {
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < kChunk / 16; ++s)
                     mma_ss(tmem + P::kR, smem_desc(sbase + P::kV + s * 2048, D == 128 ? 8192 : 0),
-                           smem_desc(sbase + P::kP + s * 32, 16), mma_idesc(128, 64, true, false), s > 0);
-                mma_commit(&s_mma);
+                           smem_desc(sbase + P::kP + s * 32, 16), mma_idesc(128, 64, true, false), s > 0, leader);
+                mma_commit(&s_mma, leader);
                 update();
-                mma_commit(&s_upd);
+                mma_commit(&s_upd, leader);
                 // the query tile has been used
-                if (c2.valid) load_q(c2);
+                if (leader && c2.valid) load_q(c2);
             }
             wait(&s_mma, mma_phase);
             tc_fence_after();
             if (row < D) {
                 uint32_t r[32];
                 tmem_ld32(r, tmem + lanes + P::kR + half * 32);
+                const float* const pw = s_pow + (rev ? m - 1 - half * 32 : 1 + half * 32);
+                const int step = rev ? -1 : 1;
+                float wt[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) wt[i] = pw[step * i];
                 tmem_wait_ld(r);
-                const int64_t base = low(c);
+                bf16 y[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const int t = half * 32 + i;
-                    float x = __uint_as_float(r[i]);
-                    if (!zero) x = fmaf(__uint_as_float(inter[i]), s_pow[t < m ? (rev ? m - 1 - t : t + 1) : 0], x);
-                    if (t < m) o[(base + t) * a.o_tok + dv] = __float2bfloat16_rn(x * a.out_scale);
+                    const float x = zero ? __uint_as_float(r[i]) : fmaf(__uint_as_float(inter[i]), wt[i], __uint_as_float(r[i]));
+                    y[i] = __float2bfloat16_rn(x * a.out_scale);
+                }
+                bf16* out = o + (low(c) + half * 32) * a.o_tok + dv;
+                if (m == kChunk) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) out[i * a.o_tok] = y[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (half * 32 + i < m) out[i * a.o_tok] = y[i];
                 }
             }
-        } else if (tid == 0) {
-            tc_fence_after();
-            update();
-            mma_commit(&s_upd);
-            if (c2.valid) load_q(c2);
+            __syncwarp();
+        } else {
+            if (warp == 0) {
+                tc_fence_after();
+                update();
+                mma_commit(&s_upd, leader);
+            }
+            c2 = next(c);
+            if (tid == 0 && c2.valid) load_q(c2);
+            __syncwarp();
         }
         wait(&s_upd, upd_phase);  // the update is done: k, v and w V are free
         tc_fence_after();
@@ -499,7 +541,7 @@ bool mma_takes(const Args& a, ak_dtype dtype) {
 }
 
 template <int D, int PARTS, bool FOLD>
-static ak_status launch(const Args& a, const Maps& maps, cudaStream_t stream) {
+static ak_status launch(const ChunkBatch& c, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
@@ -509,34 +551,43 @@ static ak_status launch(const Args& a, const Maps& maps, cudaStream_t stream) {
         if (e != cudaSuccess) return cuda_fail(e);
         ready.fetch_or(1ull << dev.device);
     }
-    k_chunks<D, PARTS, FOLD><<<dim3((unsigned)a.windows, (unsigned)a.heads), kMmaThreads, smem, stream>>>(a, maps);
+    const Args& a = c.b.a[0];
+    const dim3 grid((unsigned)a.windows, (unsigned)a.heads, (unsigned)c.b.count);
+    k_chunks<D, PARTS, FOLD><<<grid, kMmaThreads, smem, stream>>>(c);
     count_launches(1);
     return check_launch();
 }
 
 template <int D, int PARTS>
-static ak_status launch_passes(const Args& a, const Maps& maps, cudaStream_t stream) {
-    if (a.windows > 1) {
-        ak_status s = launch<D, PARTS, true>(a, maps, stream);
-        if (s == AK_OK) s = launch_join(a, stream);
+static ak_status launch_passes(const ChunkBatch& c, cudaStream_t stream) {
+    if (c.b.a[0].windows > 1 && !c.b.a[0].by_seq) {
+        ak_status s = launch<D, PARTS, true>(c, stream);
+        if (s == AK_OK) s = launch_join(c.b, stream);
         if (s != AK_OK) return s;
     }
-    return launch<D, PARTS, false>(a, maps, stream);
+    return launch<D, PARTS, false>(c, stream);
 }
 
-ak_status launch_chunks(const Args& a, uint64_t* error_word, uint64_t epoch, uint64_t wait_limit_ns,
+ak_status launch_chunks(const Batch& b, uint64_t* error_word, uint64_t epoch, uint64_t wait_limit_ns,
                         cudaStream_t stream) {
-    Maps maps;
-    if (!encode(&maps.q, a.q, a.q_tok, a.q_head, a.tokens, a.heads, a.dk) ||
-        !encode(&maps.k, a.k, a.k_tok, a.k_head, a.tokens, a.heads, a.dk) ||
-        !encode(&maps.v, a.v, a.v_tok, a.v_head, a.tokens, a.heads, a.dv))
-        return AK_ERR_UNSUPPORTED;  // nothing was launched
-    maps.q_h = a.q_head != 0 && a.heads > 1, maps.k_h = a.k_head != 0 && a.heads > 1, maps.v_h = a.v_head != 0 && a.heads > 1;
-    maps.error_word = error_word;
-    maps.epoch = epoch;
-    maps.wait_limit_ns = wait_limit_ns;
-    if (a.dk == 128) return a.s_out ? launch_passes<128, 3>(a, maps, stream) : launch_passes<128, 2>(a, maps, stream);
-    return a.s_out ? launch_passes<64, 3>(a, maps, stream) : launch_passes<64, 2>(a, maps, stream);
+    ChunkBatch c;
+    c.b = b;
+    bool final = false;
+    for (int i = 0; i < b.count; ++i) {
+        const Args& a = b.a[i];
+        Maps& m = c.maps[i];
+        if (!encode(&m.q, a.q, a.q_tok, a.q_head, a.tokens, a.heads, a.dk) ||
+            !encode(&m.k, a.k, a.k_tok, a.k_head, a.tokens, a.heads, a.dk) ||
+            !encode(&m.v, a.v, a.v_tok, a.v_head, a.tokens, a.heads, a.dv))
+            return AK_ERR_UNSUPPORTED;  // nothing was launched
+        m.q_h = a.q_head != 0 && a.heads > 1, m.k_h = a.k_head != 0 && a.heads > 1, m.v_h = a.v_head != 0 && a.heads > 1;
+        final = final || a.s_out;
+    }
+    c.error_word = error_word;
+    c.epoch = epoch;
+    c.wait_limit_ns = wait_limit_ns;
+    if (b.a[0].dk == 128) return final ? launch_passes<128, 3>(c, stream) : launch_passes<128, 2>(c, stream);
+    return final ? launch_passes<64, 3>(c, stream) : launch_passes<64, 2>(c, stream);
 }
 
 }  // namespace la

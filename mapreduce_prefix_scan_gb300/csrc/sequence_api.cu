@@ -199,6 +199,8 @@ extern "C" ak_status ak_linear_attention_backward(const ak_linattn* a, const ak_
     if (!float_ptr(log_decay, true) || !float_ptr(offsets, a->seqs != 1) || !float_ptr(state_in, false) ||
         !float_ptr(dstate_out, false) || !float_ptr(dstate_in, false))
         return AK_ERR_INVALID_ARG;
+    // the three gradients are computed side by side: none may write what another reads
+    if (dstate_in && (dstate_in == dstate_out || dstate_in == state_in)) return AK_ERR_INVALID_ARG;
     if (a->tokens == 0 && (a->seqs == 0 || !dstate_in)) return AK_OK;
     LinattnCall c = call_of(a, resolve_opts(opts));
     c.q = *q, c.k = *k, c.v = *v, c.o = *d_o;

@@ -235,6 +235,41 @@ def test_equal_calls_give_equal_bits_and_a_split_sequence_continues(dtype):
     _close(s, sf, _bound("f32", [300], 128, sf, sa), "state")
 
 
+@pytest.mark.parametrize("dtype,dim", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 80)])
+@pytest.mark.parametrize("windows", [1, 7, 0])
+def test_states_in_place(dtype, dim, windows):
+    """state_out may be state_in whatever the windows: the bits of a call with two buffers."""
+    q, k, v, _, ld, off, s0, _ = _inputs(11, dtype, [200, 0, 64, 500, 3], 2, dim, dim)
+    a = [_dev(x, DT[dtype]) for x in (q, k, v)] + [_dev(ld)]
+    opts = dict(target_blocks=windows)
+    o, s1 = ak.ak_linear_attention(*a, offsets=_off(off), state=_dev(s0), final_state=True, opts=opts)
+    s = _dev(s0)
+    for _ in range(3):
+        s.copy_(_dev(s0))
+        o2, _ = ak.ak_linear_attention(*a, offsets=_off(off), state=s, state_out=s, opts=opts)
+        assert torch.equal(o, o2) and torch.equal(s, s1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_even_sequences(dtype):
+    """A block for each sequence (max_len says that none is long)."""
+    lens = [3, 1, 5, 0, 4, 70, 2, 1] * 6
+    q, k, v, do, ld, off, s0, ds = _inputs(12, dtype, lens, 2, 64, 64)
+    d = DT[dtype]
+    a = [_dev(x, d) for x in (q, k, v)] + [_dev(ld)]
+    o, s1 = ak.ak_linear_attention(*a, offsets=_off(off), state=_dev(s0), final_state=True, max_len=70)
+    want, sf, mass = attention(q, k, v, ld, off, s0)
+    _, sa, _ = attention(np.abs(q), np.abs(k), np.abs(v), ld, off, np.abs(s0))
+    _close(o, want, _bound(dtype, lens, 64, want, mass), "o")
+    _close(s1, sf, _bound("f32", lens, 64, sf, sa), "state")
+    g = ak.ak_linear_attention_backward(_dev(do, d), *a, offsets=_off(off), state=_dev(s0), dstate_out=_dev(ds), max_len=70)
+    want = attention_gradients(do, q, k, v, ld, off, s0, ds)
+    mass = _mass_gradients(do, q, k, v, ld, off, s0, ds, 1.0)
+    for i in range(3):
+        _close(g[i], want[i], _bound(dtype, lens, 64, want[i], mass[i]), "gradient %d" % i)
+    _close(g[3], want[3], _bound("f32", lens, 64, want[3], mass[3]), "dstate")
+
+
 def test_no_tokens():
     z = torch.empty(0, 2, 64, device="cuda")
     ld = _dev(np.array([-0.1, -0.2]))

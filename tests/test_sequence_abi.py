@@ -90,7 +90,7 @@ def test_linear_attention_refusals(L):
                                               R(dq), R(dk), R(dv), d0, None, 0, None, None)
 
     for bad in (dict(a=_linattn(heads=0)), dict(do=H(0)), dict(q=H(0)), dict(dq=H(h=0)), dict(dk=H(t=10)), dict(dv=H(0)),
-                dict(ds=0x3001), dict(d0=0x3002)):
+                dict(ds=0x3001), dict(d0=0x3002), dict(ds=0x3000, d0=0x3000)):
         assert bwd(**bad) == INV, bad
 
     def step(a=None, state=0x4000, slots=0x5000, ns=5, o=H(), ld=0x1000):
