@@ -21,6 +21,14 @@
 // float32 accumulation, so it keeps 2^-17 (two parts) or 2^-25 (three) of
 // each term.
 //
+// Nine warps: eight hold the lanes (two to a quarter, half the columns each)
+// and do all elementwise work; the ninth issues copies and products and
+// never waits for more than they need, so the chain of a chunk is: products,
+// barrier, registers, barrier, products.
+//
+// A chunk of fewer than 64 tokens keeps its first row at row 0, in a reversed
+// call its last row at row 63: the weights then depend on the row alone.
+//
 // Head size 64: the A operands repeat their 64 rows (a zero stride between
 // the halves of M), lanes 64..127 hold copies.
 #include <algorithm>
@@ -35,7 +43,8 @@ namespace ak {
 namespace la {
 
 constexpr int kChunk = 64;
-constexpr int kMmaThreads = 256;
+constexpr int kWork = 256;              // threads of the eight working warps
+constexpr int kMmaThreads = kWork + 32;
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -67,9 +76,9 @@ struct Plan {
 
 // What a block walks: the chunks of the sequence pieces in its window.
 struct Chunk {
-    int64_t n;        // sequence
-    int64_t at, end;  // first token; end of the piece
-    int m;            // tokens of the chunk
+    int n;        // sequence
+    int at, end;  // first token; end of the piece (a call has less than 2^31)
+    int m;        // tokens of the chunk
     bool first;       // of the piece
     bool valid;
 };
@@ -78,58 +87,59 @@ template <int D, int PARTS, bool FOLD>
 __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant__ ChunkBatch batch) {
     using P = Plan<D, PARTS, FOLD>;
     extern __shared__ unsigned char s_raw[];
-    __shared__ uint64_t s_full, s_mma, s_upd;
+    // arrivals: TMA; products (scores, state, values, update); working warps
+    // (rows blanked, operands ready, state part read, accumulator read)
+    __shared__ uint64_t s_full, s_scores, s_inter, s_values, s_update, s_blanked, s_ready, s_taken, s_free;
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ int64_t s_count;
-    // g^n at kChunk + n, zeros below; the second table holds g^n in_scale
-    __shared__ float s_pow_raw[2 * kChunk + 1], s_pows_raw[2 * kChunk + 1];
+    // in_scale g^n at kChunk + n, zeros below
+    __shared__ float s_pow_raw[2 * kChunk + 1];
+    __shared__ alignas(16) float s_age[kChunk];  // weight of the state before the chunk at each row
     float* const s_pow = s_pow_raw + kChunk;
-    float* const s_pows = s_pows_raw + kChunk;
     const Args& a = batch.b.a[blockIdx.z];
     const Maps& maps = batch.maps[blockIdx.z];
     unsigned char* sm = s_raw + ((1024 - (smem_addr(s_raw) & 1023)) & 1023);
     const uint32_t sbase = smem_addr(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
-    const uint32_t leader = lane == 0;  // of warp 0, which issues products and copies
-    const int row = (warp % 4) * 32 + lane;  // TMEM lane
-    const int half = warp / 4;               // which half of the columns
-    const int dv = row % D;                  // state column (copies at D = 64)
-    const int64_t w = blockIdx.x;
-    const int h = blockIdx.y;
-    int64_t t0, t1;
-    block_span(a, w, &t0, &t1);
+    const int w = blockIdx.x, h = blockIdx.y;
+    int t0, t1;
+    {
+        int64_t from, to;
+        block_span(a, w, &from, &to);
+        t0 = (int)from, t1 = (int)to;
+    }
     const float ld = a.log_decay[h];
     const bool rev = a.reverse;
-    const int64_t ssize = (int64_t)D * D;
-    bf16* o = static_cast<bf16*>(a.o) + h * a.o_head;
 
-    if (warp == 0) tmem_alloc(&s_tmem, P::kCols);
-    if (tid == 0) {
-        mbar_init(&s_full, 1);
-        mbar_init(&s_mma, 1);
-        mbar_init(&s_upd, 1);
-        fence_barrier_init();
-        s_failed = 0;
-        tma_prefetch_map(&maps.k);
-        tma_prefetch_map(&maps.v);
-        if (!FOLD) tma_prefetch_map(&maps.q);
+    if (warp == kWork / kWarp) {
+        tmem_alloc(&s_tmem, P::kCols);
+        if (lane == 0) {
+            mbar_init(&s_full, 1);
+            mbar_init(&s_scores, 1);
+            mbar_init(&s_inter, 1);
+            mbar_init(&s_values, 1);
+            mbar_init(&s_update, 1);
+            mbar_init(&s_blanked, kWork / kWarp);
+            mbar_init(&s_ready, kWork / kWarp);
+            mbar_init(&s_taken, kWork / kWarp);
+            mbar_init(&s_free, kWork / kWarp);
+            fence_barrier_init();
+            s_failed = 0;
+            tma_prefetch_map(&maps.k);
+            tma_prefetch_map(&maps.v);
+            if (!FOLD) tma_prefetch_map(&maps.q);
+        }
     }
-    if (tid <= 2 * kChunk) {
-        const float x = tid < kChunk ? 0.0f : decay_pow(ld, tid - kChunk);
-        s_pow_raw[tid] = x;
-        s_pows_raw[tid] = x * a.in_scale;
-    }
-    const Factor whole = decay_factor(ld, kChunk);
+    if (tid <= 2 * kChunk) s_pow_raw[tid] = tid < kChunk ? 0.0f : decay_pow(ld, tid - kChunk) * a.in_scale;
+    if (tid < kChunk) s_age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-    const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
 
-    // Bounded waits: a block that gives up records it, skips its further
-    // waits and leaves by the ordinary way.
-    uint32_t full_phase = 0, mma_phase = 0, upd_phase = 0;
+    // Bounded waits: a warp that gives up records it; all skip their further
+    // waits and leave by the ordinary way.
     auto wait = [&](uint64_t* bar, uint32_t& phase) {
         if (!mbar_try_wait(bar, phase) && !*(volatile int*)&s_failed) {
             if (!mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) {
@@ -140,59 +150,58 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         phase ^= 1;
         __syncwarp();  // whole warps go on to the tensor-memory instructions
     };
-
-    auto addr = [&](int64_t t) { return rev ? a.tokens - 1 - t : t; };
-    auto seq_state = [&](int64_t n) { return ((rev ? a.seqs - 1 - n : n) * a.heads + h) * ssize; };
-    // first natural token of a chunk
-    auto low = [&](const Chunk& c) { return rev ? a.tokens - c.at - c.m : c.at; };
-
-    auto load_q = [&](const Chunk& c) {  // announces the whole chunk's bytes
-        mbar_arrive_expect_tx(&s_full, P::kLoadBytes);
-        if (!FOLD)
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b)
-                tma_load_3d(sm + P::kQ + b * 8192, &maps.q, b * 64, h * maps.q_h, (int)low(c), &s_full);
+    // A working warp is done with a step: its shared-memory and tensor-memory
+    // accesses come before what the issuing warp does next.
+    auto arrive = [&](uint64_t* bar) {
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
     };
-    auto load_kv = [&](const Chunk& c) {
-#pragma unroll
-        for (int b = 0; b < D / 64; ++b) {
-            tma_load_3d(sm + P::kK + b * 8192, &maps.k, b * 64, h * maps.k_h, (int)low(c), &s_full);
-            tma_load_3d(sm + P::kV + b * 8192, &maps.v, b * 64, h * maps.v_h, (int)low(c), &s_full);
-        }
-    };
+
+    const int64_t ssize = (int64_t)D * D;
+    bf16* const o = static_cast<bf16*>(a.o) + h * a.o_head;
+    auto addr = [&](int t) { return rev ? (int)a.tokens - 1 - t : t; };
+    auto offset = [&](int n) { return (int)offset_at(a, n); };
+    auto seq_state = [&](int n) { return ((rev ? a.seqs - 1 - n : n) * a.heads + h) * ssize; };
+    // natural token of row 0 (before the array's start for a short reversed chunk)
+    auto low = [&](const Chunk& c) { return rev ? (int)a.tokens - c.at - kChunk : c.at; };
+    const bool writer = tid < kWork;
 
     // tokens of no sequence get zeros
-    auto blank = [&](int64_t from, int64_t to) {
-        if constexpr (!FOLD)
-            for (int64_t t = from + tid / D; t < to; t += kMmaThreads / D)
-                o[addr(t) * a.o_tok + tid % D] = __float2bfloat16_rn(0.0f);
+    auto blank = [&](int from, int to) {
+        if (!FOLD && writer)
+            for (int t = from + tid / D; t < to; t += kWork / D) o[(int64_t)addr(t) * a.o_tok + tid % D] = __float2bfloat16_rn(0.0f);
     };
-    // the next chunk after `c`; pieces without tokens are settled on the way
-    int64_t covered = t0;
-    auto start = [&](int64_t n, int64_t begin, int64_t end) {
+    int covered = t0;
+    auto start = [&](int n, int begin, int end) {
         Chunk c;
         c.n = n;
         c.at = begin > t0 ? begin : t0;
         c.end = end < t1 ? end : t1;
-        c.m = (int)(c.end - c.at < kChunk ? c.end - c.at : kChunk);
+        c.m = c.end - c.at < kChunk ? c.end - c.at : kChunk;
         c.first = true;
         c.valid = true;
         return c;
     };
-    auto seek = [&](int64_t n) {
+    // the first chunk of sequence n or a later one; pieces without tokens are
+    // settled on the way
+    auto seek = [&](int n) {
         Chunk c = {};
         for (; n < a.seqs; ++n) {
-            const int64_t begin = offset_at(a, n), end = offset_at(a, n + 1);
+            const int begin = offset(n), end = offset(n + 1);
             if (a.by_seq ? n > w : begin >= t1 && w != a.windows - 1) break;
-            if (begin > covered) blank(covered, begin < t1 ? begin : t1);
-            if (begin > covered) covered = begin;
+            if (begin > covered) {
+                blank(covered, begin < t1 ? begin : t1);
+                covered = begin;
+            }
             c = start(n, begin, end);
             if (c.at < c.end) {
                 covered = c.end;
                 return c;
             }
-            if (a.s_out && begin >= t0) {  // an empty sequence passes its state on
-                for (int64_t i = tid; i < ssize; i += kMmaThreads)
+            if (writer && a.s_out && begin >= t0) {  // an empty sequence passes its state on
+                for (int i = tid; i < D * D; i += kWork)
                     a.s_out[seq_state(n) + i] = !a.s_in ? 0.0f
                                                 : a.s_in[seq_state(n) + (a.s_in_t ? (i % D) * D + i / D : i)];
             }
@@ -207,295 +216,327 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         x.at += c.m;
         x.first = false;
         if (x.at < c.end) {
-            x.m = (int)(c.end - x.at < kChunk ? c.end - x.at : kChunk);
+            x.m = c.end - x.at < kChunk ? c.end - x.at : kChunk;
             return x;
         }
-        if (FOLD || c.end >= t1) {
-            // nothing of a later sequence but empty ones at the axis' end
-            if (!FOLD && w == a.windows - 1) return seek(c.n + 1);
-            x.valid = false;
-            return x;
-        }
-        return seek(c.n + 1);
+        // at the window's end only empty sequences at the axis' end are left
+        if (!FOLD && (c.end < t1 || w == a.windows - 1)) return seek(c.n + 1);
+        x.valid = false;
+        return x;
     };
 
-    int64_t n = first_sequence<kMmaThreads>(a, t0, &s_count);
-    Chunk c;
+    int n = (int)first_sequence<kMmaThreads>(a, t0, &s_count);
+    Chunk c = {};
     int32_t kind = kNone;
     if (FOLD) {
-        while (n < a.seqs && offset_at(a, n + 1) <= t1) ++n;
-        const int64_t begin = n < a.seqs ? offset_at(a, n) : t1;
+        while (n < a.seqs && offset(n + 1) <= t1) ++n;
+        const int begin = n < a.seqs ? offset(n) : t1;
         kind = begin >= t1 ? kNone : (begin >= t0 ? kFresh : kThrough);
         if (tid == 0 && h == 0) a.tail[w] = kind;
-        c = {};
         if (kind != kNone) c = start(n, begin, t1);
     } else {
         c = seek(n);
     }
-    if (tid == 0 && c.valid) {
-        load_q(c);
-        load_kv(c);
-    }
+    // where the state before a piece comes from; null: zero
+    auto source = [&](const Chunk& c, bool* transposed) -> const float* {
+        *transposed = false;
+        const bool here = FOLD ? kind == kFresh : offset(c.n) >= t0;
+        if (!here) return FOLD ? nullptr : a.carry + ((int64_t)w * a.heads + h) * ssize;
+        if (!a.s_in) return nullptr;
+        // another block may already have written this sequence's result in place
+        if (!FOLD && a.stash && c.end == t1 && offset(c.n + 1) > t1) return a.stash + ((int64_t)w * a.heads + h) * ssize;
+        *transposed = a.s_in_t;
+        return a.s_in + seq_state(c.n);
+    };
 
-    bool zero = true;  // the state before the chunk is zero
-    while (c.valid) {
-        if (c.first) {
-            // the state before the piece
-            const int64_t begin = FOLD ? (kind == kFresh ? c.at : c.at - 1) : offset_at(a, c.n);
-            const float* src = nullptr;
-            bool tr = false;
-            if (begin >= t0) {
-                if (a.s_in) src = a.s_in + seq_state(c.n), tr = a.s_in_t;
-                // another block may already have written this one's result in place
-                if (!FOLD && a.stash && c.end == t1 && offset_at(a, c.n + 1) > t1) src = a.stash + (w * a.heads + h) * ssize;
-            } else if (!FOLD) {
-                src = a.carry + (w * a.heads + h) * ssize;
+    if (warp == kWork / kWarp) {
+        // ------------------------------------------------------------------
+        // copies and products
+        // ------------------------------------------------------------------
+        const uint32_t leader = lane == 0;
+        uint32_t full = 0, blanked = 0, ready = 0, taken = 0, free_ = 0, update = 0;
+        const uint64_t dq = smem_desc(sbase + P::kQ, 16), dk = smem_desc(sbase + P::kK, 16);
+        const uint64_t dkt = smem_desc(sbase + P::kK, 8192);
+        const uint64_t dvt = smem_desc(sbase + P::kV, D == 128 ? 8192 : 0);
+        const uint64_t dp = smem_desc(sbase + P::kP, 16), dw = smem_desc(sbase + P::kW, D == 128 ? 8192 : 0);
+        auto load_q = [&](const Chunk& c) {  // announces the whole chunk's bytes
+            if (!leader) return;
+            mbar_arrive_expect_tx(&s_full, P::kLoadBytes);
+            if (!FOLD)
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b)
+                    tma_load_3d(sm + P::kQ + b * 8192, &maps.q, b * 64, h * maps.q_h, (int)low(c), &s_full);
+        };
+        auto load_kv = [&](const Chunk& c) {
+            if (!leader) return;
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+                tma_load_3d(sm + P::kK + b * 8192, &maps.k, b * 64, h * maps.k_h, (int)low(c), &s_full);
+                tma_load_3d(sm + P::kV + b * 8192, &maps.v, b * 64, h * maps.v_h, (int)low(c), &s_full);
             }
-            zero = src == nullptr;
-            if (src) {
+        };
+        if (c.valid) {
+            load_q(c);
+            load_kv(c);
+        }
+        bool zero = true, begun = false;
+        while (c.valid) {
+            if (c.first) {
+                bool t;
+                zero = source(c, &t) == nullptr;
+            }
+            wait(&s_full, full);
+            if (c.m < kChunk) wait(&s_blanked, blanked);
+            if (!FOLD) {
+                if (begun) wait(&s_free, free_);
+                tc_fence_after();
+                // P = Q K^T; rows 64..127 of M read on into the next tile and are not used
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint64_t off = ((s / 4) * 8192 + (s % 4) * 32) >> 4;
+                    mma_ss(tmem + P::kR, dq + off, dk + off, mma_idesc(128, 64, false, false), s > 0, leader);
+                }
+                mma_commit(&s_scores, leader);
+            }
+            const Chunk c2 = next(c);
+            wait(&s_ready, ready);
+            tc_fence_after();
+            if (!FOLD) {
+                if (!zero) {
+                    // S^T Q^T
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_ts(tmem + P::kR, tmem + P::kB + s * 8, dq + (((s / 4) * 8192 + (s % 4) * 32) >> 4),
+                               mma_idesc(128, 64, false, false), s > 0, leader);
+                    mma_commit(&s_inter, leader);
+                    wait(&s_taken, taken);
+                    tc_fence_after();
+                }
+                // V^T P^T
+#pragma unroll
+                for (int s = 0; s < kChunk / 16; ++s)
+                    mma_ss(tmem + P::kR, dvt + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), s > 0, leader);
+                mma_commit(&s_values, leader);
+            }
+            // S^T += (w V)^T K
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                for (int s = 0; s < kChunk / 16; ++s)
+                    mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dkt + (s * 2048 >> 4),
+                           mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
+            mma_commit(&s_update, leader);
+            // the query tile has been used; key and value tiles once the update is done
+            if (c2.valid) load_q(c2);
+            wait(&s_update, update);
+            if (c2.valid) load_kv(c2);
+            zero = false;
+            begun = true;
+            c = c2;
+        }
+    } else {
+        // ------------------------------------------------------------------
+        // elementwise work
+        // ------------------------------------------------------------------
+        const int row = (warp % 4) * 32 + lane;  // TMEM lane
+        const int half = warp / 4;               // which half of the columns
+        const int dv = row % D;                  // state column (copies at D = 64)
+        const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
+        const Factor whole = decay_factor(ld, kChunk);
+        uint32_t full = 0, scores = 0, inter_ = 0, values = 0, update = 0;
+        bool zero = true;
+        while (c.valid) {
+            const int m = c.m;
+            const int r0 = rev ? kChunk - m : 0;  // rows r0 .. r0 + m - 1 hold the chunk
+            if (c.first) {
+                bool tr;
+                const float* src = source(c, &tr);
+                zero = src == nullptr;
+                if (src) {
+#pragma unroll 1
+                    for (int k0 = half * (D / 2); k0 < (half + 1) * (D / 2); k0 += 16) {
+                        uint32_t r[16];
+                        const float* p = tr ? src + dv * D + k0 : src + k0 * D + dv;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i, p += tr ? 1 : D) r[i] = __float_as_uint(*p);
+                        tmem_st16(lanes + P::kS + k0, r);
+                        if (FOLD && a.stash && row < D) {
+                            float* keep = a.stash + ((int64_t)w * a.heads + h) * ssize + k0 * D + dv;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) keep[i * D] = __uint_as_float(r[i]);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+            }
+            // S^T as a bf16 operand, and scaled by g^m
+            if (!zero) {
+                const Factor f = m == kChunk ? whole : decay_factor(ld, m);
 #pragma unroll 1
                 for (int b = 0; b < D / 64; ++b) {
                     const int k0 = half * (D / 2) + b * 32;
                     uint32_t r[32];
-                    if (tr) {
+                    tmem_ld32(r, lanes + P::kS + k0);
+                    tmem_wait_ld(r);
+                    if (!FOLD) {
+                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            // rows of a transposed state are the caller's: 4-byte alignment is all that is known
-                            const float* p = src + (int64_t)dv * D + k0 + i;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) r[i + e] = __float_as_uint(p[e]);
+                        for (int i = 0; i < 16; ++i) {
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                            memcpy(&p[i], &x, 4);
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(src[(int64_t)(k0 + i) * D + dv]);
+                        tmem_st16(lanes + P::kB + k0 / 2, p);
                     }
-                    tmem_st32(tmem + lanes + P::kS + k0, r);
-                    if (FOLD && a.stash && row < D) {
-                        float* keep = a.stash + (w * a.heads + h) * ssize;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) keep[(int64_t)(k0 + i) * D + dv] = __uint_as_float(r[i]);
-                    }
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                    tmem_st32(lanes + P::kS + k0, r);
                 }
                 tmem_wait_st();
             }
-        }
-        wait(&s_full, full_phase);
-        const int m = c.m;
-        if (m < kChunk) {
-            // rows past the chunk belong to other sequences: whatever they
-            // hold (a NaN times a zero weight is a NaN) must not enter sums
-            constexpr int kPerRow = D / 8;
-            for (int i = tid; i < (kChunk - m) * kPerRow; i += kMmaThreads) {
-                const int r = m + i / kPerRow, x = i % kPerRow;
+            wait(&s_full, full);
+            if (m < kChunk) {
+                // the other rows belong to other sequences: whatever they hold
+                // (a NaN times a zero weight is a NaN) must not enter sums
+                constexpr int kPerRow = D / 8;
+                for (int i = tid; i < (kChunk - m) * kPerRow; i += kWork) {
+                    const int r = (rev ? 0 : m) + i / kPerRow, x = i % kPerRow;
+                    const int off = (x / 8) * 8192 + swz128(r, x % 8);
+                    *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
+                }
+                arrive(&s_blanked);
+            }
+            // w V in bf16 parts
+#pragma unroll
+            for (int i = 0; i < kChunk * D / 8 / kWork; ++i) {
+                const int r = (tid + i * kWork) / (D / 8), x = (tid + i * kWork) % (D / 8);
                 const int off = (x / 8) * 8192 + swz128(r, x % 8);
-                *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            __syncthreads();
-        }
-        if (!FOLD && warp == 0) {
-            tc_fence_after();
-            // P = Q K^T; rows 64..127 of M read on into the next tile and are not used
+                uint4 vv = *reinterpret_cast<const uint4*>(sm + P::kV + off);
+                if ((unsigned)(r - r0) >= (unsigned)m) vv = make_uint4(0, 0, 0, 0);
+                const float wt = s_pow[rev ? r + 1 - r0 : m - 1 - r];
+                const uint32_t in[4] = {vv.x, vv.y, vv.z, vv.w};
+                uint32_t part[PARTS][4];
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const uint32_t off = (s / 4) * 8192 + (s % 4) * 32;
-                mma_ss(tmem + P::kR, smem_desc(sbase + P::kQ + off, 16), smem_desc(sbase + P::kK + off, 16),
-                       mma_idesc(128, 64, false, false), s > 0, leader);
-            }
-            mma_commit(&s_mma, leader);
-        }
-        // S^T as a bf16 operand, and scaled by g^m
-        if (!zero) {
-            const Factor f = m == kChunk ? whole : decay_factor(ld, m);
-#pragma unroll 1
-            for (int b = 0; b < D / 64; ++b) {
-                const int k0 = half * (D / 2) + b * 32;
-                uint32_t r[32];
-                tmem_ld32(r, tmem + lanes + P::kS + k0);
-                tmem_wait_ld(r);
-                if (!FOLD) {
-                    uint32_t p[16];
+                for (int e = 0; e < 4; ++e) {
+                    float lo = __uint_as_float(in[e] << 16) * wt, hi = __uint_as_float(in[e] & 0xffff0000u) * wt;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        memcpy(&p[i], &x, 4);
+                    for (int p = 0; p < PARTS; ++p) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+                        memcpy(&part[p][e], &y, 4);
+                        lo -= __uint_as_float(part[p][e] << 16);
+                        hi -= __uint_as_float(part[p][e] & 0xffff0000u);
                     }
-                    tmem_st16(tmem + lanes + P::kB + k0 / 2, p);
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                tmem_st32(tmem + lanes + P::kS + k0, r);
+                for (int p = 0; p < PARTS; ++p)
+                    *reinterpret_cast<uint4*>(sm + P::kW + p * P::kTileBytes + off) =
+                        make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
             }
-            tmem_wait_st();
-        }
-        // w V in bf16 parts
-        constexpr int kChunks16 = kChunk * D / 8;
+            if (!FOLD) {
+                wait(&s_scores, scores);
+                tc_fence_after();
+                if (row < kChunk) {
+                    // a row of scores, weighted by g^(i-j); later tokens count nothing
+                    const int step = rev ? 1 : -1;
+                    const int gap0 = rev ? half * 32 - row : row - half * 32;
 #pragma unroll
-        for (int i = tid; i < kChunks16; i += kMmaThreads) {
-            const int r = i / (D / 8), x = i % (D / 8);
-            const int off = (x / 8) * 8192 + swz128(r, x % 8);
-            const uint4 vv = *reinterpret_cast<const uint4*>(sm + P::kV + off);
-            const float wt = s_pows[rev ? r + 1 : m - 1 - r];  // rows past the chunk are zeros
-            const uint32_t in[4] = {vv.x, vv.y, vv.z, vv.w};
-            uint32_t part[PARTS][4];
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t r[16];
+                        tmem_ld16(r, lanes + P::kR + half * 32 + y * 16);
+                        float wt[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float lo = __uint_as_float(in[e] << 16) * wt, hi = __uint_as_float(in[e] & 0xffff0000u) * wt;
+                        for (int j = 0; j < 16; ++j) wt[j] = s_pow[gap0 + step * (y * 16 + j)];
+                        tmem_wait_ld(r);
+                        uint32_t p[8];
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
-                    memcpy(&part[p][e], &y, 4);
-                    lo -= __uint_as_float(part[p][e] << 16);
-                    hi -= __uint_as_float(part[p][e] & 0xffff0000u);
-                }
-            }
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p)
-                *reinterpret_cast<uint4*>(sm + P::kW + p * P::kTileBytes + off) =
-                    make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
-        }
-        if (!FOLD) {
-            wait(&s_mma, mma_phase);
-            tc_fence_after();
-            if (row < kChunk) {
-                // a row of scores, weighted by g^(i-j); later tokens count nothing
-                uint32_t r[32];
-                tmem_ld32(r, tmem + lanes + P::kR + half * 32);
-                const int step = rev ? 1 : -1;
-                const int gap0 = rev ? half * 32 - row : row - half * 32;
-                float wt[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) wt[j] = s_pows[gap0 + step * j];
-                tmem_wait_ld(r);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = x * 8 + e * 2;
-                        const float lo = gap0 + step * j >= 0 ? __uint_as_float(r[j]) * wt[j] : 0.0f;
-                        const float hi = gap0 + step * (j + 1) >= 0 ? __uint_as_float(r[j + 1]) * wt[j + 1] : 0.0f;
-                        const __nv_bfloat162 z = __floats2bfloat162_rn(lo, hi);
-                        memcpy(&p[e], &z, 4);
+                        for (int e = 0; e < 8; ++e) {
+                            const int j = y * 16 + e * 2;
+                            const float lo = gap0 + step * j >= 0 ? __uint_as_float(r[e * 2]) * wt[e * 2] : 0.0f;
+                            const float hi = gap0 + step * (j + 1) >= 0 ? __uint_as_float(r[e * 2 + 1]) * wt[e * 2 + 1] : 0.0f;
+                            const __nv_bfloat162 z = __floats2bfloat162_rn(lo, hi);
+                            memcpy(&p[e], &z, 4);
+                        }
+                        *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, half * 4 + y * 2)) = make_uint4(p[0], p[1], p[2], p[3]);
+                        *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, half * 4 + y * 2 + 1)) = make_uint4(p[4], p[5], p[6], p[7]);
                     }
-                    *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, half * 4 + x)) = make_uint4(p[0], p[1], p[2], p[3]);
                 }
             }
-        }
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        auto update = [&] {  // S^T += (w V)^T K
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                for (int s = 0; s < kChunk / 16; ++s)
-                    mma_ss(tmem + P::kS, smem_desc(sbase + P::kW + p * P::kTileBytes + s * 2048, D == 128 ? 8192 : 0),
-                           smem_desc(sbase + P::kK + s * 2048, 8192), mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
-        };
-        Chunk c2;
-        if (!FOLD) {
-            uint32_t inter[32];
-            if (zero) {
-                c2 = next(c);
-            } else {
-                if (warp == 0) {
+            arrive(&s_ready);
+            const Chunk c2 = next(c);
+            if (!FOLD) {
+                uint32_t inter[32];
+                if (!zero) {
+                    wait(&s_inter, inter_);
                     tc_fence_after();
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_ts(tmem + P::kR, tmem + P::kB + s * 8,
-                               smem_desc(sbase + P::kQ + (s / 4) * 8192 + (s % 4) * 32, 16),
-                               mma_idesc(128, 64, false, false), s > 0, leader);
-                    mma_commit(&s_mma, leader);
+                    if (row < D) {
+                        tmem_ld32(inter, lanes + P::kR + half * 32);
+                        tmem_wait_ld(inter);
+                    }
+                    arrive(&s_taken);
                 }
-                c2 = next(c);
-                wait(&s_mma, mma_phase);
+                wait(&s_values, values);
                 tc_fence_after();
                 if (row < D) {
-                    tmem_ld32(inter, tmem + lanes + P::kR + half * 32);
-                    tmem_wait_ld(inter);
-                }
-                tc_fence_before();
-                __syncthreads();
-            }
-            if (warp == 0) {
-                tc_fence_after();
+                    bf16* out = o + (int64_t)(low(c) + half * 32) * a.o_tok + dv;
 #pragma unroll
-                for (int s = 0; s < kChunk / 16; ++s)
-                    mma_ss(tmem + P::kR, smem_desc(sbase + P::kV + s * 2048, D == 128 ? 8192 : 0),
-                           smem_desc(sbase + P::kP + s * 32, 16), mma_idesc(128, 64, true, false), s > 0, leader);
-                mma_commit(&s_mma, leader);
-                update();
-                mma_commit(&s_upd, leader);
-                // the query tile has been used
-                if (leader && c2.valid) load_q(c2);
-            }
-            wait(&s_mma, mma_phase);
-            tc_fence_after();
-            if (row < D) {
-                uint32_t r[32];
-                tmem_ld32(r, tmem + lanes + P::kR + half * 32);
-                const float* const pw = s_pow + (rev ? m - 1 - half * 32 : 1 + half * 32);
-                const int step = rev ? -1 : 1;
-                float wt[32];
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t r[16];
+                        tmem_ld16(r, lanes + P::kR + half * 32 + y * 16);
+                        float4 wt[4];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) wt[i] = pw[step * i];
-                tmem_wait_ld(r);
-                bf16 y[32];
+                        for (int i = 0; i < 4; ++i) wt[i] = *reinterpret_cast<const float4*>(&s_age[half * 32 + y * 16 + i * 4]);
+                        tmem_wait_ld(r);
+                        if (y == 1) arrive(&s_free);
+                        bf16 z[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float x = zero ? __uint_as_float(r[i]) : fmaf(__uint_as_float(inter[i]), wt[i], __uint_as_float(r[i]));
-                    y[i] = __float2bfloat16_rn(x * a.out_scale);
-                }
-                bf16* out = o + (low(c) + half * 32) * a.o_tok + dv;
-                if (m == kChunk) {
+                        for (int i = 0; i < 16; ++i) {
+                            const float g = i % 4 == 0 ? wt[i / 4].x : i % 4 == 1 ? wt[i / 4].y : i % 4 == 2 ? wt[i / 4].z : wt[i / 4].w;
+                            float x = __uint_as_float(r[i]);
+                            if (!zero) x = fmaf(__uint_as_float(inter[y * 16 + i]), g, x);
+                            z[i] = __float2bfloat16_rn(x * a.out_scale);
+                        }
+                        if (m == kChunk) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) out[i * a.o_tok] = y[i];
+                            for (int i = 0; i < 16; ++i, out += a.o_tok) *out = z[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i, out += a.o_tok)
+                                if ((unsigned)(half * 32 + y * 16 + i - r0) < (unsigned)m) *out = z[i];
+                        }
+                    }
                 } else {
+                    arrive(&s_free);
+                }
+                __syncwarp();
+            }
+            wait(&s_update, update);  // the state is up to date; w V may be overwritten
+            tc_fence_after();
+            zero = false;
+            // the state after the piece
+            float* dst = nullptr;
+            if (c.at + m == c.end) {
+                if (FOLD) dst = a.carry + ((int64_t)w * a.heads + h) * ssize;
+                else if (a.s_out && c.end == offset(c.n + 1)) dst = a.s_out + seq_state(c.n);
+            }
+            if (dst && row < D) {
+#pragma unroll 1
+                for (int k0 = half * (D / 2); k0 < (half + 1) * (D / 2); k0 += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(r, lanes + P::kS + k0);
+                    tmem_wait_ld(r);
+                    float* to = dst + k0 * D + dv;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (half * 32 + i < m) out[i * a.o_tok] = y[i];
+                    for (int i = 0; i < 16; ++i) to[i * D] = __uint_as_float(r[i]);
                 }
             }
             __syncwarp();
-        } else {
-            if (warp == 0) {
-                tc_fence_after();
-                update();
-                mma_commit(&s_upd, leader);
-            }
-            c2 = next(c);
-            if (tid == 0 && c2.valid) load_q(c2);
-            __syncwarp();
+            c = c2;
         }
-        wait(&s_upd, upd_phase);  // the update is done: k, v and w V are free
-        tc_fence_after();
-        if (tid == 0 && c2.valid) load_kv(c2);
-        zero = false;
-        // the state after the piece
-        float* dst = nullptr;
-        if (c.at + m == c.end) {
-            if (FOLD) dst = a.carry + (w * a.heads + h) * ssize;
-            else if (a.s_out && c.end == offset_at(a, c.n + 1)) dst = a.s_out + seq_state(c.n);
-        }
-        if (dst && row < D) {
-#pragma unroll 1
-            for (int b = 0; b < D / 64; ++b) {
-                const int k0 = half * (D / 2) + b * 32;
-                uint32_t r[32];
-                tmem_ld32(r, tmem + lanes + P::kS + k0);
-                tmem_wait_ld(r);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) dst[(int64_t)(k0 + i) * D + dv] = __uint_as_float(r[i]);
-            }
-        }
-        tc_fence_before();
-        c = c2;
-        __syncthreads();
     }
+    tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_free(tmem, P::kCols);
+    tc_fence_after();
+    if (warp == kWork / kWarp) tmem_free(tmem, P::kCols);
 }
 
 // ---------------------------------------------------------------------------
