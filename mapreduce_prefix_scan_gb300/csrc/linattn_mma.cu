@@ -6,8 +6,8 @@
 //   S  <- g^m S + sum_j g^(m-1-j) k_j v_j^T
 // (a reversed call: g^i in place of g^(i+1), g^(m-j) of g^(m-1-j), see
 // linattn.cuh). Everything is held transposed, M = dv = the 128 TMEM lanes:
-//   P    = Q K^T                    64 x 64 scores (accumulator R)
-//   O^T  = V^T P^T  and  S^T Q^T    two products, combined in registers (R)
+//   P    = Q K^T                    64 x 64 scores, weighted, bf16
+//   O^T  = V^T P^T  and  S^T Q^T    one accumulator (R) in turn, combined in registers
 //   S^T += (w V)^T K                the float32 state, which stays in TMEM
 // so that S^T, read out once a chunk to be scaled, goes back to TMEM as the
 // bf16 A operand of its product with Q^T without passing shared memory, and
@@ -23,8 +23,9 @@
 //
 // Nine warps: eight hold the lanes (two to a quarter, half the columns each)
 // and do all elementwise work; the ninth issues copies and products and
-// never waits for more than they need, so the chain of a chunk is: products,
-// barrier, registers, barrier, products.
+// never waits for more than they need. A chunk's chain: state operand; w V
+// and the scores while S^T Q^T runs; V^T P^T; the outputs while the update
+// runs.
 //
 // A chunk of fewer than 64 tokens keeps its first row at row 0, in a reversed
 // call its last row at row 63: the weights then depend on the row alone.
@@ -87,9 +88,9 @@ template <int D, int PARTS, bool FOLD>
 __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant__ ChunkBatch batch) {
     using P = Plan<D, PARTS, FOLD>;
     extern __shared__ unsigned char s_raw[];
-    // arrivals: TMA; products (scores, state, values, update); working warps
-    // (rows blanked, operands ready, state part read, accumulator read)
-    __shared__ uint64_t s_full, s_scores, s_inter, s_values, s_update, s_blanked, s_ready, s_taken, s_free;
+    // arrivals: TMA (q and k, v), products (of the state, of the values, the
+    // update), working warps (state operand ready, the other operands ready)
+    __shared__ uint64_t s_qk, s_v, s_inter, s_values, s_update, s_state, s_ready;
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ int64_t s_count;
@@ -115,15 +116,13 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
     if (warp == kWork / kWarp) {
         tmem_alloc(&s_tmem, P::kCols);
         if (lane == 0) {
-            mbar_init(&s_full, 1);
-            mbar_init(&s_scores, 1);
+            mbar_init(&s_qk, 1);
+            mbar_init(&s_v, 1);
             mbar_init(&s_inter, 1);
             mbar_init(&s_values, 1);
             mbar_init(&s_update, 1);
-            mbar_init(&s_blanked, kWork / kWarp);
+            mbar_init(&s_state, kWork / kWarp);
             mbar_init(&s_ready, kWork / kWarp);
-            mbar_init(&s_taken, kWork / kWarp);
-            mbar_init(&s_free, kWork / kWarp);
             fence_barrier_init();
             s_failed = 0;
             tma_prefetch_map(&maps.k);
@@ -254,68 +253,56 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         // copies and products
         // ------------------------------------------------------------------
         const uint32_t leader = lane == 0;
-        uint32_t full = 0, blanked = 0, ready = 0, taken = 0, free_ = 0, update = 0;
-        const uint64_t dq = smem_desc(sbase + P::kQ, 16), dk = smem_desc(sbase + P::kK, 16);
-        const uint64_t dkt = smem_desc(sbase + P::kK, 8192);
-        const uint64_t dvt = smem_desc(sbase + P::kV, D == 128 ? 8192 : 0);
-        const uint64_t dp = smem_desc(sbase + P::kP, 16), dw = smem_desc(sbase + P::kW, D == 128 ? 8192 : 0);
-        auto load_q = [&](const Chunk& c) {  // announces the whole chunk's bytes
-            if (!leader) return;
-            mbar_arrive_expect_tx(&s_full, P::kLoadBytes);
-            if (!FOLD)
+        uint32_t qk = 0, v = 0, state = 0, ready = 0, values = 0, update = 0;
+        const uint64_t dq = smem_desc(sbase + P::kQ, 16), dp = smem_desc(sbase + P::kP, 16);
+        const uint64_t dk = smem_desc(sbase + P::kK, 8192);
+        const uint64_t dv = smem_desc(sbase + P::kV, D == 128 ? 8192 : 0);
+        const uint64_t dw = smem_desc(sbase + P::kW, D == 128 ? 8192 : 0);
+        auto load = [&](const Chunk& c, uint64_t* bar, uint32_t expect, const CUtensorMap* map, int head, int at) {
+            if (leader) {
+                if (expect) mbar_arrive_expect_tx(bar, expect);
 #pragma unroll
-                for (int b = 0; b < D / 64; ++b)
-                    tma_load_3d(sm + P::kQ + b * 8192, &maps.q, b * 64, h * maps.q_h, (int)low(c), &s_full);
-        };
-        auto load_kv = [&](const Chunk& c) {
-            if (!leader) return;
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-                tma_load_3d(sm + P::kK + b * 8192, &maps.k, b * 64, h * maps.k_h, (int)low(c), &s_full);
-                tma_load_3d(sm + P::kV + b * 8192, &maps.v, b * 64, h * maps.v_h, (int)low(c), &s_full);
+                for (int b = 0; b < D / 64; ++b) tma_load_3d(sm + at + b * 8192, map, b * 64, h * head, low(c), bar);
             }
+            __syncwarp();
         };
+        // q announces its own bytes and those of k, which comes later
+        auto load_q = [&](const Chunk& c) {
+            if (!FOLD) load(c, &s_qk, 2 * P::kTileBytes, &maps.q, maps.q_h, P::kQ);
+        };
+        auto load_k = [&](const Chunk& c) { load(c, &s_qk, FOLD ? P::kTileBytes : 0, &maps.k, maps.k_h, P::kK); };
+        auto load_v = [&](const Chunk& c) { load(c, &s_v, P::kTileBytes, &maps.v, maps.v_h, P::kV); };
         if (c.valid) {
+            load_v(c);
             load_q(c);
-            load_kv(c);
+            load_k(c);
         }
-        bool zero = true, begun = false;
+        bool zero = true;
         while (c.valid) {
             if (c.first) {
                 bool t;
                 zero = source(c, &t) == nullptr;
             }
-            wait(&s_full, full);
-            if (c.m < kChunk) wait(&s_blanked, blanked);
-            if (!FOLD) {
-                if (begun) wait(&s_free, free_);
+            if (!FOLD && !zero) wait(&s_state, state);
+            wait(&s_qk, qk);
+            if (!FOLD && !zero) {
+                // S^T Q^T
                 tc_fence_after();
-                // P = Q K^T; rows 64..127 of M read on into the next tile and are not used
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint64_t off = ((s / 4) * 8192 + (s % 4) * 32) >> 4;
-                    mma_ss(tmem + P::kR, dq + off, dk + off, mma_idesc(128, 64, false, false), s > 0, leader);
-                }
-                mma_commit(&s_scores, leader);
+                for (int s = 0; s < D / 16; ++s)
+                    mma_ts(tmem + P::kR, tmem + P::kB + s * 8, dq + (((s / 4) * 8192 + (s % 4) * 32) >> 4),
+                           mma_idesc(128, 64, false, false), s > 0, leader);
+                mma_commit(&s_inter, leader);
             }
             const Chunk c2 = next(c);
+            wait(&s_v, v);
             wait(&s_ready, ready);
             tc_fence_after();
             if (!FOLD) {
-                if (!zero) {
-                    // S^T Q^T
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_ts(tmem + P::kR, tmem + P::kB + s * 8, dq + (((s / 4) * 8192 + (s % 4) * 32) >> 4),
-                               mma_idesc(128, 64, false, false), s > 0, leader);
-                    mma_commit(&s_inter, leader);
-                    wait(&s_taken, taken);
-                    tc_fence_after();
-                }
                 // V^T P^T
 #pragma unroll
                 for (int s = 0; s < kChunk / 16; ++s)
-                    mma_ss(tmem + P::kR, dvt + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), s > 0, leader);
+                    mma_ss(tmem + P::kR, dv + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), s > 0, leader);
                 mma_commit(&s_values, leader);
             }
             // S^T += (w V)^T K
@@ -323,15 +310,17 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                 for (int s = 0; s < kChunk / 16; ++s)
-                    mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dkt + (s * 2048 >> 4),
+                    mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dk + (s * 2048 >> 4),
                            mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
             mma_commit(&s_update, leader);
-            // the query tile has been used; key and value tiles once the update is done
+            // the next chunk's tiles, each as soon as its buffer has been used
             if (c2.valid) load_q(c2);
-            wait(&s_update, update);
-            if (c2.valid) load_kv(c2);
+            if (!FOLD) wait(&s_values, values);
+            if (FOLD) wait(&s_update, update);
+            if (c2.valid) load_v(c2);
+            if (!FOLD) wait(&s_update, update);
+            if (c2.valid) load_k(c2);
             zero = false;
-            begun = true;
             c = c2;
         }
     } else {
@@ -343,7 +332,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         const int dv = row % D;                  // state column (copies at D = 64)
         const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
         const Factor whole = decay_factor(ld, kChunk);
-        uint32_t full = 0, scores = 0, inter_ = 0, values = 0, update = 0;
+        uint32_t qk = 0, v = 0, inter_ = 0, values = 0, update = 0;
         bool zero = true;
         while (c.valid) {
             const int m = c.m;
@@ -392,9 +381,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                     tmem_st32(lanes + P::kS + k0, r);
                 }
                 tmem_wait_st();
+                if (!FOLD) arrive(&s_state);
             }
-            wait(&s_full, full);
+            wait(&s_v, v);
             if (m < kChunk) {
+                wait(&s_qk, qk);
                 // the other rows belong to other sequences: whatever they hold
                 // (a NaN times a zero weight is a NaN) must not enter sums
                 constexpr int kPerRow = D / 8;
@@ -404,7 +395,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                     *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
                 }
-                arrive(&s_blanked);
             }
             // w V in bf16 parts
 #pragma unroll
@@ -432,39 +422,42 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                     *reinterpret_cast<uint4*>(sm + P::kW + p * P::kTileBytes + off) =
                         make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
             }
+            if (m == kChunk) wait(&s_qk, qk);
+            uint32_t inter[32];
             if (!FOLD) {
-                wait(&s_scores, scores);
-                tc_fence_after();
-                if (row < kChunk) {
-                    // a row of scores, weighted by g^(i-j); later tokens count nothing
-                    const int step = rev ? 1 : -1;
-                    const int gap0 = rev ? half * 32 - row : row - half * 32;
+                // Scores of 16 rows and 32 columns a warp, on register-level
+                // matrix instructions: a tile of 64 x 64 leaves half of a
+                // tcgen05 product unused, and its way through TMEM (issue,
+                // barrier, load: about 1300 cycles) lies on the chunk's chain,
+                // which these 32 instructions from shared memory shorten.
+                const int rb = (warp % 4) * 16, cb = half * 32;
+                const int gap0 = rev ? cb - rb : rb - cb;  // of the corner
+                float x[4][4] = {};
+                if (gap0 > -16 - (rev ? 32 - 16 : 0)) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint32_t r[16];
-                        tmem_ld16(r, lanes + P::kR + half * 32 + y * 16);
-                        float wt[16];
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint32_t box = sbase + (s / 4) * 8192;
+                        uint32_t qa[4], kb[8];
+                        ldmatrix4(qa, box + P::kQ + swz128(rb + lane % 16, (s % 4) * 2 + lane / 16));
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) wt[j] = s_pow[gap0 + step * (y * 16 + j)];
-                        tmem_wait_ld(r);
-                        uint32_t p[8];
+                        for (int t = 0; t < 2; ++t)
+                            ldmatrix4(kb + 4 * t, box + P::kK + swz128(cb + t * 16 + lane % 8 + lane / 16 * 8, (s % 4) * 2 + lane / 8 % 2));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int j = y * 16 + e * 2;
-                            const float lo = gap0 + step * j >= 0 ? __uint_as_float(r[e * 2]) * wt[e * 2] : 0.0f;
-                            const float hi = gap0 + step * (j + 1) >= 0 ? __uint_as_float(r[e * 2 + 1]) * wt[e * 2 + 1] : 0.0f;
-                            const __nv_bfloat162 z = __floats2bfloat162_rn(lo, hi);
-                            memcpy(&p[e], &z, 4);
-                        }
-                        *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, half * 4 + y * 2)) = make_uint4(p[0], p[1], p[2], p[3]);
-                        *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, half * 4 + y * 2 + 1)) = make_uint4(p[4], p[5], p[6], p[7]);
+                        for (int t = 0; t < 4; ++t) mma_16x8x16(x[t], qa, kb[2 * t], kb[2 * t + 1]);
                     }
                 }
-            }
-            arrive(&s_ready);
-            const Chunk c2 = next(c);
-            if (!FOLD) {
-                uint32_t inter[32];
+                // weighted by g^(i-j); later tokens count nothing
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = rb + lane / 4 + 8 * e, j = cb + t * 8 + lane % 4 * 2;
+                        const int gap = rev ? j - i : i - j, gap1 = rev ? gap + 1 : gap - 1;
+                        const float lo = gap >= 0 ? x[t][2 * e] * s_pow[gap] : 0.0f;
+                        const float hi = gap1 >= 0 ? x[t][2 * e + 1] * s_pow[gap1] : 0.0f;
+                        *reinterpret_cast<__nv_bfloat162*>(sm + P::kP + swz128(i, j / 8) + j % 8 * 2) = __floats2bfloat162_rn(lo, hi);
+                    }
+                }
                 if (!zero) {
                     wait(&s_inter, inter_);
                     tc_fence_after();
@@ -472,8 +465,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                         tmem_ld32(inter, lanes + P::kR + half * 32);
                         tmem_wait_ld(inter);
                     }
-                    arrive(&s_taken);
                 }
+            }
+            arrive(&s_ready);
+            const Chunk c2 = next(c);
+            if (!FOLD) {
                 wait(&s_values, values);
                 tc_fence_after();
                 if (row < D) {
@@ -486,7 +482,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
 #pragma unroll
                         for (int i = 0; i < 4; ++i) wt[i] = *reinterpret_cast<const float4*>(&s_age[half * 32 + y * 16 + i * 4]);
                         tmem_wait_ld(r);
-                        if (y == 1) arrive(&s_free);
                         bf16 z[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -504,8 +499,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                                 if ((unsigned)(half * 32 + y * 16 + i - r0) < (unsigned)m) *out = z[i];
                         }
                     }
-                } else {
-                    arrive(&s_free);
                 }
                 __syncwarp();
             }
