@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
         }
     };
 
-    int64_t n = first_sequence<kThreads>(a, t0, &s_count);
+    int64_t n = first_sequence<kThreads>(a, w, t0, &s_count);
     if (FOLD) {
         // the sequence that crosses the window's end
         while (n < a.seqs && offset_at(a, n + 1) <= t1) ++n;
@@ -386,19 +386,22 @@ struct Division {
 // states to pass on. By sequence there is no fold of window states and no
 // join (about a third of the main pass), but the longest sequence, or the
 // last ones to start, set the time: that is taken where it ends sooner.
+constexpr int64_t kMaxWindows = 65535;  // a grid's second extent
+
 static Division divide(const LinattnCall& c, int64_t slots, int64_t lanes) {
     const int64_t unit = 64;
     Division d = {};
     const int64_t units = std::max<int64_t>(1, (c.tokens + unit - 1) / unit);
     int64_t want = c.windows > 0 ? c.windows : slots / lanes;
-    want = std::max<int64_t>(1, std::min(want, units));
+    want = std::max<int64_t>(1, std::min({want, units, kMaxWindows}));
     const int64_t per = (units + want - 1) / want;
     d.window = per * unit;
     d.windows = std::max<int64_t>(1, (c.tokens + d.window - 1) / d.window);
-    if (c.windows > 0 || !c.offsets || c.seqs < 2) return d;
+    if (c.windows > 0 || !c.offsets || c.seqs < 2 || c.seqs > kMaxWindows) return d;
     const double work = (double)(units + c.seqs) * lanes / slots;  // steps of 64 tokens, spread evenly
     const double longest = (double)((c.max_len + unit - 1) / unit);
-    const double seq_steps = std::max(longest, work + 0.5 * longest);
+    // (the longest start first, see linattn_mma.cu)
+    const double seq_steps = std::max(longest, work + (c.seqs <= la::kRanked ? 0.15 : 0.5) * longest);
     const double window_steps = d.windows == 1 ? (double)(units + c.seqs) * std::max<int64_t>(1, lanes / slots)
                                                : std::max(1.35 * work, (double)per) + 4;
     if (seq_steps <= window_steps) {

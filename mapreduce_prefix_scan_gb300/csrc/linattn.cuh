@@ -62,6 +62,7 @@ struct Args {
 
 // Calls of one launch: the same tokens, heads and windows.
 constexpr int kMaxCalls = 3;
+constexpr int kRanked = 256;  // sequences that blocks sort by length
 struct Batch {
     Args a[kMaxCalls];
     int count;
@@ -115,8 +116,8 @@ __device__ __forceinline__ void block_span(const Args& a, int64_t w, int64_t* t0
 // The first sequence with tokens at or after t0, or that is empty at or
 // after t0. All threads of the block take part.
 template <int THREADS>
-__device__ __forceinline__ int64_t first_sequence(const Args& a, int64_t t0, int64_t* s_count) {
-    if (a.by_seq) return blockIdx.x;
+__device__ __forceinline__ int64_t first_sequence(const Args& a, int64_t w, int64_t t0, int64_t* s_count) {
+    if (a.by_seq) return w;
     if (!a.offsets || t0 == 0) return 0;
     int64_t c = 0;
     for (int64_t n = threadIdx.x; n < a.seqs; n += THREADS)

@@ -16,14 +16,20 @@
 //
 // Precision. Scores and the state are rounded to bf16 (once each) where they
 // enter a product whose result is rounded to bf16 anyway. The state itself is
-// float32 and may be an output: w V is split into bf16 parts (hi, mid and,
-// where the final state is asked for, lo), whose products are exact in the
-// float32 accumulation, so it keeps 2^-17 (two parts) or 2^-25 (three) of
-// each term.
+// float32 and may be an output: w V is split into bf16 parts whose products
+// are exact in the float32 accumulation. Two parts keep 2^-17 of a term, three
+// 2^-25; the third is spent where the final state is asked for and the term
+// will still weigh more than 2^-8 in it.
 //
-// Nine warps: eight hold the lanes (two to a quarter, half the columns each)
-// and do all elementwise work; the ninth issues copies and products and
-// never waits for more than they need. A chunk's chain: state operand; w V
+// What bounds it: shared memory, whose 128 bytes a cycle serve the tensor
+// core's operands, TMA and the working warps alike. A chunk of 64 tokens at
+// D = 128 needs about 2000 cycles of it (tiles in 384, w V 384, its products
+// 512, scores 450, the other two products 320), against 2700 that its 64 KB
+// take from HBM at an SM's share.
+//
+// Seventeen warps: sixteen do the elementwise work (on TMEM, four to a
+// quarter of the lanes, a quarter of the columns each); the last issues
+// copies and products and never waits for more than they need. A chunk's chain: state operand; w V
 // and the scores while S^T Q^T runs; V^T P^T; the outputs while the update
 // runs.
 //
@@ -44,8 +50,9 @@ namespace ak {
 namespace la {
 
 constexpr int kChunk = 64;
-constexpr int kWork = 256;              // threads of the eight working warps
+constexpr int kWork = 512;              // threads of the working warps
 constexpr int kMmaThreads = kWork + 32;
+constexpr int kScoreWarps = 6;           // of the sixteen; the others make w V
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -94,16 +101,33 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ int64_t s_count;
-    // in_scale g^n at kChunk + n, zeros below
-    __shared__ float s_pow_raw[2 * kChunk + 1];
+    // g^n at kChunk + n, zeros below: times in_scale for the update, times
+    // both scales for the scores
+    __shared__ float s_pow_raw[2 * kChunk + 1], s_score_raw[2 * kChunk + 1];
     __shared__ alignas(16) float s_age[kChunk];  // weight of the state before the chunk at each row
+    __shared__ int s_len[kRanked], s_rank;
     float* const s_pow = s_pow_raw + kChunk;
+    float* const s_score = s_score_raw + kChunk;
     const Args& a = batch.b.a[blockIdx.z];
     const Maps& maps = batch.maps[blockIdx.z];
     unsigned char* sm = s_raw + ((1024 - (smem_addr(s_raw) & 1023)) & 1023);
     const uint32_t sbase = smem_addr(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
-    const int w = blockIdx.x, h = blockIdx.y;
+    const int h = blockIdx.x;
+    int w = blockIdx.y;
+    if (a.by_seq && a.seqs <= kRanked) {
+        // block w takes the w-th longest sequence: the long ones start first
+        for (int i = tid; i < a.seqs; i += kMmaThreads) s_len[i] = (int)(offset_at(a, i + 1) - offset_at(a, i));
+        __syncthreads();
+        for (int i = tid; i < a.seqs; i += kMmaThreads) {
+            const int mine = s_len[i];
+            int rank = 0;
+            for (int j = 0; j < a.seqs; ++j) rank += s_len[j] > mine || (s_len[j] == mine && j < i);
+            if (rank == w) s_rank = i;
+        }
+        __syncthreads();
+        w = s_rank;
+    }
     int t0, t1;
     {
         int64_t from, to;
@@ -130,8 +154,15 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             if (!FOLD) tma_prefetch_map(&maps.q);
         }
     }
-    if (tid <= 2 * kChunk) s_pow_raw[tid] = tid < kChunk ? 0.0f : decay_pow(ld, tid - kChunk) * a.in_scale;
-    if (tid < kChunk) s_age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1);
+    if (tid <= 2 * kChunk) {
+        const float x = tid < kChunk ? 0.0f : decay_pow(ld, tid - kChunk) * a.in_scale;
+        s_pow_raw[tid] = x;
+        s_score_raw[tid] = x * a.out_scale;
+    }
+    if (tid < kChunk) s_age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1) * a.out_scale;
+    if (!FOLD)  // scores after their row stay zero
+        for (int i = tid; i < kChunk * kChunk / 8; i += kMmaThreads) *reinterpret_cast<uint4*>(sm + P::kP + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -224,7 +255,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         return x;
     };
 
-    int n = (int)first_sequence<kMmaThreads>(a, t0, &s_count);
+    int n = (int)first_sequence<kMmaThreads>(a, w, t0, &s_count);
     Chunk c = {};
     int32_t kind = kNone;
     if (FOLD) {
@@ -236,6 +267,10 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
     } else {
         c = seek(n);
     }
+    // parts of w V that a chunk's terms need
+    auto parts_of = [&](const Chunk& c) {
+        return PARTS == 3 && ld * (float)(offset(c.n + 1) - c.at - c.m) > -5.55f ? 3 : 2;
+    };
     // where the state before a piece comes from; null: zero
     auto source = [&](const Chunk& c, bool* transposed) -> const float* {
         *transposed = false;
@@ -294,6 +329,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                            mma_idesc(128, 64, false, false), s > 0, leader);
                 mma_commit(&s_inter, leader);
             }
+            const int parts = parts_of(c);
             const Chunk c2 = next(c);
             wait(&s_v, v);
             wait(&s_ready, ready);
@@ -308,10 +344,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             // S^T += (w V)^T K
 #pragma unroll
             for (int p = 0; p < PARTS; ++p)
+                if (p < 2 || parts == 3)
 #pragma unroll
-                for (int s = 0; s < kChunk / 16; ++s)
-                    mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dk + (s * 2048 >> 4),
-                           mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
+                    for (int s = 0; s < kChunk / 16; ++s)
+                        mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dk + (s * 2048 >> 4),
+                               mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
             mma_commit(&s_update, leader);
             // the next chunk's tiles, each as soon as its buffer has been used
             if (c2.valid) load_q(c2);
@@ -328,7 +365,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         // elementwise work
         // ------------------------------------------------------------------
         const int row = (warp % 4) * 32 + lane;  // TMEM lane
-        const int half = warp / 4;               // which half of the columns
+        const int part = warp / 4;               // which quarter of the columns
         const int dv = row % D;                  // state column (copies at D = 64)
         const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
         const Factor whole = decay_factor(ld, kChunk);
@@ -342,129 +379,162 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                 const float* src = source(c, &tr);
                 zero = src == nullptr;
                 if (src) {
+                    // a fold ages its state once, not chunk by chunk
+                    const float age = FOLD ? decay_pow(ld, t1 - c.at) : 1.0f;
 #pragma unroll 1
-                    for (int k0 = half * (D / 2); k0 < (half + 1) * (D / 2); k0 += 16) {
+                    for (int k0 = part * (D / 4); k0 < (part + 1) * (D / 4); k0 += 16) {
                         uint32_t r[16];
                         const float* p = tr ? src + dv * D + k0 : src + k0 * D + dv;
 #pragma unroll
                         for (int i = 0; i < 16; ++i, p += tr ? 1 : D) r[i] = __float_as_uint(*p);
-                        tmem_st16(lanes + P::kS + k0, r);
                         if (FOLD && a.stash && row < D) {
                             float* keep = a.stash + ((int64_t)w * a.heads + h) * ssize + k0 * D + dv;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) keep[i * D] = __uint_as_float(r[i]);
                         }
+                        if (FOLD)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * age);
+                        tmem_st16(lanes + P::kS + k0, r);
                     }
                     tmem_wait_st();
                 }
             }
             // S^T as a bf16 operand, and scaled by g^m
-            if (!zero) {
+            if (!FOLD && !zero) {
                 const Factor f = m == kChunk ? whole : decay_factor(ld, m);
 #pragma unroll 1
-                for (int b = 0; b < D / 64; ++b) {
-                    const int k0 = half * (D / 2) + b * 32;
-                    uint32_t r[32];
-                    tmem_ld32(r, lanes + P::kS + k0);
+                for (int k0 = part * (D / 4); k0 < (part + 1) * (D / 4); k0 += 16) {
+                    uint32_t r[16], p[8];
+                    tmem_ld16(r, lanes + P::kS + k0);
                     tmem_wait_ld(r);
-                    if (!FOLD) {
-                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                            memcpy(&p[i], &x, 4);
-                        }
-                        tmem_st16(lanes + P::kB + k0 / 2, p);
+                    for (int i = 0; i < 8; ++i) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                        memcpy(&p[i], &x, 4);
                     }
+                    tmem_st8(lanes + P::kB + k0 / 2, p);
+                    if (f.hi == 1.0f) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                    tmem_st32(lanes + P::kS + k0, r);
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(fmaf(__uint_as_float(r[i]), f.lo, __uint_as_float(r[i])));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f.hi);
+                    }
+                    tmem_st16(lanes + P::kS + k0, r);
                 }
                 tmem_wait_st();
-                if (!FOLD) arrive(&s_state);
+                arrive(&s_state);
             }
-            wait(&s_v, v);
-            if (m < kChunk) {
+            uint32_t inter[16];
+            if (!FOLD && warp < kScoreWarps) {
                 wait(&s_qk, qk);
-                // the other rows belong to other sequences: whatever they hold
-                // (a NaN times a zero weight is a NaN) must not enter sums
-                constexpr int kPerRow = D / 8;
-                for (int i = tid; i < (kChunk - m) * kPerRow; i += kWork) {
-                    const int r = (rev ? 0 : m) + i / kPerRow, x = i % kPerRow;
-                    const int off = (x / 8) * 8192 + swz128(r, x % 8);
-                    *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            // w V in bf16 parts
+                v ^= 1;
+                // Scores: 32 x 16 a warp, on register-level matrix
+                // instructions; the quarter of the tile after its rows stays
+                // zero. The way through TMEM (issue, barrier, load: about 1300
+                // cycles) would lie on the chunk's chain and wants 64 columns
+                // that are not there.
+                const int rb = (rev ? warp > 3 : warp > 1) * 32;
+                const int cb = (rev ? (warp > 3 ? warp - 2 : warp) : (warp > 1 ? warp - 2 : warp)) * 16;
+                float x[2][2][4] = {};
 #pragma unroll
-            for (int i = 0; i < kChunk * D / 8 / kWork; ++i) {
-                const int r = (tid + i * kWork) / (D / 8), x = (tid + i * kWork) % (D / 8);
-                const int off = (x / 8) * 8192 + swz128(r, x % 8);
-                uint4 vv = *reinterpret_cast<const uint4*>(sm + P::kV + off);
-                if ((unsigned)(r - r0) >= (unsigned)m) vv = make_uint4(0, 0, 0, 0);
-                const float wt = s_pow[rev ? r + 1 - r0 : m - 1 - r];
-                const uint32_t in[4] = {vv.x, vv.y, vv.z, vv.w};
-                uint32_t part[PARTS][4];
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t box = sbase + (s / 4) * 8192;
+                    uint32_t qa[2][4], kb[4];
+                    ldmatrix4(kb, box + P::kK + swz128(cb + lane % 8 + lane / 16 * 8, (s % 4) * 2 + lane / 8 % 2));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float lo = __uint_as_float(in[e] << 16) * wt, hi = __uint_as_float(in[e] & 0xffff0000u) * wt;
+                    for (int u = 0; u < 2; ++u) {
+                        ldmatrix4(qa[u], box + P::kQ + swz128(rb + u * 16 + lane % 16, (s % 4) * 2 + lane / 16));
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p) {
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
-                        memcpy(&part[p][e], &y, 4);
-                        lo -= __uint_as_float(part[p][e] << 16);
-                        hi -= __uint_as_float(part[p][e] & 0xffff0000u);
-                    }
-                }
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-                    *reinterpret_cast<uint4*>(sm + P::kW + p * P::kTileBytes + off) =
-                        make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
-            }
-            if (m == kChunk) wait(&s_qk, qk);
-            uint32_t inter[32];
-            if (!FOLD) {
-                // Scores of 16 rows and 32 columns a warp, on register-level
-                // matrix instructions: a tile of 64 x 64 leaves half of a
-                // tcgen05 product unused, and its way through TMEM (issue,
-                // barrier, load: about 1300 cycles) lies on the chunk's chain,
-                // which these 32 instructions from shared memory shorten.
-                const int rb = (warp % 4) * 16, cb = half * 32;
-                const int gap0 = rev ? cb - rb : rb - cb;  // of the corner
-                float x[4][4] = {};
-                if (gap0 > -16 - (rev ? 32 - 16 : 0)) {
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t box = sbase + (s / 4) * 8192;
-                        uint32_t qa[4], kb[8];
-                        ldmatrix4(qa, box + P::kQ + swz128(rb + lane % 16, (s % 4) * 2 + lane / 16));
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            ldmatrix4(kb + 4 * t, box + P::kK + swz128(cb + t * 16 + lane % 8 + lane / 16 * 8, (s % 4) * 2 + lane / 8 % 2));
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) mma_16x8x16(x[t], qa, kb[2 * t], kb[2 * t + 1]);
+                        for (int t = 0; t < 2; ++t) mma_16x8x16(x[u][t], qa[u], kb[2 * t], kb[2 * t + 1]);
                     }
                 }
                 // weighted by g^(i-j); later tokens count nothing
+                const int i0 = rb + lane / 4, j0 = cb + lane % 4 * 2;
+                const int corner = rev ? j0 - i0 : i0 - j0;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int i = rb + lane / 4 + 8 * e, j = cb + t * 8 + lane % 4 * 2;
-                        const int gap = rev ? j - i : i - j, gap1 = rev ? gap + 1 : gap - 1;
-                        const float lo = gap >= 0 ? x[t][2 * e] * s_pow[gap] : 0.0f;
-                        const float hi = gap1 >= 0 ? x[t][2 * e + 1] * s_pow[gap1] : 0.0f;
-                        *reinterpret_cast<__nv_bfloat162*>(sm + P::kP + swz128(i, j / 8) + j % 8 * 2) = __floats2bfloat162_rn(lo, hi);
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int di = u * 16 + e * 8, dj = t * 8;
+                            const int gap = corner + (rev ? dj - di : di - dj), gap1 = rev ? gap + 1 : gap - 1;
+                            const float wl = s_score[gap], wh = s_score[gap1];
+                            const float lo = gap >= 0 ? x[u][t][2 * e] * wl : 0.0f;
+                            const float hi = gap1 >= 0 ? x[u][t][2 * e + 1] * wh : 0.0f;
+                            *reinterpret_cast<__nv_bfloat162*>(sm + P::kP + swz128(i0 + di, cb / 8 + t) + lane % 4 * 4) =
+                                __floats2bfloat162_rn(lo, hi);
+                        }
+            } else {
+                // w V in bf16 parts
+                constexpr int kFirst = FOLD ? 0 : kScoreWarps * kWarp, kCount = kWork - kFirst;
+                const int mine = tid - kFirst;
+                wait(&s_v, v);
+                if (m < kChunk) {
+                    // the other rows belong to other sequences: whatever they hold
+                    // (a NaN times a zero weight is a NaN) must not enter sums
+                    wait(&s_qk, qk);
+                    constexpr int kPerRow = D / 8;
+                    for (int i = mine; i < (kChunk - m) * kPerRow; i += kCount) {
+                        const int r = (rev ? 0 : m) + i / kPerRow, x = i % kPerRow;
+                        const int off = (x / 8) * 8192 + swz128(r, x % 8);
+                        *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
+                    }
+                } else {
+                    qk ^= 1;
+                }
+                const int parts = parts_of(c);
+                const float* const pw = s_pow + (rev ? 1 - r0 : m - 1);
+                const float age = FOLD ? decay_pow(ld, t1 - c.at - m) : 1.0f;
+#pragma unroll 2
+                for (int i = mine; i < kChunk * D / 8; i += kCount) {
+                    const int r = i / (D / 8), x = i % (D / 8);
+                    const int off = (x / 8) * 8192 + swz128(r, x % 8);
+                    uint4 vv = *reinterpret_cast<const uint4*>(sm + P::kV + off);
+                    if ((unsigned)(r - r0) >= (unsigned)m) vv = make_uint4(0, 0, 0, 0);
+                    const float wt = pw[rev ? r : -r] * age;
+                    const uint32_t in[4] = {vv.x, vv.y, vv.z, vv.w};
+                    uint32_t part[2][4];
+                    float rest[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lo = __uint_as_float(in[e] << 16) * wt, hi = __uint_as_float(in[e] & 0xffff0000u) * wt;
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+                            memcpy(&part[p][e], &y, 4);
+                            if (p == 0 || PARTS == 3) {
+                                lo -= __uint_as_float(part[p][e] << 16);
+                                hi -= __uint_as_float(part[p][e] & 0xffff0000u);
+                            }
+                        }
+                        rest[2 * e] = lo, rest[2 * e + 1] = hi;
+                    }
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        *reinterpret_cast<uint4*>(sm + P::kW + p * P::kTileBytes + off) =
+                            make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+                    if (PARTS == 3 && parts == 3) {
+                        uint32_t last[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 y = __floats2bfloat162_rn(rest[2 * e], rest[2 * e + 1]);
+                            memcpy(&last[e], &y, 4);
+                        }
+                        *reinterpret_cast<uint4*>(sm + P::kW + 2 * P::kTileBytes + off) = make_uint4(last[0], last[1], last[2], last[3]);
                     }
                 }
-                if (!zero) {
-                    wait(&s_inter, inter_);
-                    tc_fence_after();
-                    if (row < D) {
-                        tmem_ld32(inter, lanes + P::kR + half * 32);
-                        tmem_wait_ld(inter);
-                    }
+            }
+            __syncwarp();
+            if (!FOLD && !zero) {
+                wait(&s_inter, inter_);
+                tc_fence_after();
+                if (row < D) {
+                    tmem_ld16(inter, lanes + P::kR + part * 16);
+                    tmem_wait_ld(inter);
                 }
             }
             arrive(&s_ready);
@@ -473,31 +543,30 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                 wait(&s_values, values);
                 tc_fence_after();
                 if (row < D) {
-                    bf16* out = o + (int64_t)(low(c) + half * 32) * a.o_tok + dv;
+                    bf16* const out = o + (int64_t)(low(c) + part * 16) * a.o_tok + dv;
+                    const int tok = (int)a.o_tok;
+                    uint32_t r[16];
+                    tmem_ld16(r, lanes + P::kR + part * 16);
+                    tmem_wait_ld(r);
+                    bf16 z[16];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint32_t r[16];
-                        tmem_ld16(r, lanes + P::kR + half * 32 + y * 16);
-                        float4 wt[4];
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 g = *reinterpret_cast<const float4*>(&s_age[part * 16 + i]);
+                        const float wt[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) wt[i] = *reinterpret_cast<const float4*>(&s_age[half * 32 + y * 16 + i * 4]);
-                        tmem_wait_ld(r);
-                        bf16 z[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float g = i % 4 == 0 ? wt[i / 4].x : i % 4 == 1 ? wt[i / 4].y : i % 4 == 2 ? wt[i / 4].z : wt[i / 4].w;
-                            float x = __uint_as_float(r[i]);
-                            if (!zero) x = fmaf(__uint_as_float(inter[y * 16 + i]), g, x);
-                            z[i] = __float2bfloat16_rn(x * a.out_scale);
+                        for (int e = 0; e < 4; ++e) {
+                            float x = __uint_as_float(r[i + e]);
+                            if (!zero) x = fmaf(__uint_as_float(inter[i + e]), wt[e], x);
+                            z[i + e] = __float2bfloat16_rn(x);
                         }
-                        if (m == kChunk) {
+                    }
+                    if (m == kChunk) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i, out += a.o_tok) *out = z[i];
-                        } else {
+                        for (int i = 0; i < 16; ++i) out[(int64_t)tok * i] = z[i];
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i, out += a.o_tok)
-                                if ((unsigned)(half * 32 + y * 16 + i - r0) < (unsigned)m) *out = z[i];
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            if ((unsigned)(part * 16 + i - r0) < (unsigned)m) out[(int64_t)tok * i] = z[i];
                     }
                 }
                 __syncwarp();
@@ -513,7 +582,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             }
             if (dst && row < D) {
 #pragma unroll 1
-                for (int k0 = half * (D / 2); k0 < (half + 1) * (D / 2); k0 += 16) {
+                for (int k0 = part * (D / 4); k0 < (part + 1) * (D / 4); k0 += 16) {
                     uint32_t r[16];
                     tmem_ld16(r, lanes + P::kS + k0);
                     tmem_wait_ld(r);
@@ -569,7 +638,7 @@ static bool tma_rows(const void* p, int64_t tok, int64_t head, int64_t tokens, i
 
 // Whether the chunked kernel takes a call of these roles.
 bool mma_takes(const Args& a, ak_dtype dtype) {
-    return dtype == AK_BF16 && a.dk == a.dv && (a.dk == 64 || a.dk == 128) && a.tokens > 0 &&
+    return dtype == AK_BF16 && a.o_tok < (1 << 30) && a.dk == a.dv && (a.dk == 64 || a.dk == 128) && a.tokens > 0 &&
            tma_rows(a.q, a.q_tok, a.q_head, a.tokens, a.heads) && tma_rows(a.k, a.k_tok, a.k_head, a.tokens, a.heads) &&
            tma_rows(a.v, a.v_tok, a.v_head, a.tokens, a.heads) && encoder() != nullptr;
 }
@@ -586,7 +655,7 @@ static ak_status launch(const ChunkBatch& c, cudaStream_t stream) {
         ready.fetch_or(1ull << dev.device);
     }
     const Args& a = c.b.a[0];
-    const dim3 grid((unsigned)a.windows, (unsigned)a.heads, (unsigned)c.b.count);
+    const dim3 grid((unsigned)a.heads, (unsigned)a.windows, (unsigned)c.b.count);
     k_chunks<D, PARTS, FOLD><<<grid, kMmaThreads, smem, stream>>>(c);
     count_launches(1);
     return check_launch();
