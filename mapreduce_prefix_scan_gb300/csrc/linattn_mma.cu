@@ -27,11 +27,12 @@
 // 512, scores 450, the other two products 320), against 2700 that its 64 KB
 // take from HBM at an SM's share.
 //
-// Seventeen warps: sixteen do the elementwise work (on TMEM, four to a
-// quarter of the lanes, a quarter of the columns each); the last issues
-// copies and products and never waits for more than they need. A chunk's chain: state operand; w V
-// and the scores while S^T Q^T runs; V^T P^T; the outputs while the update
-// runs.
+// Nine warps: eight do the elementwise work (on TMEM, two to a quarter of the
+// lanes, half of the columns each); the ninth issues copies and products, each as soon as its operands are there and its target
+// is free. A chunk's chain is S^T Q^T, Q K^T, weights, V^T P^T; beside the
+// first two run the outputs of the chunk before and w V, beside the last the
+// state's pass for the next chunk; the update runs beside the weights, so the
+// key tile is free half a chunk before its successor is needed.
 //
 // A chunk of fewer than 64 tokens keeps its first row at row 0, in a reversed
 // call its last row at row 63: the weights then depend on the row alone.
@@ -50,9 +51,8 @@ namespace ak {
 namespace la {
 
 constexpr int kChunk = 64;
-constexpr int kWork = 512;              // threads of the working warps
+constexpr int kWork = 256;              // threads of the working warps
 constexpr int kMmaThreads = kWork + 32;
-constexpr int kScoreWarps = 6;           // of the sixteen; the others make w V
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -77,37 +77,78 @@ struct Plan {
     static constexpr int kEnd = kW + PARTS * kTileBytes;
     // two blocks an SM share its TMEM: no third one may become resident
     static constexpr int kSmem = 1024 + (kEnd < 80 * 1024 && !FOLD ? 80 * 1024 : kEnd);
-    static constexpr uint32_t kS = 0, kB = D, kR = D + D / 2;
+    // columns: S, its bf16 form, accumulator, scores (over the bf16 form at D = 128)
+    static constexpr uint32_t kS = 0, kB = D, kR = D + D / 2, kX = D == 128 ? kB : kR + 64;
     static constexpr uint32_t kCols = FOLD ? D : 256;
-    static constexpr uint32_t kLoadBytes = (FOLD ? 2 : 3) * kTileBytes;
 };
 
 // What a block walks: the chunks of the sequence pieces in its window.
 struct Chunk {
     int n;        // sequence
     int at, end;  // first token; end of the piece (a call has less than 2^31)
+    int stop;     // end of the sequence
     int m;        // tokens of the chunk
-    bool first;       // of the piece
+    bool first;   // of the piece
     bool valid;
 };
+
+// Two float32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) { return pair(__uint_as_float(a), __uint_as_float(b)); }
+// Two values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16x2_of(uint64_t x) {
+    const float2 f = unpair(x);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(f.x, f.y);
+    uint32_t r;
+    memcpy(&r, &y, 4);
+    return r;
+}
+// The negatives of two bf16 values (a product with them is exact).
+__device__ __forceinline__ uint64_t minus_bf16x2(uint32_t x) {
+    const uint32_t n = x ^ 0x80008000u;
+    return pair(__uint_as_float(n << 16), __uint_as_float(n & 0xffff0000u));
+}
 
 template <int D, int PARTS, bool FOLD>
 __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant__ ChunkBatch batch) {
     using P = Plan<D, PARTS, FOLD>;
     extern __shared__ unsigned char s_raw[];
-    // arrivals: TMA (q and k, v), products (of the state, of the values, the
-    // update), working warps (state operand ready, the other operands ready)
-    __shared__ uint64_t s_qk, s_v, s_inter, s_values, s_update, s_state, s_ready;
+    // arrivals: TMA (q and k, v), products (of the state, the scores, of the
+    // values, the update), working warps (state operand ready and accumulator
+    // read, w V ready, scores ready)
+    __shared__ uint64_t s_qk, s_v, s_inter, s_scores, s_values, s_update, s_state, s_wv, s_ready;
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ int64_t s_count;
-    // g^n at kChunk + n, zeros below: times in_scale for the update, times
-    // both scales for the scores
-    __shared__ float s_pow_raw[2 * kChunk + 1], s_score_raw[2 * kChunk + 1];
-    __shared__ alignas(16) float s_age[kChunk];  // weight of the state before the chunk at each row
+    // weights: of the score of rows i and j at kChunk + i - j; of row j in the
+    // update after a whole chunk; of the state before the chunk at row i
+    __shared__ float s_score[2 * kChunk], s_wrow[kChunk];
+    __shared__ alignas(16) float s_age[kChunk];
     __shared__ int s_len[kRanked], s_rank;
-    float* const s_pow = s_pow_raw + kChunk;
-    float* const s_score = s_score_raw + kChunk;
     const Args& a = batch.b.a[blockIdx.z];
     const Maps& maps = batch.maps[blockIdx.z];
     unsigned char* sm = s_raw + ((1024 - (smem_addr(s_raw) & 1023)) & 1023);
@@ -143,9 +184,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             mbar_init(&s_qk, 1);
             mbar_init(&s_v, 1);
             mbar_init(&s_inter, 1);
+            mbar_init(&s_scores, 1);
             mbar_init(&s_values, 1);
             mbar_init(&s_update, 1);
             mbar_init(&s_state, kWork / kWarp);
+            mbar_init(&s_wv, kWork / kWarp);
             mbar_init(&s_ready, kWork / kWarp);
             fence_barrier_init();
             s_failed = 0;
@@ -154,15 +197,14 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             if (!FOLD) tma_prefetch_map(&maps.q);
         }
     }
-    if (tid <= 2 * kChunk) {
-        const float x = tid < kChunk ? 0.0f : decay_pow(ld, tid - kChunk) * a.in_scale;
-        s_pow_raw[tid] = x;
-        s_score_raw[tid] = x * a.out_scale;
+    if (tid < 2 * kChunk) {
+        const int gap = rev ? kChunk - tid : tid - kChunk;
+        s_score[tid] = gap < 0 ? 0.0f : decay_pow(ld, gap) * a.in_scale * a.out_scale;
     }
-    if (tid < kChunk) s_age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1) * a.out_scale;
-    if (!FOLD)  // scores after their row stay zero
-        for (int i = tid; i < kChunk * kChunk / 8; i += kMmaThreads) *reinterpret_cast<uint4*>(sm + P::kP + i * 16) = make_uint4(0, 0, 0, 0);
-    fence_async_smem();
+    if (tid < kChunk) {
+        s_age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1) * a.out_scale;
+        s_wrow[tid] = decay_pow(ld, rev ? tid + 1 : kChunk - 1 - tid) * a.in_scale;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -209,6 +251,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         c.n = n;
         c.at = begin > t0 ? begin : t0;
         c.end = end < t1 ? end : t1;
+        c.stop = end;
         c.m = c.end - c.at < kChunk ? c.end - c.at : kChunk;
         c.first = true;
         c.valid = true;
@@ -263,13 +306,13 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         const int begin = n < a.seqs ? offset(n) : t1;
         kind = begin >= t1 ? kNone : (begin >= t0 ? kFresh : kThrough);
         if (tid == 0 && h == 0) a.tail[w] = kind;
-        if (kind != kNone) c = start(n, begin, t1);
+        if (kind != kNone) c = start(n, begin, offset(n + 1));
     } else {
         c = seek(n);
     }
     // parts of w V that a chunk's terms need
     auto parts_of = [&](const Chunk& c) {
-        return PARTS == 3 && ld * (float)(offset(c.n + 1) - c.at - c.m) > -5.55f ? 3 : 2;
+        return PARTS == 3 && ld * (float)(c.stop - c.at - c.m) > -5.55f ? 3 : 2;
     };
     // where the state before a piece comes from; null: zero
     auto source = [&](const Chunk& c, bool* transposed) -> const float* {
@@ -278,7 +321,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         if (!here) return FOLD ? nullptr : a.carry + ((int64_t)w * a.heads + h) * ssize;
         if (!a.s_in) return nullptr;
         // another block may already have written this sequence's result in place
-        if (!FOLD && a.stash && c.end == t1 && offset(c.n + 1) > t1) return a.stash + ((int64_t)w * a.heads + h) * ssize;
+        if (!FOLD && a.stash && c.end < c.stop) return a.stash + ((int64_t)w * a.heads + h) * ssize;
         *transposed = a.s_in_t;
         return a.s_in + seq_state(c.n);
     };
@@ -288,9 +331,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         // copies and products
         // ------------------------------------------------------------------
         const uint32_t leader = lane == 0;
-        uint32_t qk = 0, v = 0, state = 0, ready = 0, values = 0, update = 0;
+        uint32_t qk = 0, v = 0, state = 0, inter = 0, wv = 0, ready = 0, values = 0, update = 0;
         const uint64_t dq = smem_desc(sbase + P::kQ, 16), dp = smem_desc(sbase + P::kP, 16);
-        const uint64_t dk = smem_desc(sbase + P::kK, 8192);
+        const uint64_t dkk = smem_desc(sbase + P::kK, 16), dk = smem_desc(sbase + P::kK, 8192);
         const uint64_t dv = smem_desc(sbase + P::kV, D == 128 ? 8192 : 0);
         const uint64_t dw = smem_desc(sbase + P::kW, D == 128 ? 8192 : 0);
         auto load = [&](const Chunk& c, uint64_t* bar, uint32_t expect, const CUtensorMap* map, int head, int at) {
@@ -318,29 +361,32 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                 bool t;
                 zero = source(c, &t) == nullptr;
             }
-            if (!FOLD && !zero) wait(&s_state, state);
+            if (!FOLD) wait(&s_state, state);
             wait(&s_qk, qk);
-            if (!FOLD && !zero) {
-                // S^T Q^T
+            if (!FOLD) {
                 tc_fence_after();
+                if (!zero) {
+                    // S^T Q^T
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    mma_ts(tmem + P::kR, tmem + P::kB + s * 8, dq + (((s / 4) * 8192 + (s % 4) * 32) >> 4),
-                           mma_idesc(128, 64, false, false), s > 0, leader);
-                mma_commit(&s_inter, leader);
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_ts(tmem + P::kR, tmem + P::kB + s * 8, dq + (((s / 4) * 8192 + (s % 4) * 32) >> 4),
+                               mma_idesc(128, 64, false, false), s > 0, leader);
+                    mma_commit(&s_inter, leader);
+                    if (P::kX == P::kB) wait(&s_inter, inter);  // its operand's columns are free
+                }
+                // Q K^T; rows 64..127 of M read on into the next tile and are not used
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint64_t off = ((s / 4) * 8192 + (s % 4) * 32) >> 4;
+                    mma_ss(tmem + P::kX, dq + off, dkk + off, mma_idesc(128, 64, false, false), s > 0, leader);
+                }
+                mma_commit(&s_scores, leader);
             }
             const int parts = parts_of(c);
             const Chunk c2 = next(c);
             wait(&s_v, v);
-            wait(&s_ready, ready);
+            wait(&s_wv, wv);
             tc_fence_after();
-            if (!FOLD) {
-                // V^T P^T
-#pragma unroll
-                for (int s = 0; s < kChunk / 16; ++s)
-                    mma_ss(tmem + P::kR, dv + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), s > 0, leader);
-                mma_commit(&s_values, leader);
-            }
             // S^T += (w V)^T K
 #pragma unroll
             for (int p = 0; p < PARTS; ++p)
@@ -350,13 +396,21 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                         mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dk + (s * 2048 >> 4),
                                mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
             mma_commit(&s_update, leader);
+            if (!FOLD) {
+                wait(&s_ready, ready);
+                tc_fence_after();
+                // V^T P^T
+#pragma unroll
+                for (int s = 0; s < kChunk / 16; ++s)
+                    mma_ss(tmem + P::kR, dv + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), s > 0, leader);
+                mma_commit(&s_values, leader);
+            }
             // the next chunk's tiles, each as soon as its buffer has been used
             if (c2.valid) load_q(c2);
-            if (!FOLD) wait(&s_values, values);
-            if (FOLD) wait(&s_update, update);
-            if (c2.valid) load_v(c2);
-            if (!FOLD) wait(&s_update, update);
+            wait(&s_update, update);
             if (c2.valid) load_k(c2);
+            if (!FOLD) wait(&s_values, values);
+            if (c2.valid) load_v(c2);
             zero = false;
             c = c2;
         }
@@ -365,224 +419,41 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         // elementwise work
         // ------------------------------------------------------------------
         const int row = (warp % 4) * 32 + lane;  // TMEM lane
-        const int part = warp / 4;               // which quarter of the columns
+        const int part = warp / 4;               // which half of the columns
         const int dv = row % D;                  // state column (copies at D = 64)
         const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
         const Factor whole = decay_factor(ld, kChunk);
-        uint32_t qk = 0, v = 0, inter_ = 0, values = 0, update = 0;
-        bool zero = true;
-        while (c.valid) {
-            const int m = c.m;
-            const int r0 = rev ? kChunk - m : 0;  // rows r0 .. r0 + m - 1 hold the chunk
-            if (c.first) {
-                bool tr;
-                const float* src = source(c, &tr);
-                zero = src == nullptr;
-                if (src) {
-                    // a fold ages its state once, not chunk by chunk
-                    const float age = FOLD ? decay_pow(ld, t1 - c.at) : 1.0f;
+        uint32_t qk = 0, v = 0, scores = 0, values = 0, update = 0;
+        // S before a piece; false where it is zero
+        auto load_state = [&](const Chunk& c) {
+            bool tr;
+            const float* src = source(c, &tr);
+            if (!src) return false;
+            // a fold ages its state once, not chunk by chunk
+            const float age = FOLD ? decay_pow(ld, t1 - c.at) : 1.0f;
 #pragma unroll 1
-                    for (int k0 = part * (D / 4); k0 < (part + 1) * (D / 4); k0 += 16) {
-                        uint32_t r[16];
-                        const float* p = tr ? src + dv * D + k0 : src + k0 * D + dv;
+            for (int k0 = part * (D / 2); k0 < (part + 1) * (D / 2); k0 += 16) {
+                uint32_t r[16];
+                const float* p = tr ? src + dv * D + k0 : src + k0 * D + dv;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i, p += tr ? 1 : D) r[i] = __float_as_uint(*p);
-                        if (FOLD && a.stash && row < D) {
-                            float* keep = a.stash + ((int64_t)w * a.heads + h) * ssize + k0 * D + dv;
+                for (int i = 0; i < 16; ++i, p += tr ? 1 : D) r[i] = __float_as_uint(*p);
+                if (FOLD && a.stash && row < D) {
+                    float* keep = a.stash + ((int64_t)w * a.heads + h) * ssize + k0 * D + dv;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) keep[i * D] = __uint_as_float(r[i]);
-                        }
-                        if (FOLD)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * age);
-                        tmem_st16(lanes + P::kS + k0, r);
-                    }
-                    tmem_wait_st();
+                    for (int i = 0; i < 16; ++i) keep[i * D] = __uint_as_float(r[i]);
                 }
+                if (FOLD)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * age);
+                tmem_st16(lanes + P::kS + k0, r);
             }
-            // S^T as a bf16 operand, and scaled by g^m
-            if (!FOLD && !zero) {
-                const Factor f = m == kChunk ? whole : decay_factor(ld, m);
+            tmem_wait_st();
+            return true;
+        };
+        auto store_state = [&](float* dst) {
+            if (row < D) {
 #pragma unroll 1
-                for (int k0 = part * (D / 4); k0 < (part + 1) * (D / 4); k0 += 16) {
-                    uint32_t r[16], p[8];
-                    tmem_ld16(r, lanes + P::kS + k0);
-                    tmem_wait_ld(r);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        memcpy(&p[i], &x, 4);
-                    }
-                    tmem_st8(lanes + P::kB + k0 / 2, p);
-                    if (f.hi == 1.0f) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(fmaf(__uint_as_float(r[i]), f.lo, __uint_as_float(r[i])));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f.hi);
-                    }
-                    tmem_st16(lanes + P::kS + k0, r);
-                }
-                tmem_wait_st();
-                arrive(&s_state);
-            }
-            uint32_t inter[16];
-            if (!FOLD && warp < kScoreWarps) {
-                wait(&s_qk, qk);
-                v ^= 1;
-                // Scores: 32 x 16 a warp, on register-level matrix
-                // instructions; the quarter of the tile after its rows stays
-                // zero. The way through TMEM (issue, barrier, load: about 1300
-                // cycles) would lie on the chunk's chain and wants 64 columns
-                // that are not there.
-                const int rb = (rev ? warp > 3 : warp > 1) * 32;
-                const int cb = (rev ? (warp > 3 ? warp - 2 : warp) : (warp > 1 ? warp - 2 : warp)) * 16;
-                float x[2][2][4] = {};
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t box = sbase + (s / 4) * 8192;
-                    uint32_t qa[2][4], kb[4];
-                    ldmatrix4(kb, box + P::kK + swz128(cb + lane % 8 + lane / 16 * 8, (s % 4) * 2 + lane / 8 % 2));
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        ldmatrix4(qa[u], box + P::kQ + swz128(rb + u * 16 + lane % 16, (s % 4) * 2 + lane / 16));
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) mma_16x8x16(x[u][t], qa[u], kb[2 * t], kb[2 * t + 1]);
-                    }
-                }
-                // weighted by g^(i-j); later tokens count nothing
-                const int i0 = rb + lane / 4, j0 = cb + lane % 4 * 2;
-                const int corner = rev ? j0 - i0 : i0 - j0;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int di = u * 16 + e * 8, dj = t * 8;
-                            const int gap = corner + (rev ? dj - di : di - dj), gap1 = rev ? gap + 1 : gap - 1;
-                            const float wl = s_score[gap], wh = s_score[gap1];
-                            const float lo = gap >= 0 ? x[u][t][2 * e] * wl : 0.0f;
-                            const float hi = gap1 >= 0 ? x[u][t][2 * e + 1] * wh : 0.0f;
-                            *reinterpret_cast<__nv_bfloat162*>(sm + P::kP + swz128(i0 + di, cb / 8 + t) + lane % 4 * 4) =
-                                __floats2bfloat162_rn(lo, hi);
-                        }
-            } else {
-                // w V in bf16 parts
-                constexpr int kFirst = FOLD ? 0 : kScoreWarps * kWarp, kCount = kWork - kFirst;
-                const int mine = tid - kFirst;
-                wait(&s_v, v);
-                if (m < kChunk) {
-                    // the other rows belong to other sequences: whatever they hold
-                    // (a NaN times a zero weight is a NaN) must not enter sums
-                    wait(&s_qk, qk);
-                    constexpr int kPerRow = D / 8;
-                    for (int i = mine; i < (kChunk - m) * kPerRow; i += kCount) {
-                        const int r = (rev ? 0 : m) + i / kPerRow, x = i % kPerRow;
-                        const int off = (x / 8) * 8192 + swz128(r, x % 8);
-                        *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
-                    }
-                } else {
-                    qk ^= 1;
-                }
-                const int parts = parts_of(c);
-                const float* const pw = s_pow + (rev ? 1 - r0 : m - 1);
-                const float age = FOLD ? decay_pow(ld, t1 - c.at - m) : 1.0f;
-#pragma unroll 2
-                for (int i = mine; i < kChunk * D / 8; i += kCount) {
-                    const int r = i / (D / 8), x = i % (D / 8);
-                    const int off = (x / 8) * 8192 + swz128(r, x % 8);
-                    uint4 vv = *reinterpret_cast<const uint4*>(sm + P::kV + off);
-                    if ((unsigned)(r - r0) >= (unsigned)m) vv = make_uint4(0, 0, 0, 0);
-                    const float wt = pw[rev ? r : -r] * age;
-                    const uint32_t in[4] = {vv.x, vv.y, vv.z, vv.w};
-                    uint32_t part[2][4];
-                    float rest[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float lo = __uint_as_float(in[e] << 16) * wt, hi = __uint_as_float(in[e] & 0xffff0000u) * wt;
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
-                            memcpy(&part[p][e], &y, 4);
-                            if (p == 0 || PARTS == 3) {
-                                lo -= __uint_as_float(part[p][e] << 16);
-                                hi -= __uint_as_float(part[p][e] & 0xffff0000u);
-                            }
-                        }
-                        rest[2 * e] = lo, rest[2 * e + 1] = hi;
-                    }
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        *reinterpret_cast<uint4*>(sm + P::kW + p * P::kTileBytes + off) =
-                            make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
-                    if (PARTS == 3 && parts == 3) {
-                        uint32_t last[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 y = __floats2bfloat162_rn(rest[2 * e], rest[2 * e + 1]);
-                            memcpy(&last[e], &y, 4);
-                        }
-                        *reinterpret_cast<uint4*>(sm + P::kW + 2 * P::kTileBytes + off) = make_uint4(last[0], last[1], last[2], last[3]);
-                    }
-                }
-            }
-            __syncwarp();
-            if (!FOLD && !zero) {
-                wait(&s_inter, inter_);
-                tc_fence_after();
-                if (row < D) {
-                    tmem_ld16(inter, lanes + P::kR + part * 16);
-                    tmem_wait_ld(inter);
-                }
-            }
-            arrive(&s_ready);
-            const Chunk c2 = next(c);
-            if (!FOLD) {
-                wait(&s_values, values);
-                tc_fence_after();
-                if (row < D) {
-                    bf16* const out = o + (int64_t)(low(c) + part * 16) * a.o_tok + dv;
-                    const int tok = (int)a.o_tok;
-                    uint32_t r[16];
-                    tmem_ld16(r, lanes + P::kR + part * 16);
-                    tmem_wait_ld(r);
-                    bf16 z[16];
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 g = *reinterpret_cast<const float4*>(&s_age[part * 16 + i]);
-                        const float wt[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float x = __uint_as_float(r[i + e]);
-                            if (!zero) x = fmaf(__uint_as_float(inter[i + e]), wt[e], x);
-                            z[i + e] = __float2bfloat16_rn(x);
-                        }
-                    }
-                    if (m == kChunk) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) out[(int64_t)tok * i] = z[i];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if ((unsigned)(part * 16 + i - r0) < (unsigned)m) out[(int64_t)tok * i] = z[i];
-                    }
-                }
-                __syncwarp();
-            }
-            wait(&s_update, update);  // the state is up to date; w V may be overwritten
-            tc_fence_after();
-            zero = false;
-            // the state after the piece
-            float* dst = nullptr;
-            if (c.at + m == c.end) {
-                if (FOLD) dst = a.carry + ((int64_t)w * a.heads + h) * ssize;
-                else if (a.s_out && c.end == offset(c.n + 1)) dst = a.s_out + seq_state(c.n);
-            }
-            if (dst && row < D) {
-#pragma unroll 1
-                for (int k0 = part * (D / 4); k0 < (part + 1) * (D / 4); k0 += 16) {
+                for (int k0 = part * (D / 2); k0 < (part + 1) * (D / 2); k0 += 16) {
                     uint32_t r[16];
                     tmem_ld16(r, lanes + P::kS + k0);
                     tmem_wait_ld(r);
@@ -592,6 +463,188 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                 }
             }
             __syncwarp();
+        };
+        // S^T as a bf16 operand, and scaled by g^m
+        auto pass_state = [&](int m) {
+            const Factor f = m == kChunk ? whole : decay_factor(ld, m);
+            const uint64_t lo = pair(f.lo, f.lo), hi = pair(f.hi, f.hi);
+#pragma unroll 1
+            for (int k0 = part * (D / 2); k0 < (part + 1) * (D / 2); k0 += 32) {
+                uint32_t r[32], p[16];
+                tmem_ld32(r, lanes + P::kS + k0);
+                tmem_wait_ld(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = bf16x2_of(pair_of(r[2 * i], r[2 * i + 1]));
+                tmem_st16(lanes + P::kB + k0 / 2, p);
+                if (f.hi == 1.0f) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t x = pair_of(r[2 * i], r[2 * i + 1]);
+                        const float2 y = unpair(fma2(x, lo, x));
+                        r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 y = unpair(mul2(pair_of(r[2 * i], r[2 * i + 1]), hi));
+                        r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
+                    }
+                }
+                tmem_st32(lanes + P::kS + k0, r);
+            }
+            tmem_wait_st();
+        };
+        // w V in bf16 parts: 16-byte pieces, a thread's all in one column of
+        // pieces and in rows of equal swizzle
+        constexpr int kRowStep = kWork / (D / 8);
+        const int v_row = tid / (D / 8);
+        unsigned char* const v_at = sm + P::kV + (tid % (D / 8) / 8) * 8192 + swz128(v_row, tid % 8);
+        auto split_values = [&](const Chunk& c, auto whole_chunk, auto three) {
+            constexpr bool kFull = decltype(whole_chunk)::value, kThree = decltype(three)::value;
+            const int r0 = rev ? kChunk - c.m : 0, shift = rev ? -r0 : kChunk - c.m;
+            const float age = FOLD ? decay_pow(ld, t1 - c.at - c.m) : 1.0f;
+#pragma unroll
+            for (int i = 0; i < kChunk / kRowStep; ++i) {
+                const int r = v_row + i * kRowStep;
+                uint4 in = *reinterpret_cast<const uint4*>(v_at + i * kRowStep * 128);
+                float w = s_wrow[kFull ? r : (r + shift) & (kChunk - 1)];
+                if (!kFull && (unsigned)(r - r0) >= (unsigned)c.m) in = make_uint4(0, 0, 0, 0);
+                if (FOLD) w *= age;
+                const uint64_t ww = pair(w, w);
+                uint32_t* const x = &in.x;
+                uint32_t y[2][4], z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint64_t t = mul2(pair_of(x[e] << 16, x[e] & 0xffff0000u), ww);
+                    y[0][e] = bf16x2_of(t);
+                    t = add2(t, minus_bf16x2(y[0][e]));
+                    y[1][e] = bf16x2_of(t);
+                    if (kThree) z[e] = bf16x2_of(add2(t, minus_bf16x2(y[1][e])));
+                }
+                unsigned char* const to = v_at + (P::kW - P::kV) + i * kRowStep * 128;
+                *reinterpret_cast<uint4*>(to) = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
+                *reinterpret_cast<uint4*>(to + P::kTileBytes) = make_uint4(y[1][0], y[1][1], y[1][2], y[1][3]);
+                if (kThree) *reinterpret_cast<uint4*>(to + 2 * P::kTileBytes) = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        const float* const score_at = s_score + kChunk + row - part * 32;
+        bool zero = true;
+        if (c.valid) {
+            zero = !load_state(c);
+            if (!FOLD) {
+                if (!zero) pass_state(c.m);
+                arrive(&s_state);
+            }
+        }
+        while (c.valid) {
+            const bool full = c.m == kChunk;
+            const int r0 = rev ? kChunk - c.m : 0;  // rows r0 .. r0 + m - 1 hold the chunk
+            // ---- w V ----
+            wait(&s_v, v);
+            if (full) {
+                qk ^= 1;
+                if (parts_of(c) == 3) split_values(c, Yes{}, Yes{});
+                else split_values(c, Yes{}, No{});
+            } else {
+                // the other rows belong to other sequences: whatever they hold
+                // (a NaN times a zero weight is a NaN) must not enter sums
+                wait(&s_qk, qk);
+                constexpr int kPerRow = D / 8;
+                for (int i = tid; i < (kChunk - c.m) * kPerRow; i += kWork) {
+                    const int r = (rev ? 0 : c.m) + i / kPerRow, x = i % kPerRow;
+                    const int off = (x / 8) * 8192 + swz128(r, x % 8);
+                    *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
+                }
+                if (PARTS == 3) split_values(c, No{}, Yes{});
+                else split_values(c, No{}, No{});
+            }
+            arrive(&s_wv);
+            const Chunk c2 = next(c);
+            uint32_t inter[32];
+            if (!FOLD) {
+                // ---- scores, and the state's part of the outputs ----
+                wait(&s_scores, scores);
+                tc_fence_after();
+                if (row < kChunk) {
+                    // a row, weighted by g^(i-j) (later tokens: zero)
+                    uint32_t r[32];
+                    tmem_ld32(r, lanes + P::kX + part * 32);
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = y * 8 + e * 2;
+                            const float w0 = score_at[-j], w1 = score_at[-j - 1];
+                            if (!full) {  // a masked column may hold anything
+                                if (w0 == 0.0f) r[j] = 0;
+                                if (w1 == 0.0f) r[j + 1] = 0;
+                            }
+                            p[e] = bf16x2_of(mul2(pair_of(r[j], r[j + 1]), pair(w0, w1)));
+                        }
+                        *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, part * 4 + y)) = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                }
+                if (row < D && !zero) {
+                    tmem_ld32(inter, lanes + P::kR + part * 32);
+                    tmem_wait_ld(inter);
+                }
+                arrive(&s_ready);
+            }
+            // ---- the state after the chunk; that before the next one ----
+            wait(&s_update, update);
+            tc_fence_after();
+            if (c.at + c.m == c.end) {
+                if (FOLD) store_state(a.carry + ((int64_t)w * a.heads + h) * ssize);
+                else if (a.s_out && c.end == c.stop) store_state(a.s_out + seq_state(c.n));
+            }
+            bool zero2 = false;
+            if (c2.valid && c2.first) zero2 = !load_state(c2);
+            if (!FOLD) {
+                if (c2.valid && !zero2) pass_state(c2.m);
+                // ---- outputs ----
+                wait(&s_values, values);
+                tc_fence_after();
+                uint32_t r[32];
+                if (row < D) {
+                    tmem_ld32(r, lanes + P::kR + part * 32);
+                    tmem_wait_ld(r);
+                }
+                if (c2.valid) arrive(&s_state);  // the accumulator is free
+                if (row < D) {
+                    bf16* const out = o + (int64_t)(low(c) + part * 32) * a.o_tok + dv;
+                    const int tok = (int)a.o_tok;
+                    uint32_t z[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 g = *reinterpret_cast<const float4*>(&s_age[part * 32 + i]);
+                        uint64_t x = pair_of(r[i], r[i + 1]), y = pair_of(r[i + 2], r[i + 3]);
+                        if (!zero) {
+                            x = fma2(pair_of(inter[i], inter[i + 1]), pair(g.x, g.y), x);
+                            y = fma2(pair_of(inter[i + 2], inter[i + 3]), pair(g.z, g.w), y);
+                        }
+                        z[i / 2] = bf16x2_of(x), z[i / 2 + 1] = bf16x2_of(y);
+                    }
+                    auto put = [&](int i) {
+                        const unsigned short x = (unsigned short)(i % 2 ? z[i / 2] >> 16 : z[i / 2]);
+                        *reinterpret_cast<unsigned short*>(out + (int64_t)tok * i) = x;
+                    };
+                    if (full) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) put(i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if ((unsigned)(part * 32 + i - r0) < (unsigned)c.m) put(i);
+                    }
+                }
+                __syncwarp();
+            }
+            zero = zero2;
             c = c2;
         }
     }
