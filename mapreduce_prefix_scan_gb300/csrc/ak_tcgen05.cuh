@@ -43,33 +43,33 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // 32 consecutive columns of this warp's 32 lanes (warp w of a warpgroup: lanes
 // 32 w .. 32 w + 31): thread = lane, register = column. The registers hold
 // the values only after tmem_wait_ld(r).
-__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[32], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : AK_R8(r, 0), AK_R8(r, 8), AK_R8(r, 16), AK_R8(r, 24)
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[16], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : AK_R8(r, 0), AK_R8(r, 8)
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
         AK_W8(r, 0), AK_W8(r, 8), AK_W8(r, 16), AK_W8(r, 24)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
         AK_W8(r, 0), AK_W8(r, 8)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), AK_W8(r, 0) : "memory");
 }
 // Waits for this thread's TMEM loads; the registers pass through the

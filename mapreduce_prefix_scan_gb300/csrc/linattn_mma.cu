@@ -27,8 +27,9 @@
 // 512, scores 450, the other two products 320), against 2700 that its 64 KB
 // take from HBM at an SM's share.
 //
-// Nine warps: eight do the elementwise work (on TMEM, two to a quarter of the
-// lanes, half of the columns each); the ninth issues copies and products, each as soon as its operands are there and its target
+// Seventeen warps: sixteen do the elementwise work (on TMEM, four to a
+// quarter of the lanes, a quarter of the columns each); the last issues
+// copies and products, each as soon as its operands are there and its target
 // is free. A chunk's chain is S^T Q^T, Q K^T, weights, V^T P^T; beside the
 // first two run the outputs of the chunk before and w V, beside the last the
 // state's pass for the next chunk; the update runs beside the weights, so the
@@ -41,6 +42,7 @@
 // the halves of M), lanes 64..127 hold copies.
 #include <algorithm>
 #include <atomic>
+#include <cstddef>
 #include <mutex>
 #include <cudaTypedefs.h>
 
@@ -51,8 +53,6 @@ namespace ak {
 namespace la {
 
 constexpr int kChunk = 64;
-constexpr int kWork = 256;              // threads of the working warps
-constexpr int kMmaThreads = kWork + 32;
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -66,20 +66,45 @@ struct ChunkBatch {
     uint64_t wait_limit_ns;
 };
 
+// Barriers and tables of a block.
+struct Small {
+    // arrivals: copies of q and k, of v (a stage each), products (of
+    // the state, the scores, of the values, the update), working warps (state
+    // operand ready and accumulator read, w V ready, scores ready)
+    uint64_t qk[2], v[2], inter, scores, values, update, state, wv, ready;
+    int64_t count;
+    uint32_t tmem;
+    int failed, rank;
+    // weights: of row j in the update after a whole chunk; and, which a fold
+    // pass does not have, of the state before the chunk at row i, and of the
+    // score of rows i and j at kChunk + i - j
+    float wrow[kChunk];
+    alignas(16) float age[kChunk];
+    float score[2 * kChunk];
+    int len[kRanked];
+};
+
 template <int D, int PARTS, bool FOLD>
 struct Plan {
+    static constexpr int kWork = 512;        // threads of the working warps
+    static constexpr int kThreads = kWork + 32;
+    static constexpr int kSplit = kWork / 128;             // working warps of a quarter of the lanes
+    static constexpr int kCols = kChunk / kSplit;          // accumulator columns of a thread
+    static constexpr int kStages = FOLD ? 2 : 1;           // of the key and value tiles
+    // shared memory: the tiles, then Small
     static constexpr int kTileBytes = kChunk * D * 2;
     static constexpr int kQ = 0;
     static constexpr int kK = FOLD ? 0 : kTileBytes;
-    static constexpr int kV = kK + kTileBytes;
-    static constexpr int kP = kV + kTileBytes;
+    static constexpr int kV = kK + kStages * kTileBytes;
+    static constexpr int kP = kV + kStages * kTileBytes;
     static constexpr int kW = kP + (FOLD ? 0 : kChunk * kChunk * 2);
-    static constexpr int kEnd = kW + PARTS * kTileBytes;
+    static constexpr int kSmall = kW + PARTS * kTileBytes;
+    static constexpr int kUsed = kSmall + (int)(FOLD ? offsetof(Small, age) : sizeof(Small));
     // two blocks an SM share its TMEM: no third one may become resident
-    static constexpr int kSmem = 1024 + (kEnd < 80 * 1024 && !FOLD ? 80 * 1024 : kEnd);
+    static constexpr int kSmem = kUsed < 80 * 1024 && !FOLD ? 80 * 1024 : kUsed;
     // columns: S, its bf16 form, accumulator, scores (over the bf16 form at D = 128)
     static constexpr uint32_t kS = 0, kB = D, kR = D + D / 2, kX = D == 128 ? kB : kR + 64;
-    static constexpr uint32_t kCols = FOLD ? D : 256;
+    static constexpr uint32_t kTmem = FOLD ? D : 256;
 };
 
 // What a block walks: the chunks of the sequence pieces in its window.
@@ -134,40 +159,29 @@ __device__ __forceinline__ uint64_t minus_bf16x2(uint32_t x) {
 }
 
 template <int D, int PARTS, bool FOLD>
-__global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant__ ChunkBatch batch) {
+__global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(const __grid_constant__ ChunkBatch batch) {
     using P = Plan<D, PARTS, FOLD>;
-    extern __shared__ unsigned char s_raw[];
-    // arrivals: TMA (q and k, v), products (of the state, the scores, of the
-    // values, the update), working warps (state operand ready and accumulator
-    // read, w V ready, scores ready)
-    __shared__ uint64_t s_qk, s_v, s_inter, s_scores, s_values, s_update, s_state, s_wv, s_ready;
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_failed;
-    __shared__ int64_t s_count;
-    // weights: of the score of rows i and j at kChunk + i - j; of row j in the
-    // update after a whole chunk; of the state before the chunk at row i
-    __shared__ float s_score[2 * kChunk], s_wrow[kChunk];
-    __shared__ alignas(16) float s_age[kChunk];
-    __shared__ int s_len[kRanked], s_rank;
+    constexpr int kWork = P::kWork, kMmaThreads = P::kThreads, kSplit = P::kSplit, kCols = P::kCols;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Small& t = *reinterpret_cast<Small*>(sm + P::kSmall);
     const Args& a = batch.b.a[blockIdx.z];
     const Maps& maps = batch.maps[blockIdx.z];
-    unsigned char* sm = s_raw + ((1024 - (smem_addr(s_raw) & 1023)) & 1023);
     const uint32_t sbase = smem_addr(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
     const int h = blockIdx.x;
     int w = blockIdx.y;
-    if (a.by_seq && a.seqs <= kRanked) {
+    if (!FOLD && a.by_seq && a.seqs <= kRanked) {
         // block w takes the w-th longest sequence: the long ones start first
-        for (int i = tid; i < a.seqs; i += kMmaThreads) s_len[i] = (int)(offset_at(a, i + 1) - offset_at(a, i));
+        for (int i = tid; i < a.seqs; i += kMmaThreads) t.len[i] = (int)(offset_at(a, i + 1) - offset_at(a, i));
         __syncthreads();
         for (int i = tid; i < a.seqs; i += kMmaThreads) {
-            const int mine = s_len[i];
+            const int mine = t.len[i];
             int rank = 0;
-            for (int j = 0; j < a.seqs; ++j) rank += s_len[j] > mine || (s_len[j] == mine && j < i);
-            if (rank == w) s_rank = i;
+            for (int j = 0; j < a.seqs; ++j) rank += t.len[j] > mine || (t.len[j] == mine && j < i);
+            if (rank == w) t.rank = i;
         }
         __syncthreads();
-        w = s_rank;
+        w = t.rank;
     }
     int t0, t1;
     {
@@ -179,48 +193,53 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
     const bool rev = a.reverse;
 
     if (warp == kWork / kWarp) {
-        tmem_alloc(&s_tmem, P::kCols);
+        tmem_alloc(&t.tmem, P::kTmem);
         if (lane == 0) {
-            mbar_init(&s_qk, 1);
-            mbar_init(&s_v, 1);
-            mbar_init(&s_inter, 1);
-            mbar_init(&s_scores, 1);
-            mbar_init(&s_values, 1);
-            mbar_init(&s_update, 1);
-            mbar_init(&s_state, kWork / kWarp);
-            mbar_init(&s_wv, kWork / kWarp);
-            mbar_init(&s_ready, kWork / kWarp);
+            for (int i = 0; i < P::kStages; ++i) {
+                mbar_init(&t.qk[i], 1);
+                mbar_init(&t.v[i], 1);
+            }
+            mbar_init(&t.inter, 1);
+            mbar_init(&t.scores, 1);
+            mbar_init(&t.values, 1);
+            mbar_init(&t.update, 1);
+            mbar_init(&t.state, kWork / kWarp);
+            mbar_init(&t.wv, kWork / kWarp);
+            mbar_init(&t.ready, kWork / kWarp);
             fence_barrier_init();
-            s_failed = 0;
+            t.failed = 0;
             tma_prefetch_map(&maps.k);
             tma_prefetch_map(&maps.v);
             if (!FOLD) tma_prefetch_map(&maps.q);
         }
     }
-    if (tid < 2 * kChunk) {
+    if (!FOLD && tid < 2 * kChunk) {
         const int gap = rev ? kChunk - tid : tid - kChunk;
-        s_score[tid] = gap < 0 ? 0.0f : decay_pow(ld, gap) * a.in_scale * a.out_scale;
+        t.score[tid] = gap < 0 ? 0.0f : decay_pow(ld, gap) * a.in_scale * a.out_scale;
     }
     if (tid < kChunk) {
-        s_age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1) * a.out_scale;
-        s_wrow[tid] = decay_pow(ld, rev ? tid + 1 : kChunk - 1 - tid) * a.in_scale;
+        if (!FOLD) t.age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1) * a.out_scale;
+        t.wrow[tid] = decay_pow(ld, rev ? tid + 1 : kChunk - 1 - tid) * a.in_scale;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, t.tmem, 0);
 
     // Bounded waits: a warp that gives up records it; all skip their further
     // waits and leave by the ordinary way.
-    auto wait = [&](uint64_t* bar, uint32_t& phase) {
-        if (!mbar_try_wait(bar, phase) && !*(volatile int*)&s_failed) {
+    auto wait_at = [&](uint64_t* bar, uint32_t phase) {
+        if (!mbar_try_wait(bar, phase) && !*(volatile int*)&t.failed) {
             if (!mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) {
-                *(volatile int*)&s_failed = 1;
+                *(volatile int*)&t.failed = 1;
                 if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
             }
         }
-        phase ^= 1;
         __syncwarp();  // whole warps go on to the tensor-memory instructions
+    };
+    auto wait = [&](uint64_t* bar, uint32_t& phase) {
+        wait_at(bar, phase);
+        phase ^= 1;
     };
     // A working warp is done with a step: its shared-memory and tensor-memory
     // accesses come before what the issuing warp does next.
@@ -243,7 +262,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
     // tokens of no sequence get zeros
     auto blank = [&](int from, int to) {
         if (!FOLD && writer)
-            for (int t = from + tid / D; t < to; t += kWork / D) o[(int64_t)addr(t) * a.o_tok + tid % D] = __float2bfloat16_rn(0.0f);
+            for (int x = from + tid / D; x < to; x += kWork / D) o[(int64_t)addr(x) * a.o_tok + tid % D] = __float2bfloat16_rn(0.0f);
     };
     int covered = t0;
     auto start = [&](int n, int begin, int end) {
@@ -298,7 +317,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         return x;
     };
 
-    int n = (int)first_sequence<kMmaThreads>(a, w, t0, &s_count);
+    int n = (int)first_sequence<kMmaThreads>(a, w, t0, &t.count);
     Chunk c = {};
     int32_t kind = kNone;
     if (FOLD) {
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         // copies and products
         // ------------------------------------------------------------------
         const uint32_t leader = lane == 0;
-        uint32_t qk = 0, v = 0, state = 0, inter = 0, wv = 0, ready = 0, values = 0, update = 0;
+        uint32_t stage = 0, phase = 0, state = 0, inter = 0, wv = 0, ready = 0, values = 0, update = 0;
         const uint64_t dq = smem_desc(sbase + P::kQ, 16), dp = smem_desc(sbase + P::kP, 16);
         const uint64_t dkk = smem_desc(sbase + P::kK, 16), dk = smem_desc(sbase + P::kK, 8192);
         const uint64_t dv = smem_desc(sbase + P::kV, D == 128 ? 8192 : 0);
@@ -345,24 +364,26 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             __syncwarp();
         };
         // q announces its own bytes and those of k, which comes later
-        auto load_q = [&](const Chunk& c) {
-            if (!FOLD) load(c, &s_qk, 2 * P::kTileBytes, &maps.q, maps.q_h, P::kQ);
+        auto load_q = [&](const Chunk& c) { load(c, &t.qk[0], 2 * P::kTileBytes, &maps.q, maps.q_h, P::kQ); };
+        auto load_k = [&](const Chunk& c, int st) {
+            load(c, &t.qk[st], FOLD ? P::kTileBytes : 0, &maps.k, maps.k_h, P::kK + st * P::kTileBytes);
         };
-        auto load_k = [&](const Chunk& c) { load(c, &s_qk, FOLD ? P::kTileBytes : 0, &maps.k, maps.k_h, P::kK); };
-        auto load_v = [&](const Chunk& c) { load(c, &s_v, P::kTileBytes, &maps.v, maps.v_h, P::kV); };
+        auto load_v = [&](const Chunk& c, int st) {
+            load(c, &t.v[st], P::kTileBytes, &maps.v, maps.v_h, P::kV + st * P::kTileBytes);
+        };
         if (c.valid) {
-            load_v(c);
-            load_q(c);
-            load_k(c);
+            load_v(c, 0);
+            if (!FOLD) load_q(c);
+            load_k(c, 0);
         }
         bool zero = true;
         while (c.valid) {
             if (c.first) {
-                bool t;
-                zero = source(c, &t) == nullptr;
+                bool tr;
+                zero = source(c, &tr) == nullptr;
             }
-            if (!FOLD) wait(&s_state, state);
-            wait(&s_qk, qk);
+            if (!FOLD) wait(&t.state, state);
+            wait_at(&t.qk[stage], phase);
             if (!FOLD) {
                 tc_fence_after();
                 if (!zero) {
@@ -371,8 +392,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                     for (int s = 0; s < D / 16; ++s)
                         mma_ts(tmem + P::kR, tmem + P::kB + s * 8, dq + (((s / 4) * 8192 + (s % 4) * 32) >> 4),
                                mma_idesc(128, 64, false, false), s > 0, leader);
-                    mma_commit(&s_inter, leader);
-                    if (P::kX == P::kB) wait(&s_inter, inter);  // its operand's columns are free
+                    mma_commit(&t.inter, leader);
+                    if (P::kX == P::kB) wait(&t.inter, inter);  // its operand's columns are free
                 }
                 // Q K^T; rows 64..127 of M read on into the next tile and are not used
 #pragma unroll
@@ -380,12 +401,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                     const uint64_t off = ((s / 4) * 8192 + (s % 4) * 32) >> 4;
                     mma_ss(tmem + P::kX, dq + off, dkk + off, mma_idesc(128, 64, false, false), s > 0, leader);
                 }
-                mma_commit(&s_scores, leader);
+                mma_commit(&t.scores, leader);
             }
             const int parts = parts_of(c);
             const Chunk c2 = next(c);
-            wait(&s_v, v);
-            wait(&s_wv, wv);
+            if (FOLD && c2.valid) {  // the other stage was used up with the update before
+                load_v(c2, stage ^ 1);
+                load_k(c2, stage ^ 1);
+            }
+            wait_at(&t.v[stage], phase);
+            wait(&t.wv, wv);
             tc_fence_after();
             // S^T += (w V)^T K
 #pragma unroll
@@ -393,24 +418,28 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                 if (p < 2 || parts == 3)
 #pragma unroll
                     for (int s = 0; s < kChunk / 16; ++s)
-                        mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dk + (s * 2048 >> 4),
+                        mma_ss(tmem + P::kS, dw + ((p * P::kTileBytes + s * 2048) >> 4), dk + ((stage * P::kTileBytes + s * 2048) >> 4),
                                mma_idesc(128, D, true, true), !zero || p > 0 || s > 0, leader);
-            mma_commit(&s_update, leader);
+            mma_commit(&t.update, leader);
             if (!FOLD) {
-                wait(&s_ready, ready);
+                wait(&t.ready, ready);
                 tc_fence_after();
                 // V^T P^T
 #pragma unroll
                 for (int s = 0; s < kChunk / 16; ++s)
                     mma_ss(tmem + P::kR, dv + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), s > 0, leader);
-                mma_commit(&s_values, leader);
+                mma_commit(&t.values, leader);
             }
             // the next chunk's tiles, each as soon as its buffer has been used
-            if (c2.valid) load_q(c2);
-            wait(&s_update, update);
-            if (c2.valid) load_k(c2);
-            if (!FOLD) wait(&s_values, values);
-            if (c2.valid) load_v(c2);
+            if (!FOLD && c2.valid) load_q(c2);
+            wait(&t.update, update);
+            if (!FOLD) {
+                if (c2.valid) load_k(c2, 0);
+                wait(&t.values, values);
+                if (c2.valid) load_v(c2, 0);
+            }
+            if (P::kStages == 2) stage ^= 1;
+            if (stage == 0) phase ^= 1;
             zero = false;
             c = c2;
         }
@@ -419,11 +448,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         // elementwise work
         // ------------------------------------------------------------------
         const int row = (warp % 4) * 32 + lane;  // TMEM lane
-        const int part = warp / 4;               // which half of the columns
+        const int part = warp / 4;               // which quarter of the columns
         const int dv = row % D;                  // state column (copies at D = 64)
         const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
         const Factor whole = decay_factor(ld, kChunk);
-        uint32_t qk = 0, v = 0, scores = 0, values = 0, update = 0;
+        uint32_t stage = 0, phase = 0, scores = 0, values = 0, update = 0;
         // S before a piece; false where it is zero
         auto load_state = [&](const Chunk& c) {
             bool tr;
@@ -432,7 +461,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             // a fold ages its state once, not chunk by chunk
             const float age = FOLD ? decay_pow(ld, t1 - c.at) : 1.0f;
 #pragma unroll 1
-            for (int k0 = part * (D / 2); k0 < (part + 1) * (D / 2); k0 += 16) {
+            for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += 16) {
                 uint32_t r[16];
                 const float* p = tr ? src + dv * D + k0 : src + k0 * D + dv;
 #pragma unroll
@@ -445,7 +474,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                 if (FOLD)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * age);
-                tmem_st16(lanes + P::kS + k0, r);
+                tmem_st(lanes + P::kS + k0, r);
             }
             tmem_wait_st();
             return true;
@@ -453,9 +482,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         auto store_state = [&](float* dst) {
             if (row < D) {
 #pragma unroll 1
-                for (int k0 = part * (D / 2); k0 < (part + 1) * (D / 2); k0 += 16) {
+                for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += 16) {
                     uint32_t r[16];
-                    tmem_ld16(r, lanes + P::kS + k0);
+                    tmem_ld(r, lanes + P::kS + k0);
                     tmem_wait_ld(r);
                     float* to = dst + k0 * D + dv;
 #pragma unroll
@@ -468,29 +497,30 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         auto pass_state = [&](int m) {
             const Factor f = m == kChunk ? whole : decay_factor(ld, m);
             const uint64_t lo = pair(f.lo, f.lo), hi = pair(f.hi, f.hi);
+            constexpr int N = D / kSplit < kCols ? D / kSplit : kCols;
 #pragma unroll 1
-            for (int k0 = part * (D / 2); k0 < (part + 1) * (D / 2); k0 += 32) {
-                uint32_t r[32], p[16];
-                tmem_ld32(r, lanes + P::kS + k0);
+            for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += N) {
+                uint32_t r[N], p[N / 2];
+                tmem_ld(r, lanes + P::kS + k0);
                 tmem_wait_ld(r);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = bf16x2_of(pair_of(r[2 * i], r[2 * i + 1]));
-                tmem_st16(lanes + P::kB + k0 / 2, p);
+                for (int i = 0; i < N / 2; ++i) p[i] = bf16x2_of(pair_of(r[2 * i], r[2 * i + 1]));
+                tmem_st(lanes + P::kB + k0 / 2, p);
                 if (f.hi == 1.0f) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < N / 2; ++i) {
                         const uint64_t x = pair_of(r[2 * i], r[2 * i + 1]);
                         const float2 y = unpair(fma2(x, lo, x));
                         r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < N / 2; ++i) {
                         const float2 y = unpair(mul2(pair_of(r[2 * i], r[2 * i + 1]), hi));
                         r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
                     }
                 }
-                tmem_st32(lanes + P::kS + k0, r);
+                tmem_st(lanes + P::kS + k0, r);
             }
             tmem_wait_st();
         };
@@ -506,8 +536,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
 #pragma unroll
             for (int i = 0; i < kChunk / kRowStep; ++i) {
                 const int r = v_row + i * kRowStep;
-                uint4 in = *reinterpret_cast<const uint4*>(v_at + i * kRowStep * 128);
-                float w = s_wrow[kFull ? r : (r + shift) & (kChunk - 1)];
+                uint4 in = *reinterpret_cast<const uint4*>(v_at + stage * P::kTileBytes + i * kRowStep * 128);
+                float w = t.wrow[kFull ? r : (r + shift) & (kChunk - 1)];
                 if (!kFull && (unsigned)(r - r0) >= (unsigned)c.m) in = make_uint4(0, 0, 0, 0);
                 if (FOLD) w *= age;
                 const uint64_t ww = pair(w, w);
@@ -515,11 +545,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                 uint32_t y[2][4], z[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    uint64_t t = mul2(pair_of(x[e] << 16, x[e] & 0xffff0000u), ww);
-                    y[0][e] = bf16x2_of(t);
-                    t = add2(t, minus_bf16x2(y[0][e]));
-                    y[1][e] = bf16x2_of(t);
-                    if (kThree) z[e] = bf16x2_of(add2(t, minus_bf16x2(y[1][e])));
+                    uint64_t wv = mul2(pair_of(x[e] << 16, x[e] & 0xffff0000u), ww);
+                    y[0][e] = bf16x2_of(wv);
+                    wv = add2(wv, minus_bf16x2(y[0][e]));
+                    y[1][e] = bf16x2_of(wv);
+                    if (kThree) z[e] = bf16x2_of(add2(wv, minus_bf16x2(y[1][e])));
                 }
                 unsigned char* const to = v_at + (P::kW - P::kV) + i * kRowStep * 128;
                 *reinterpret_cast<uint4*>(to) = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
@@ -529,52 +559,51 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
         };
         using Yes = std::true_type;
         using No = std::false_type;
-        const float* const score_at = s_score + kChunk + row - part * 32;
+        const float* const score_at = t.score + kChunk + row - part * kCols;
         bool zero = true;
         if (c.valid) {
             zero = !load_state(c);
             if (!FOLD) {
                 if (!zero) pass_state(c.m);
-                arrive(&s_state);
+                arrive(&t.state);
             }
         }
         while (c.valid) {
             const bool full = c.m == kChunk;
             const int r0 = rev ? kChunk - c.m : 0;  // rows r0 .. r0 + m - 1 hold the chunk
             // ---- w V ----
-            wait(&s_v, v);
+            wait_at(&t.v[stage], phase);
             if (full) {
-                qk ^= 1;
                 if (parts_of(c) == 3) split_values(c, Yes{}, Yes{});
                 else split_values(c, Yes{}, No{});
             } else {
                 // the other rows belong to other sequences: whatever they hold
                 // (a NaN times a zero weight is a NaN) must not enter sums
-                wait(&s_qk, qk);
+                wait_at(&t.qk[stage], phase);
                 constexpr int kPerRow = D / 8;
                 for (int i = tid; i < (kChunk - c.m) * kPerRow; i += kWork) {
                     const int r = (rev ? 0 : c.m) + i / kPerRow, x = i % kPerRow;
                     const int off = (x / 8) * 8192 + swz128(r, x % 8);
-                    *reinterpret_cast<uint4*>(sm + P::kK + off) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(sm + P::kV + off) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(sm + P::kK + stage * P::kTileBytes + off) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(sm + P::kV + stage * P::kTileBytes + off) = make_uint4(0, 0, 0, 0);
                 }
                 if (PARTS == 3) split_values(c, No{}, Yes{});
                 else split_values(c, No{}, No{});
             }
-            arrive(&s_wv);
+            arrive(&t.wv);
             const Chunk c2 = next(c);
-            uint32_t inter[32];
+            uint32_t inter[kCols];
             if (!FOLD) {
                 // ---- scores, and the state's part of the outputs ----
-                wait(&s_scores, scores);
+                wait(&t.scores, scores);
                 tc_fence_after();
                 if (row < kChunk) {
                     // a row, weighted by g^(i-j) (later tokens: zero)
-                    uint32_t r[32];
-                    tmem_ld32(r, lanes + P::kX + part * 32);
+                    uint32_t r[kCols];
+                    tmem_ld(r, lanes + P::kX + part * kCols);
                     tmem_wait_ld(r);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
+                    for (int y = 0; y < kCols / 8; ++y) {
                         uint32_t p[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -586,17 +615,17 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                             }
                             p[e] = bf16x2_of(mul2(pair_of(r[j], r[j + 1]), pair(w0, w1)));
                         }
-                        *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, part * 4 + y)) = make_uint4(p[0], p[1], p[2], p[3]);
+                        *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, part * (kCols / 8) + y)) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
                 }
-                if (row < D && !zero) {
-                    tmem_ld32(inter, lanes + P::kR + part * 32);
+                if (!zero) {
+                    tmem_ld(inter, lanes + P::kR + part * kCols);
                     tmem_wait_ld(inter);
                 }
-                arrive(&s_ready);
+                arrive(&t.ready);
             }
             // ---- the state after the chunk; that before the next one ----
-            wait(&s_update, update);
+            wait(&t.update, update);
             tc_fence_after();
             if (c.at + c.m == c.end) {
                 if (FOLD) store_state(a.carry + ((int64_t)w * a.heads + h) * ssize);
@@ -607,21 +636,19 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
             if (!FOLD) {
                 if (c2.valid && !zero2) pass_state(c2.m);
                 // ---- outputs ----
-                wait(&s_values, values);
+                wait(&t.values, values);
                 tc_fence_after();
-                uint32_t r[32];
+                uint32_t r[kCols];
+                tmem_ld(r, lanes + P::kR + part * kCols);
+                tmem_wait_ld(r);
+                if (c2.valid) arrive(&t.state);  // the accumulator is free
                 if (row < D) {
-                    tmem_ld32(r, lanes + P::kR + part * 32);
-                    tmem_wait_ld(r);
-                }
-                if (c2.valid) arrive(&s_state);  // the accumulator is free
-                if (row < D) {
-                    bf16* const out = o + (int64_t)(low(c) + part * 32) * a.o_tok + dv;
+                    bf16* const out = o + (int64_t)(low(c) + part * kCols) * a.o_tok + dv;
                     const int tok = (int)a.o_tok;
-                    uint32_t z[16];
+                    uint32_t z[kCols / 2];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 g = *reinterpret_cast<const float4*>(&s_age[part * 32 + i]);
+                    for (int i = 0; i < kCols; i += 4) {
+                        const float4 g = *reinterpret_cast<const float4*>(&t.age[part * kCols + i]);
                         uint64_t x = pair_of(r[i], r[i + 1]), y = pair_of(r[i + 2], r[i + 3]);
                         if (!zero) {
                             x = fma2(pair_of(inter[i], inter[i + 1]), pair(g.x, g.y), x);
@@ -635,15 +662,17 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
                     };
                     if (full) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) put(i);
+                        for (int i = 0; i < kCols; ++i) put(i);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if ((unsigned)(part * 32 + i - r0) < (unsigned)c.m) put(i);
+                        for (int i = 0; i < kCols; ++i)
+                            if ((unsigned)(part * kCols + i - r0) < (unsigned)c.m) put(i);
                     }
                 }
                 __syncwarp();
             }
+            if (P::kStages == 2) stage ^= 1;
+            if (stage == 0) phase ^= 1;
             zero = zero2;
             c = c2;
         }
@@ -651,7 +680,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_chunks(const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWork / kWarp) tmem_free(tmem, P::kCols);
+    if (warp == kWork / kWarp) tmem_free(tmem, P::kTmem);
 }
 
 // ---------------------------------------------------------------------------
@@ -709,7 +738,7 @@ static ak_status launch(const ChunkBatch& c, cudaStream_t stream) {
     }
     const Args& a = c.b.a[0];
     const dim3 grid((unsigned)a.heads, (unsigned)a.windows, (unsigned)c.b.count);
-    k_chunks<D, PARTS, FOLD><<<grid, kMmaThreads, smem, stream>>>(c);
+    k_chunks<D, PARTS, FOLD><<<grid, Plan<D, PARTS, FOLD>::kThreads, smem, stream>>>(c);
     count_launches(1);
     return check_launch();
 }
