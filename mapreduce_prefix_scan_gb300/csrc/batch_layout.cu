@@ -22,6 +22,7 @@
 // Bound by latency (a launch, two dependent loads, the block scan), and by
 // the 16 bytes written per token once there are millions of them.
 #include <algorithm>
+#include <atomic>
 
 #include "ak_common.cuh"
 #include "ak_internal.h"
@@ -98,10 +99,11 @@ __device__ __forceinline__ int64_t slot_of(const LayoutCall& c, int64_t r, int p
     return id < 0 ? -1 : (int64_t)id * b + (pos - col * b);
 }
 
-// Tokens [first, last) of the token axis, kTok a thread. Off / Base: prefix
-// arrays over the requests (shared or global memory).
-__device__ __forceinline__ void expand(const LayoutCall& c, const int32_t* off, const int32_t* base, int64_t first,
-                                       int64_t last) {
+// Tokens [first, last) of the token axis, kTok a thread. off, base: prefix
+// arrays over the requests; ctx_of: their cached lengths (shared or global
+// memory).
+__device__ __forceinline__ void expand(const LayoutCall& c, const int32_t* off, const int32_t* base,
+                                       const int32_t* ctx_of, int64_t first, int64_t last) {
     const int64_t n = c.nreq;
     const int64_t total = off[n];
     for (int64_t t0 = first + (int64_t)threadIdx.x * kTok; t0 < last; t0 += (int64_t)kThreads * kTok) {
@@ -130,7 +132,7 @@ __device__ __forceinline__ void expand(const LayoutCall& c, const int32_t* off, 
                 while (r + 1 < n && off[r + 1] <= t) ++r;
                 if (r != held) {
                     held = r;
-                    ctx = max(c.ctx_lens[r], 0);
+                    ctx = max(ctx_of[r], 0);
                     have = (int)(((int64_t)ctx + c.block_size - 1) / c.block_size);
                     start = off[r];
                     bs = (uint32_t)base[r];
@@ -155,19 +157,20 @@ __device__ __forceinline__ void expand(const LayoutCall& c, const int32_t* off, 
     }
 }
 
-// Scans requests [first, first + kSmallReqs) (kPer a thread); off and base
-// receive the prefixes at `at0 + request`. Returns this thread's inclusive
-// sum after its last request.
-__device__ __forceinline__ uint64_t scan_tile(const LayoutCall& c, int64_t first, uint64_t carry, int32_t* off,
-                                              int32_t* base, uint64_t* s_warp) {
+// Scans requests [first, first + kThreads * per), per <= kPer of them a
+// thread; off and base receive the prefixes, keep_ctx (where given) the
+// cached lengths. Returns this thread's inclusive sum after its last request.
+__device__ __forceinline__ uint64_t scan_tile(const LayoutCall& c, int64_t first, int per, uint64_t carry, int32_t* off,
+                                              int32_t* base, int32_t* keep_ctx, uint64_t* s_warp) {
     uint64_t v[kPer], sum = 0;
-    const int64_t r0 = first + (int64_t)threadIdx.x * kPer;
+    const int64_t r0 = first + (int64_t)threadIdx.x * per;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         v[i] = 0;
-        if (r0 + i < c.nreq) {
+        if (i < per && r0 + i < c.nreq) {
             const Req q = request(c, r0 + i);
             v[i] = pack((uint32_t)q.fresh, (uint32_t)(q.want - q.have));
+            if (keep_ctx) keep_ctx[r0 + i] = q.ctx;
         }
         sum += v[i];
     }
@@ -175,7 +178,7 @@ __device__ __forceinline__ uint64_t scan_tile(const LayoutCall& c, int64_t first
     uint64_t run = incl - sum;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (r0 + i < c.nreq && off) {
+        if (i < per && r0 + i < c.nreq && off) {
             off[r0 + i] = (int32_t)(uint32_t)run;
             base[r0 + i] = (int32_t)(run >> 32);
         }
@@ -186,11 +189,12 @@ __device__ __forceinline__ uint64_t scan_tile(const LayoutCall& c, int64_t first
 
 __global__ void __launch_bounds__(kThreads) k_layout_small(const LayoutCall c) {
     __shared__ uint64_t s_warp[kThreads / kWarp];
-    extern __shared__ int32_t s_pre[];  // off[nreq + 1], base[nreq + 1]
+    extern __shared__ int32_t s_pre[];  // off[nreq + 1], base[nreq + 1], ctx[nreq]
     const int n = (int)c.nreq;
     int32_t* off = s_pre;
-    int32_t* base = s_pre + n + 1;
-    const uint64_t incl = scan_tile(c, 0, 0, off, base, s_warp);
+    int32_t* base = off + n + 1;
+    int32_t* ctx = base + n + 1;
+    const uint64_t incl = scan_tile(c, 0, (n + kThreads - 1) / kThreads, 0, off, base, ctx, s_warp);
     if (threadIdx.x == kThreads - 1) {
         off[n] = (int32_t)(uint32_t)incl;
         base[n] = (int32_t)(incl >> 32);
@@ -211,12 +215,12 @@ __global__ void __launch_bounds__(kThreads) k_layout_small(const LayoutCall c) {
         append(c, r, q, (uint32_t)base[r], threadIdx.x % G, G);
     }
     const int64_t first = (int64_t)blockIdx.x * c.tokens_per_block;
-    expand(c, off, base, first, min(first + c.tokens_per_block, c.max_tokens));
+    expand(c, off, base, ctx, first, min(first + c.tokens_per_block, c.max_tokens));
 }
 
 __global__ void __launch_bounds__(kThreads) k_layout_sums(const LayoutCall c) {
     __shared__ uint64_t s_warp[kThreads / kWarp];
-    const uint64_t incl = scan_tile(c, (int64_t)blockIdx.x * kSmallReqs, 0, nullptr, nullptr, s_warp);
+    const uint64_t incl = scan_tile(c, (int64_t)blockIdx.x * kSmallReqs, kPer, 0, nullptr, nullptr, nullptr, s_warp);
     if (threadIdx.x == kThreads - 1) c.tile_sums[blockIdx.x] = incl;
 }
 
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) k_layout_prefix(const LayoutCall c) 
     if (threadIdx.x == kThreads - 1) s_carry = v;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * kSmallReqs;
-    const uint64_t incl = scan_tile(c, first, s_carry, c.offsets, c.base, s_warp);
+    const uint64_t incl = scan_tile(c, first, kPer, s_carry, c.offsets, c.base, nullptr, s_warp);
     if (blockIdx.x == gridDim.x - 1 && threadIdx.x == kThreads - 1) {
         c.offsets[c.nreq] = (int32_t)(uint32_t)incl;
         c.counts[0] = (int32_t)(uint32_t)incl;
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) k_layout_prefix(const LayoutCall c) 
 
 __global__ void __launch_bounds__(kThreads) k_layout_expand(const LayoutCall c) {
     const int64_t first = (int64_t)blockIdx.x * c.tokens_per_block;
-    expand(c, c.offsets, c.base, first, min(first + c.tokens_per_block, c.max_tokens));
+    expand(c, c.offsets, c.base, c.ctx_lens, first, min(first + c.tokens_per_block, c.max_tokens));
 }
 
 }  // namespace bl
@@ -265,7 +269,14 @@ ak_status run_layout(LayoutCall c, void* ws, cudaStream_t stream) {
     int64_t grid = std::max<int64_t>(1, std::min<int64_t>((c.max_tokens + per - 1) / per, 2 * dev.sm_count));
     c.tokens_per_block = align_up((size_t)((c.max_tokens + grid - 1) / grid), kTok);
     if (c.nreq <= kSmallReqs) {
-        const size_t smem = 2 * ((size_t)c.nreq + 1) * 4;
+        const size_t smem = (3 * (size_t)c.nreq + 2) * 4;
+        static std::atomic<uint64_t> ready{0};
+        if (smem > 40 * 1024 && !(ready.load() >> dev.device & 1)) {
+            const cudaError_t e = cudaFuncSetAttribute(k_layout_small, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (3 * kSmallReqs + 2) * 4);
+            if (e != cudaSuccess) return cuda_fail(e);
+            ready.fetch_or(1ull << dev.device);
+        }
         k_layout_small<<<(unsigned)grid, kThreads, smem, stream>>>(c);
         count_launches(1);
         return check_launch();

@@ -23,8 +23,9 @@ __device__ __forceinline__ T from_f(float v) {
 // A block holds 32 columns of the state of one head: 4 groups of DK / 4 rows
 // x 32 columns, a column's rows of a group in one thread's registers, so the
 // state is read and written once a sequence piece. k, q and v of kTile tokens
-// are staged in shared memory (k and q are read as 16-byte broadcasts); the
-// groups' parts of each output are added in shared memory once a tile.
+// pass through registers into shared memory, the next tile's loads in flight
+// while one is worked on (k and q are read as 16-byte broadcasts); the groups'
+// parts of each output are added in shared memory once a tile.
 //
 // The decay leaves the inner loop: with X = g S before a block of b tokens,
 //   S_e = g^e (X + sum_{j<=e} g^-j k_j v_j^T),  e = 0 .. b - 1,
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
     constexpr int R = DK / kGroups;
     __shared__ alignas(16) float s_k[kTile][DK]; __shared__ alignas(16) float s_q[FOLD ? 1 : kTile][FOLD ? 4 : DK];
     __shared__ float s_v[kTile][32];
-    __shared__ float s_w[kTile];  // g^e of each token, times the output's scale
+    __shared__ float s_w[kTile], s_inv[kTile];  // g^e of each token times the output's scale, g^-e times the input's
     __shared__ float s_o[FOLD ? 1 : kTile][kGroups][32];
     __shared__ int64_t s_count;
     const int col = threadIdx.x % 32, grp = threadIdx.x / 32;
@@ -92,33 +93,51 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
         const int64_t m = a.reverse ? a.seqs - 1 - n : n;
         return (m * a.heads + h) * ssize;
     };
+    if (threadIdx.x < kTile) {
+        const int e = threadIdx.x & (block - 1);
+        s_w[threadIdx.x] = decay_pow(ld, e) * a.out_scale;
+        s_inv[threadIdx.x] = decay_pow(ld, -e) * a.in_scale;
+    }
     // tokens [from, to) of one sequence
+    constexpr int kLoads = kTile * DK / kThreads, kLoadsV = kTile * 32 / kThreads;
+    float fk[kLoads], fq[FOLD ? 1 : kLoads], fv[kLoadsV];
+    auto fetch = [&](int64_t tb, int m) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int x = threadIdx.x + i * kThreads, t = x / DK, r = x % DK;
+            const bool in = t < m && r < a.dk;
+            fk[i] = in ? as_f(k[addr(tb + t) * a.k_tok + r]) : 0.0f;
+            if (!FOLD) fq[i] = in ? as_f(q[addr(tb + t) * a.q_tok + r]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoadsV; ++i) {
+            const int t = grp + i * kGroups;
+            fv[i] = t < m && live ? as_f(v[addr(tb + t) * a.v_tok + c0 + col]) : 0.0f;
+        }
+    };
     auto walk = [&](int64_t from, int64_t to) {
         if (!a.reverse) {
             const Factor one = decay_factor(ld, 1);
 #pragma unroll
             for (int i = 0; i < R; ++i) s[i] = s[i] * one;
         }
+        fetch(from, (int)(to - from < kTile ? to - from : kTile));
         for (int64_t tb = from; tb < to; tb += kTile) {
             const int m = (int)(to - tb < kTile ? to - tb : kTile);
             __syncthreads();
-            for (int i = threadIdx.x; i < kTile * DK; i += kThreads) {
-                const int t = i / DK, r = i % DK;
-                const bool in = t < m && r < a.dk;
-                s_k[t][r] = in ? as_f(k[addr(tb + t) * a.k_tok + r]) : 0.0f;
-                if (!FOLD) s_q[t][r] = in ? as_f(q[addr(tb + t) * a.q_tok + r]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int x = threadIdx.x + i * kThreads;
+                s_k[x / DK][x % DK] = fk[i];
+                if (!FOLD) s_q[x / DK][x % DK] = fq[i];
             }
-            for (int i = threadIdx.x; i < kTile * 32; i += kThreads) {
-                const int t = i / 32, c = i % 32;
-                s_v[t][c] = t < m && c0 + c < a.dv
-                                ? as_f(v[addr(tb + t) * a.v_tok + c0 + c]) * (a.in_scale * decay_pow(ld, -(t & (block - 1))))
-                                : 0.0f;
-            }
-            if (threadIdx.x < kTile) s_w[threadIdx.x] = decay_pow(ld, threadIdx.x & (block - 1)) * a.out_scale;
+#pragma unroll
+            for (int i = 0; i < kLoadsV; ++i) s_v[grp + i * kGroups][col] = fv[i] * s_inv[grp + i * kGroups];
             __syncthreads();
+            if (tb + kTile < to) fetch(tb + kTile, (int)(to - tb - kTile < kTile ? to - tb - kTile : kTile));
             for (int t = 0; t < m; ++t) {
                 const float vv = s_v[t][col];
-                float acc = 0.0f;
+                float acc[4] = {};
 #pragma unroll
                 for (int i = 0; i < R; i += 4) {
                     const float4 kk = *reinterpret_cast<const float4*>(&s_k[t][grp * R + i]);
@@ -126,11 +145,11 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
                     s[i + 2] = fmaf(kk.z, vv, s[i + 2]), s[i + 3] = fmaf(kk.w, vv, s[i + 3]);
                     if (!FOLD) {
                         const float4 qq = *reinterpret_cast<const float4*>(&s_q[t][grp * R + i]);
-                        acc = fmaf(qq.x, s[i], acc), acc = fmaf(qq.y, s[i + 1], acc);
-                        acc = fmaf(qq.z, s[i + 2], acc), acc = fmaf(qq.w, s[i + 3], acc);
+                        acc[0] = fmaf(qq.x, s[i], acc[0]), acc[1] = fmaf(qq.y, s[i + 1], acc[1]);
+                        acc[2] = fmaf(qq.z, s[i + 2], acc[2]), acc[3] = fmaf(qq.w, s[i + 3], acc[3]);
                     }
                 }
-                if (!FOLD) s_o[t][grp][col] = acc;
+                if (!FOLD) s_o[t][grp][col] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
                 const int e = t & (block - 1);
                 const bool last = tb + t == to - 1;
                 if (last || e == block - 1) {
@@ -256,6 +275,7 @@ ak_status launch_tokens_of(const Batch& b, cudaStream_t stream) {
     const int dk = std::max(b.a[0].dk, b.count > 1 ? b.a[0].dv : 0);
     if (dk <= 32) return launch_tokens<T, 32>(b, stream);
     if (dk <= 64) return launch_tokens<T, 64>(b, stream);
+    if (dk <= 96) return launch_tokens<T, 96>(b, stream);
     if (dk <= 128) return launch_tokens<T, 128>(b, stream);
     return launch_tokens<T, 256>(b, stream);
 }
@@ -418,7 +438,7 @@ static Division divide_chunks(const LinattnCall& c, const DeviceInfo& dev, int c
     return divide(c, 2 * dev.sm_count, (int64_t)c.heads * calls);
 }
 static Division divide_tokens(const LinattnCall& c, const DeviceInfo& dev, int calls) {
-    return divide(c, 8 * dev.sm_count, (int64_t)c.heads * calls * token_slices(std::max(c.dk, c.dv)));
+    return divide(c, 3 * dev.sm_count, (int64_t)c.heads * calls * token_slices(std::max(c.dk, c.dv)));
 }
 
 static size_t carry_bytes(const LinattnCall& c, const Division& d, int calls) {

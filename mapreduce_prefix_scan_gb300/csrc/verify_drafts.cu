@@ -33,6 +33,7 @@ namespace ak {
 namespace vd {
 
 constexpr int kThreads = 512;
+constexpr int kBlocksPerSm = 3;
 
 __device__ __forceinline__ float as_f(float v) { return v; }
 __device__ __forceinline__ float as_f(bf16 v) { return __bfloat162float(v); }
@@ -79,18 +80,32 @@ __device__ __forceinline__ uint64_t fold(const T* p, const T* q, const float* e,
         }
         first = full;
     }
-#pragma unroll 4
-    for (int64_t v = first + threadIdx.x; v < last; v += kThreads) {
-        float w = as_f(p[v]);
-        if (MODE == 1) w -= as_f(q[v]);
-        if (MODE == 2 && v == draft) w = 0.0f;
-        offer(best, w, e[v], (uint32_t)v);
+    // rows that 16-byte loads do not fit, and a row's end: one value a load,
+    // kOnce of them in flight (the candidates' branches would keep the
+    // compiler from starting one before the last is done with)
+    constexpr int kOnce = 6;
+    for (int64_t v = first + threadIdx.x; v < last; v += kOnce * kThreads) {
+        float w[kOnce], x[kOnce], n[kOnce];
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i) {
+            const int64_t at = min(v + i * kThreads, last - 1);
+            w[i] = as_f(p[at]);
+            if (MODE == 1) x[i] = as_f(q[at]);
+            n[i] = e[at];
+        }
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i) {
+            const int64_t at = v + i * kThreads;
+            if (MODE == 1) w[i] -= x[i];
+            if (MODE == 2 && at == draft) w[i] = 0.0f;
+            if (at < last) offer(best, w[i], n[i], (uint32_t)at);
+        }
     }
     return best;
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_verify(const VerifyCall c) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_verify(const VerifyCall c) {
     __shared__ uint64_t s_warp[kThreads / kWarp];
     __shared__ uint64_t s_best[2];
     __shared__ int s_taken, s_count;
@@ -104,20 +119,20 @@ __global__ void __launch_bounds__(kThreads) k_verify(const VerifyCall c) {
     const int32_t* d = c.drafts + r * c.k;
 
     if (warp == 0) {
+        // the first loads do not wait for the count
+        int64_t t = lane < c.k ? d[lane] : -1;
+        float u = lane < c.k ? c.uniform[r * c.k + lane] : 0.0f;
         int m = c.counts ? c.counts[r] : c.k;
         m = max(0, min(m, c.k));
         int taken = m;
         for (int j0 = 0; j0 < m; j0 += kWarp) {
             const int j = j0 + lane;
-            bool ok = j < m;
+            if (j0 > 0 && j < m) t = d[j], u = c.uniform[r * c.k + j];
+            bool ok = j < m && t >= 0 && t < c.vocab;
             if (ok) {
-                const int64_t t = d[j];
-                ok = t >= 0 && t < c.vocab;
-                if (ok) {
-                    const float pv = as_f(p[j * c.p_row + t]);
-                    const float qv = q ? as_f(q[j * c.q_row + t]) : 1.0f;
-                    ok = __fmul_rn(c.uniform[r * c.k + j], qv) < pv;
-                }
+                const float pv = as_f(p[j * c.p_row + t]);
+                const float qv = q ? as_f(q[j * c.q_row + t]) : 1.0f;
+                ok = __fmul_rn(u, qv) < pv;
             }
             const unsigned refused = __ballot_sync(0xffffffffu, !ok && j < m);
             if (refused) {
@@ -192,10 +207,11 @@ ak_status run_verify(const VerifyCall& c, cudaStream_t stream) {
     using namespace vd;
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
-    // blocks of a request: enough for two blocks an SM over all requests,
-    // each with at least one round of vector loads
+    // blocks of a request: as many as run at once over all requests (three an
+    // SM), each with at least one round of vector loads. 192 requests of
+    // 128000 float32: 2 blocks 45 us, 4 blocks (a second wave) 51, 8 blocks 60.
     int parts = 1;
-    while (parts < 8 && c.nreq * parts < 2 * dev.sm_count && c.vocab / (2 * parts) >= kThreads * 4) parts *= 2;
+    while (parts < 8 && c.nreq * parts * 2 <= kBlocksPerSm * dev.sm_count && c.vocab / (2 * parts) >= kThreads * 4) parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(c.nreq * parts));
     cfg.blockDim = dim3(kThreads);

@@ -29,21 +29,24 @@ class BatchLayout(NamedTuple):
     counts: torch.Tensor
 
 
-def _stream_of(stream) -> int:
+# the handle alone: torch.cuda.current_stream() builds an object around it, which takes longer than a call here
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _current is not None:
+            return _current(t.get_device())
+        return torch.cuda.current_stream(t.device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _keep(stream, *tensors):
-    """Memory allocated here for a call on another stream than the current one is not handed out again before
-    that stream is done with it."""
+def _empty(size, dtype, device, stream):
+    """Memory for a call on `stream`: from that stream's own pool, so that nothing queued elsewhere still uses it."""
     if stream is None:
-        return
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device)):
+        return torch.empty(size, dtype=dtype, device=device)
 
 
 def _opts(opts):
@@ -54,7 +57,7 @@ def _opts(opts):
 
 
 def _check(status: int, where: str) -> None:
-    if status != _abi.AK_OK:
+    if status:
         from . import AkError
         raise AkError(status, where)
 
@@ -66,7 +69,7 @@ def _need(cond, message):
 
 def _flat(t, dtype, numel, name):
     """Pointer of a contiguous CUDA tensor of `numel` elements of `dtype`."""
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() == numel):
+    if not (t.dtype is dtype and t.numel() == numel and t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name}: a contiguous CUDA tensor of {numel} {dtype} values is needed, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
@@ -82,8 +85,7 @@ def _workspace_ptr(nbytes, device, workspace, stream):
         size = workspace.numel() * workspace.element_size()
         _need(size >= nbytes, "workspace too small")
         return workspace.data_ptr(), size
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _keep(stream, ws)
+    ws = _empty(nbytes, torch.uint8, device, stream)
     return ws.data_ptr(), nbytes
 
 
@@ -107,36 +109,42 @@ def ak_batch_layout(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     new entries of ``block_table`` ([requests, width] int32, in place) taken in
     order from ``free_blocks``. Token arrays hold ``max_tokens`` entries, -1 / 0
     / -1 past the batch's end."""
-    n = ctx_lens.numel()
+    n, width = block_table.shape
     dev = ctx_lens.device
-    _need(block_table.is_cuda and block_table.dtype == torch.int32 and block_table.dim() == 2 and
-          block_table.shape[0] == n and _dense_rows(block_table),
-          "block_table: a [requests, width] int32 CUDA tensor with contiguous rows is needed")
+    if not (block_table.dtype is torch.int32 and block_table.is_cuda and _dense_rows(block_table)):
+        raise ValueError("block_table: a [requests, width] int32 CUDA tensor with contiguous rows is needed")
+    nfree = free_blocks.numel()
+    inputs = (_flat(ctx_lens, torch.int32, n, "ctx_lens"), _flat(new_lens, torch.int32, n, "new_lens"),
+              _flat(free_blocks, torch.int32, nfree, "free_blocks"))
+    p_off = p_slots = p_pos = p_req = p_cnt = None
     if offsets is None:
-        offsets = torch.empty(n + 1, dtype=torch.int32, device=dev)
-        _keep(stream, offsets)
+        offsets = _empty(n + 1, torch.int32, dev, stream)
+    else:
+        p_off = _flat(offsets, torch.int32, n + 1, "offsets")
     if slots is None:
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-        _keep(stream, slots)
+        slots = _empty(max_tokens, torch.int64, dev, stream)
+    else:
+        p_slots = _flat(slots, torch.int64, max_tokens, "slots")
     if positions is None:
-        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-        _keep(stream, positions)
+        positions = _empty(max_tokens, torch.int32, dev, stream)
+    else:
+        p_pos = _flat(positions, torch.int32, max_tokens, "positions")
     if requests is None:
-        requests = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-        _keep(stream, requests)
+        requests = _empty(max_tokens, torch.int32, dev, stream)
+    else:
+        p_req = _flat(requests, torch.int32, max_tokens, "requests")
     if counts is None:
-        counts = torch.empty(2, dtype=torch.int32, device=dev)
-        _keep(stream, counts)
-    L = _abi.load()
-    size = ak_batch_layout_workspace_size(n) if n > 4096 else 0
-    wp, wb = _workspace_ptr(size, dev, workspace, stream) if size or workspace is not None else (None, 0)
-    _check(L.ak_batch_layout(
-        _flat(ctx_lens, torch.int32, n, "ctx_lens"), _flat(new_lens, torch.int32, n, "new_lens"), n,
-        block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
-        _flat(free_blocks, torch.int32, free_blocks.numel(), "free_blocks"), free_blocks.numel(), int(block_size),
-        int(max_tokens), _flat(offsets, torch.int32, n + 1, "offsets"), _flat(slots, torch.int64, max_tokens, "slots"),
-        _flat(positions, torch.int32, max_tokens, "positions"), _flat(requests, torch.int32, max_tokens, "requests"),
-        _flat(counts, torch.int32, 2, "counts"), wp, wb, _opts(opts), _stream_of(stream)), "ak_batch_layout")
+        counts = _empty(2, torch.int32, dev, stream)
+    else:
+        p_cnt = _flat(counts, torch.int32, 2, "counts")
+    wp, wb = None, 0
+    if n > 4096 or workspace is not None:  # smaller batches need none
+        wp, wb = _workspace_ptr(ak_batch_layout_workspace_size(n), dev, workspace, stream)
+    _check(_abi.load().ak_batch_layout(
+        inputs[0], inputs[1], n, block_table.data_ptr(), max(block_table.stride(0), width), width, inputs[2], nfree,
+        block_size, max_tokens, p_off or offsets.data_ptr(), p_slots or slots.data_ptr(), p_pos or positions.data_ptr(),
+        p_req or requests.data_ptr(), p_cnt or counts.data_ptr(), wp, wb, _opts(opts), _stream_of(stream, ctx_lens)),
+        "ak_batch_layout")
     return BatchLayout(offsets, slots, positions, requests, counts)
 
 
@@ -156,33 +164,38 @@ def ak_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
     and how many drafts were kept."""
     n, k = draft_tokens.shape
     vocab = target_probs.shape[-1]
-    dev = target_probs.device
-    dt = target_probs.dtype
-    _need(dt in _FLOAT, "probabilities are float32 or bfloat16")
-    _need(target_probs.is_cuda and target_probs.shape == (n, k + 1, vocab) and _dense_rows(target_probs),
-          "target_probs: a [requests, k + 1, vocab] CUDA tensor with contiguous rows is needed")
-    _need(noise.is_cuda and noise.dtype == torch.float32 and noise.shape == (n, vocab) and _dense_rows(noise),
-          "noise: a [requests, vocab] float32 CUDA tensor with contiguous rows is needed")
+    dev, dt = target_probs.device, target_probs.dtype
+    kind = _FLOAT.get(dt)
+    if kind is None:
+        raise ValueError("probabilities are float32 or bfloat16")
+    if not (target_probs.shape == (n, k + 1, vocab) and target_probs.is_cuda and _dense_rows(target_probs)):
+        raise ValueError("target_probs: a [requests, k + 1, vocab] CUDA tensor with contiguous rows is needed")
+    if not (noise.dtype is torch.float32 and noise.shape == (n, vocab) and noise.is_cuda and _dense_rows(noise)):
+        raise ValueError("noise: a [requests, vocab] float32 CUDA tensor with contiguous rows is needed")
     q, qs = None, (0, 0)
     if draft_probs is not None:
-        _need(draft_probs.is_cuda and draft_probs.dtype == dt and draft_probs.shape == (n, k, vocab) and
-              _dense_rows(draft_probs),
-              "draft_probs: a [requests, k, vocab] CUDA tensor of the target's type with contiguous rows is needed")
+        if not (draft_probs.dtype is dt and draft_probs.shape == (n, k, vocab) and draft_probs.is_cuda and
+                _dense_rows(draft_probs)):
+            raise ValueError("draft_probs: a [requests, k, vocab] CUDA tensor of the target's type with contiguous "
+                             "rows is needed")
         q, qs = (draft_probs.data_ptr() if k else None), draft_probs.stride()
+    drafts = _flat(draft_tokens, torch.int32, n * k, "draft_tokens")
+    u = _flat(uniform, torch.float32, n * k, "uniform")
+    m = None if draft_counts is None else _flat(draft_counts, torch.int32, n, "draft_counts")
+    p_tok = p_acc = None
     if tokens is None:
-        tokens = torch.empty(n, k + 1, dtype=torch.int32, device=dev)
-        _keep(stream, tokens)
+        tokens = _empty((n, k + 1), torch.int32, dev, stream)
+    else:
+        p_tok = _flat(tokens, torch.int32, n * (k + 1), "tokens")
     if accepted is None:
-        accepted = torch.empty(n, dtype=torch.int32, device=dev)
-        _keep(stream, accepted)
+        accepted = _empty(n, torch.int32, dev, stream)
+    else:
+        p_acc = _flat(accepted, torch.int32, n, "accepted")
     ps = target_probs.stride()
     _check(_abi.load().ak_verify_drafts(
-        target_probs.data_ptr(), ps[0], ps[1], q, qs[0], qs[1], _FLOAT[dt],
-        _flat(draft_tokens, torch.int32, n * k, "draft_tokens"),
-        None if draft_counts is None else _flat(draft_counts, torch.int32, n, "draft_counts"),
-        _flat(uniform, torch.float32, n * k, "uniform"), noise.data_ptr(), noise.stride(0), n, k, vocab,
-        _flat(tokens, torch.int32, n * (k + 1), "tokens"), _flat(accepted, torch.int32, n, "accepted"), _opts(opts),
-        _stream_of(stream)), "ak_verify_drafts")
+        target_probs.data_ptr(), ps[0], ps[1], q, qs[0], qs[1], kind, drafts, m, u, noise.data_ptr(), noise.stride(0),
+        n, k, vocab, p_tok or tokens.data_ptr(), p_acc or accepted.data_ptr(), _opts(opts),
+        _stream_of(stream, target_probs)), "ak_verify_drafts")
     return tokens, accepted
 
 
@@ -191,10 +204,10 @@ def ak_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
 # ---------------------------------------------------------------------------
 
 def _heads(t: torch.Tensor, shape, dtype, name) -> ak_heads:
-    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and (t.stride(2) == 1 or shape[2] == 1)):
-        raise ValueError(f"{name}: a {list(shape)} {dtype} CUDA tensor with a contiguous last dimension is needed, "
-                         f"got {list(t.shape)} {t.dtype} with strides {list(t.stride())} on {t.device}")
     s = t.stride()
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and (s[2] == 1 or shape[2] == 1)):
+        raise ValueError(f"{name}: a {list(shape)} {dtype} CUDA tensor with a contiguous last dimension is needed, "
+                         f"got {list(t.shape)} {t.dtype} with strides {list(s)} on {t.device}")
     return ak_heads(t.data_ptr(), s[0], s[1])
 
 
@@ -207,16 +220,22 @@ def _state_ptr(t, shape, name):
 
 
 def _geometry(q, k, v, log_decay, offsets, scale, max_len):
-    _need(q.dim() == 3 and v.dim() == 3, "q, k and v are [tokens, heads, dim] tensors")
-    t, h, dk = q.shape
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v are [tokens, heads, dim] tensors")
+    sk = q.shape
+    t, h, dk = sk
     dv = v.shape[2]
     dt = q.dtype
-    _need(dt in _FLOAT, "q, k and v are float32 or bfloat16")
-    n = 1 if offsets is None else offsets.numel() - 1
-    _need(n >= 0, "offsets: at least one value is needed")
-    a = ak_linattn(t, n, int(max_len or 0), h, dk, dv, _FLOAT[dt], scale, 0)
+    kind = _FLOAT.get(dt)
+    if kind is None:
+        raise ValueError("q, k and v are float32 or bfloat16")
+    n, off = 1, None
+    if offsets is not None:
+        n = offsets.numel() - 1
+        _need(n >= 0, "offsets: at least one value is needed")
+        off = _flat(offsets, torch.int32, n + 1, "offsets")
+    a = ak_linattn(t, n, max_len or 0, h, dk, dv, kind, scale, 0)
     ld = _flat(log_decay, torch.float32, h, "log_decay")
-    off = None if offsets is None else _flat(offsets, torch.int32, n + 1, "offsets")
     return a, (t, h, dk), (t, h, dv), (n, h, dk, dv), dt, ld, off
 
 
@@ -231,8 +250,7 @@ def ak_linear_attention_workspace_size(tokens: int, heads: int, dk: int, dv: int
 
 def _workspace(a, device, workspace, opts, stream):
     b = ctypes.c_size_t()
-    _check(_abi.load().ak_linear_attention_workspace_size(ctypes.byref(a), opts, ctypes.byref(b)),
-           "ak_linear_attention_workspace_size")
+    _check(_abi.load().ak_linear_attention_workspace_size(a, opts, b), "ak_linear_attention_workspace_size")
     return _workspace_ptr(b.value, device, workspace, stream)
 
 
@@ -247,17 +265,14 @@ def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     state_out)``, the latter None unless given or asked for by ``final_state``."""
     a, sk, sv, ss, dt, ld, off = _geometry(q, k, v, log_decay, offsets, scale, max_len)
     if out is None:
-        out = torch.empty(sv, dtype=dt, device=q.device)
-        _keep(stream, out)
+        out = _empty(sv, dt, q.device, stream)
     if state_out is None and final_state:
-        state_out = torch.empty(ss, dtype=torch.float32, device=q.device)
-        _keep(stream, state_out)
+        state_out = _empty(ss, torch.float32, q.device, stream)
     op = _opts(opts)
     hq, hk, hv, ho = _heads(q, sk, dt, "q"), _heads(k, sk, dt, "k"), _heads(v, sv, dt, "v"), _heads(out, sv, dt, "out")
     s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(state_out, ss, "state_out")
     wp, wb = _workspace(a, q.device, workspace, op, stream)
-    _check(_abi.load().ak_linear_attention(ctypes.byref(a), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), ld,
-                                           off, s0, ctypes.byref(ho), s1, wp, wb, op, _stream_of(stream)),
+    _check(_abi.load().ak_linear_attention(a, hq, hk, hv, ld, off, s0, ho, s1, wp, wb, op, _stream_of(stream, q)),
            "ak_linear_attention")
     return out, state_out
 
@@ -275,26 +290,22 @@ def ak_linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Ten
     a, sk, sv, ss, dt, ld, off = _geometry(q, k, v, log_decay, offsets, scale, max_len)
     dev = q.device
     if dq is None:
-        dq = torch.empty(sk, dtype=dt, device=dev)
-        _keep(stream, dq)
+        dq = _empty(sk, dt, dev, stream)
     if dk is None:
-        dk = torch.empty(sk, dtype=dt, device=dev)
-        _keep(stream, dk)
+        dk = _empty(sk, dt, dev, stream)
     if dv is None:
-        dv = torch.empty(sv, dtype=dt, device=dev)
-        _keep(stream, dv)
+        dv = _empty(sv, dt, dev, stream)
     if dstate is None and state is not None:
-        dstate = torch.empty(ss, dtype=torch.float32, device=dev)
-        _keep(stream, dstate)
+        dstate = _empty(ss, torch.float32, dev, stream)
     op = _opts(opts)
     hs = [_heads(x, s, dt, n) for x, s, n in ((do, sv, "do"), (q, sk, "q"), (k, sk, "k"), (v, sv, "v"),
                                               (dq, sk, "dq"), (dk, sk, "dk"), (dv, sv, "dv"))]
-    hdo, hq, hk, hv, hdq, hdk, hdv = [ctypes.byref(x) for x in hs]
+    hdo, hq, hk, hv, hdq, hdk, hdv = hs
     s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(dstate_out, ss, "dstate_out")
     s2 = _state_ptr(dstate, ss, "dstate")
     wp, wb = _workspace(a, dev, workspace, op, stream)
-    _check(_abi.load().ak_linear_attention_backward(ctypes.byref(a), hdo, hq, hk, hv, ld, off, s0, s1, hdq, hdk, hdv,
-                                                    s2, wp, wb, op, _stream_of(stream)),
+    _check(_abi.load().ak_linear_attention_backward(a, hdo, hq, hk, hv, ld, off, s0, s1, hdq, hdk, hdv,
+                                                    s2, wp, wb, op, _stream_of(stream, q)),
            "ak_linear_attention_backward")
     return dq, dk, dv, dstate
 
@@ -308,14 +319,13 @@ def ak_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     mark padding and give zeros."""
     a, sk, sv, ss, dt, ld, _ = _geometry(q, k, v, log_decay, None, scale, None)
     if out is None:
-        out = torch.empty(sv, dtype=dt, device=q.device)
-        _keep(stream, out)
+        out = _empty(sv, dt, q.device, stream)
     hq, hk, hv, ho = _heads(q, sk, dt, "q"), _heads(k, sk, dt, "k"), _heads(v, sv, dt, "v"), _heads(out, sv, dt, "out")
     pool = state.shape[0]
     sp = _state_ptr(state, (pool,) + ss[1:], "state")
     at = None if slots is None else _flat(slots, torch.int32, sk[0], "slots")
     _need(slots is not None or pool >= sk[0], "state: one matrix for each request and head is needed")
-    _check(_abi.load().ak_linear_attention_step(ctypes.byref(a), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
-                                                ld, sp, at, pool, ctypes.byref(ho), _opts(opts), _stream_of(stream)),
+    _check(_abi.load().ak_linear_attention_step(a, hq, hk, hv, ld, sp, at, pool, ho, _opts(opts),
+                                                _stream_of(stream, q)),
            "ak_linear_attention_step")
     return out
