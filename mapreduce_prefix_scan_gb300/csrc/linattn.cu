@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
 // on return it holds the state before window w. One thread takes E values of
 // the state and walks the windows; kAhead loads are in flight before the
 // chain needs them.
-constexpr int kAhead = 8;
+constexpr int kAhead = 16;
 
 template <int E>
 __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Batch batch, int64_t n) {
@@ -226,8 +226,10 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Batch batc
         int32_t kind[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            kind[j] = w0 + j < a.windows ? a.tail[w0 + j] : (int32_t)kNone;
-            if (kind[j] != kNone) u[j] = c[(w0 + j) * n];
+            // (a slot that no fold wrote is read as well, and not used)
+            const bool in = w0 + j < a.windows;
+            kind[j] = in ? a.tail[w0 + j] : (int32_t)kNone;
+            if (in) u[j] = c[(w0 + j) * n];
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -396,7 +398,7 @@ ak_status launch_step(const StepArgs& a, int64_t batch, bool vec, cudaStream_t s
 
 // How the token axis is divided among blocks.
 struct Division {
-    bool by_seq;
+    bool by_seq, ranked;
     int64_t window, windows;
 };
 
@@ -426,6 +428,8 @@ static Division divide(const LinattnCall& c, int64_t slots, int64_t lanes) {
                                                : std::max(1.35 * work, (double)per) + 4;
     if (seq_steps <= window_steps) {
         d.by_seq = true;
+        // (sorting takes a block about 2 us, which a few chunks do not earn back)
+        d.ranked = c.seqs <= la::kRanked && longest > 4;
         d.windows = c.seqs;
     }
     return d;
@@ -485,7 +489,7 @@ static ak_status run_batch(la::Batch& b, const LinattnCall& c, const DeviceInfo&
         char* w = static_cast<char*>(ws) + kWsHeader;
         for (int i = 0; i < b.count; ++i) {
             la::Args& a = b.a[i];
-            a.by_seq = d.by_seq, a.window = d.window, a.windows = d.windows;
+            a.by_seq = d.by_seq, a.ranked = d.ranked, a.window = d.window, a.windows = d.windows;
             a.tail = reinterpret_cast<int32_t*>(w);
             w += align_up((size_t)d.windows * 4, 256);
             a.carry = reinterpret_cast<float*>(w);

@@ -51,6 +51,7 @@ struct Args {
     bool reverse;
     float out_scale, in_scale;
     bool by_seq;             // block w takes sequence w; windows = seqs
+    bool ranked;             // block w takes the w-th longest sequence
     int64_t window, windows;
     float* carry;            // [windows][H][dk * dv]
     int32_t* tail;           // [windows]

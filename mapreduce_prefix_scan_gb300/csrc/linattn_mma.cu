@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
     const int h = blockIdx.x;
     int w = blockIdx.y;
-    if (!FOLD && a.by_seq && a.seqs <= kRanked) {
+    if (!FOLD && a.ranked) {
         // block w takes the w-th longest sequence: the long ones start first
         for (int i = tid; i < a.seqs; i += kMmaThreads) t.len[i] = (int)(offset_at(a, i + 1) - offset_at(a, i));
         __syncthreads();
