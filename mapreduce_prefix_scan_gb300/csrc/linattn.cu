@@ -49,8 +49,10 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
     const int col = threadIdx.x % 32, grp = threadIdx.x / 32;
     const int64_t w = blockIdx.x;
     const int h = blockIdx.y;
-    const Args& a = batch.a[blockIdx.z % batch.count];
-    const int c0 = blockIdx.z / batch.count * 32;
+    const int calls = FOLD ? batch.folds : batch.count;
+    const Args& a = batch.a[blockIdx.z % calls];
+    const int c0 = blockIdx.z / calls * 32;
+    if (FOLD) griddep_launch_dependents();
     if (c0 >= a.dv) return;  // the calls of a batch may differ in dv
     const bool live = c0 + col < a.dv;
     int64_t t0, t1;
@@ -171,6 +173,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
     };
 
     int64_t n = first_sequence<kThreads>(a, w, t0, &s_count);
+    if (!FOLD) griddep_wait();  // the carries; and nothing is written before
     if (FOLD) {
         // the sequence that crosses the window's end
         while (n < a.seqs && offset_at(a, n + 1) <= t1) ++n;
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
         if (begin > at) blank(at, begin < t1 ? begin : t1);
         const bool before = begin < t0;  // never, by sequence
         const int64_t from = before ? t0 : begin, to = end < t1 ? end : t1;
-        if (before) load_state(a.carry + (w * a.heads + h) * ssize, false);
+        if (before) load_state(a.carry + (w * a.heads + h) * ssize, a.carry_t);
         else if (a.stash && end > t1) load_state(a.stash + (w * a.heads + h) * ssize, false);
         else load_state(a.s_in ? a.s_in + seq_state(n) : nullptr, a.s_in_t);
         if (from < to) walk(from, to);
@@ -212,12 +215,15 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
 constexpr int kAhead = 16;
 
 template <int E>
-__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Batch batch, int64_t n) {
+__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Batch batch) {
     const Args& a = batch.a[blockIdx.y];
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    griddep_launch_dependents();
+    const int64_t n = (int64_t)a.heads * a.dk * a.dv / E;
     if (i >= n) return;
     const int64_t per_head = (int64_t)a.dk * a.dv / E;
     const Factor g = decay_factor(a.log_decay[i / per_head], (int)a.window);
+    griddep_wait();
     Raw<4 * E>* c = reinterpret_cast<Raw<4 * E>*>(a.carry) + i;
     Raw<4 * E> run = {};
     int32_t before = kNone;  // tail of the window before: kNone, and nothing reads the window's state
@@ -248,25 +254,25 @@ ak_status launch_join(const Batch& b, cudaStream_t stream) {
     const Args& a = b.a[0];
     const int64_t n = (int64_t)a.heads * a.dk * a.dv;
     const bool four = (int64_t)a.dk * a.dv % 4 == 0;
-    const dim3 grid((unsigned)((n / (four ? 4 : 1) + 127) / 128), (unsigned)b.count);
-    if (four) k_join<4><<<grid, 128, 0, stream>>>(b, n / 4);
-    else k_join<1><<<grid, 128, 0, stream>>>(b, n);
-    count_launches(1);
-    return check_launch();
+    const dim3 grid((unsigned)((n / (four ? 4 : 1) + 127) / 128), (unsigned)b.folds);
+    return launch_behind(four ? k_join<4> : k_join<1>, grid, 128, 0, stream, b);
 }
 
 template <class T, int DK>
 ak_status launch_tokens(const Batch& b, cudaStream_t stream) {
     const Args& a = b.a[0];
     const int dv = std::max(a.dv, b.count > 1 ? a.dk : 0);
-    const dim3 grid((unsigned)a.windows, (unsigned)a.heads, (unsigned)((dv + 31) / 32 * b.count));
-    if (a.windows > 1 && !a.by_seq) {
+    dim3 grid((unsigned)a.windows, (unsigned)a.heads, (unsigned)((dv + 31) / 32 * b.folds));
+    const bool fold = a.windows > 1 && !a.by_seq;
+    if (fold) {
         k_tokens<T, DK, true><<<grid, kThreads, 0, stream>>>(b);
         count_launches(1);
         ak_status s = check_launch();
         if (s == AK_OK) s = launch_join(b, stream);
         if (s != AK_OK) return s;
     }
+    grid.z = (unsigned)((dv + 31) / 32 * b.count);
+    if (fold) return launch_behind(k_tokens<T, DK, false>, grid, kThreads, 0, stream, b);
     k_tokens<T, DK, false><<<grid, kThreads, 0, stream>>>(b);
     count_launches(1);
     return check_launch();
@@ -496,6 +502,8 @@ static ak_status run_batch(la::Batch& b, const LinattnCall& c, const DeviceInfo&
             w += align_up((size_t)d.windows * c.heads * c.dk * c.dv * 4, 256);
             a.stash = nullptr;
         }
+        // the third call of the backward pass folds the transposes of the second's states
+        if (b.count == 3) b.a[2].carry = b.a[1].carry, b.a[2].tail = b.a[1].tail, b.a[2].carry_t = true;
         // the backward pass has room for three carries and never works in place
         la::Args& a = b.a[0];
         if (b.count == 1 && a.s_in && a.s_in == a.s_out && !d.by_seq && d.windows > 1) a.stash = reinterpret_cast<float*>(w);
@@ -515,7 +523,7 @@ ak_status run_linattn(const LinattnCall& c, void* ws, cudaStream_t stream) {
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
     la::Batch b = {};
-    b.count = 1;
+    b.count = b.folds = 1;
     la::Args& a = b.a[0];
     a = args_of(c);
     roles(a, c.q, c.k, c.v, c.o, c.dk, c.dv);
@@ -528,7 +536,7 @@ ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stre
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
     la::Batch b = {};
-    b.count = 3;
+    b.count = 3, b.folds = 2;
     for (la::Args& a : b.a) a = args_of(c);
     // dq = F(do, v, k) from the transposed initial state
     roles(b.a[0], c.o, c.v, c.k, c.dq, c.dv, c.dk);

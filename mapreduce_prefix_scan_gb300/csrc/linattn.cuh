@@ -54,6 +54,7 @@ struct Args {
     bool ranked;             // block w takes the w-th longest sequence
     int64_t window, windows;
     float* carry;            // [windows][H][dk * dv]
+    bool carry_t;            // the carry is another call's, transposed
     int32_t* tail;           // [windows]
     // states written in place (s_out == s_in): the fold pass keeps here what
     // the main pass needs after another block may have overwritten it, the
@@ -67,7 +68,29 @@ constexpr int kRanked = 256;  // sequences that blocks sort by length
 struct Batch {
     Args a[kMaxCalls];
     int count;
+    int folds;  // of them, from the first, have a fold and a join of their own
 };
+
+// Launches `kernel` so that it may start while the launch before it still
+// runs: until griddep_wait() it touches nothing of that one's. A fold pass, the
+// join and the main pass follow each other this way.
+template <class K, class A>
+inline ak_status launch_behind(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A& arg) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, arg);
+    if (e != cudaSuccess) return cuda_fail(e);
+    count_launches(1);
+    return check_launch();
+}
 
 __device__ __forceinline__ int64_t offset_at(const Args& a, int64_t n) {
     if (!a.offsets) return n == 0 ? 0 : a.tokens;

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
     const int h = blockIdx.x;
     int w = blockIdx.y;
+    if (FOLD) griddep_launch_dependents();
     if (!FOLD && a.ranked) {
         // block w takes the w-th longest sequence: the long ones start first
         for (int i = tid; i < a.seqs; i += kMmaThreads) t.len[i] = (int)(offset_at(a, i + 1) - offset_at(a, i));
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     };
 
     int n = (int)first_sequence<kMmaThreads>(a, w, t0, &t.count);
+    if (!FOLD) griddep_wait();  // the carries; and nothing is written before
     Chunk c = {};
     int32_t kind = kNone;
     if (FOLD) {
@@ -337,7 +339,10 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     auto source = [&](const Chunk& c, bool* transposed) -> const float* {
         *transposed = false;
         const bool here = FOLD ? kind == kFresh : offset(c.n) >= t0;
-        if (!here) return FOLD ? nullptr : a.carry + ((int64_t)w * a.heads + h) * ssize;
+        if (!here) {
+            *transposed = a.carry_t;
+            return FOLD ? nullptr : a.carry + ((int64_t)w * a.heads + h) * ssize;
+        }
         if (!a.s_in) return nullptr;
         // another block may already have written this sequence's result in place
         if (!FOLD && a.stash && c.end < c.stop) return a.stash + ((int64_t)w * a.heads + h) * ssize;
@@ -737,7 +742,9 @@ static ak_status launch(const ChunkBatch& c, cudaStream_t stream) {
         ready.fetch_or(1ull << dev.device);
     }
     const Args& a = c.b.a[0];
-    const dim3 grid((unsigned)a.heads, (unsigned)a.windows, (unsigned)c.b.count);
+    const dim3 grid((unsigned)a.heads, (unsigned)a.windows, (unsigned)(FOLD ? c.b.folds : c.b.count));
+    if (!FOLD && a.windows > 1 && !a.by_seq)
+        return launch_behind(k_chunks<D, PARTS, FOLD>, grid, Plan<D, PARTS, FOLD>::kThreads, smem, stream, c);
     k_chunks<D, PARTS, FOLD><<<grid, Plan<D, PARTS, FOLD>::kThreads, smem, stream>>>(c);
     count_launches(1);
     return check_launch();
