@@ -45,13 +45,21 @@ struct Req {
     int ctx, fresh, have, want;
 };
 
+// Blocks that `tokens` fill. 32-bit, and a shift for powers of two: 64-bit
+// divisions of every length in every block were half of this kernel's
+// instructions.
+__device__ __forceinline__ int blocks_of(const LayoutCall& c, uint32_t tokens) {
+    const uint32_t b = (uint32_t)c.block_size;
+    if (c.block_shift >= 0) return (int)((tokens >> c.block_shift) + ((tokens & (b - 1)) != 0));
+    return (int)(tokens / b + (tokens % b != 0));
+}
+
 __device__ __forceinline__ Req request(const LayoutCall& c, int64_t r) {
     Req q;
     q.ctx = max(c.ctx_lens[r], 0);
     q.fresh = max(c.new_lens[r], 0);
-    const int b = c.block_size;
-    q.have = (int)(((int64_t)q.ctx + b - 1) / b);
-    q.want = (int)(((int64_t)q.ctx + q.fresh + b - 1) / b);
+    q.have = blocks_of(c, (uint32_t)q.ctx);
+    q.want = blocks_of(c, (uint32_t)q.ctx + (uint32_t)q.fresh);
     return q;
 }
 
@@ -133,7 +141,7 @@ __device__ __forceinline__ void expand(const LayoutCall& c, const int32_t* off, 
                 if (r != held) {
                     held = r;
                     ctx = max(ctx_of[r], 0);
-                    have = (int)(((int64_t)ctx + c.block_size - 1) / c.block_size);
+                    have = blocks_of(c, (uint32_t)ctx);
                     start = off[r];
                     bs = (uint32_t)base[r];
                 }
