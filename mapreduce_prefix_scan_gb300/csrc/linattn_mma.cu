@@ -66,6 +66,8 @@ struct ChunkBatch {
     uint64_t wait_limit_ns;
 };
 
+constexpr int kFrame = 16;  // chunks of a frame at most
+
 // Barriers and tables of a block.
 struct Small {
     // arrivals: copies of q and k, of v (a stage each), products (of
@@ -74,13 +76,14 @@ struct Small {
     uint64_t qk[2], v[2], inter, scores, values, update, state, wv, ready;
     int64_t count;
     uint32_t tmem;
-    int failed, rank;
+    int failed, w, t0, t1;  // w: window or sequence of the block, t0, t1: its span
     // weights: of row j in the update after a whole chunk; and, which a fold
     // pass does not have, of the state before the chunk at row i, and of the
     // score of rows i and j at kChunk + i - j
     float wrow[kChunk];
     alignas(16) float age[kChunk];
     float score[2 * kChunk];
+    float up[kFrame], down[kFrame];  // g^64u, and g^-64(u+1) or 1 (see `frame`)
     int len[kRanked];
 };
 
@@ -169,8 +172,8 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     const uint32_t sbase = smem_addr(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
     const int h = blockIdx.x;
-    int w = blockIdx.y;
     if (FOLD) griddep_launch_dependents();
+    if (tid == 0) t.w = blockIdx.y;
     if (!FOLD && a.ranked) {
         // block w takes the w-th longest sequence: the long ones start first
         for (int i = tid; i < a.seqs; i += kMmaThreads) t.len[i] = (int)(offset_at(a, i + 1) - offset_at(a, i));
@@ -179,19 +182,26 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             const int mine = t.len[i];
             int rank = 0;
             for (int j = 0; j < a.seqs; ++j) rank += t.len[j] > mine || (t.len[j] == mine && j < i);
-            if (rank == w) t.rank = i;
+            if (rank == blockIdx.y) t.w = i;
         }
-        __syncthreads();
-        w = t.rank;
     }
-    int t0, t1;
-    {
+    __syncthreads();
+    if (tid == 0) {
         int64_t from, to;
-        block_span(a, w, &from, &to);
-        t0 = (int)from, t1 = (int)to;
+        block_span(a, t.w, &from, &to);
+        t.t0 = (int)from, t.t1 = (int)to;
     }
     const float ld = a.log_decay[h];
     const bool rev = a.reverse;
+    // The state's frame. S is held divided by the decay since the frame
+    // began, `frame` chunks at most, so that a chunk reads it for its bf16
+    // form but writes it back only when a frame ends: TMEM traffic, at the
+    // 128 bytes a cycle that shared memory has too, is what these warps
+    // spend most on, and the write was a fifth of it. A chunk's terms enter
+    // divided by the decay up to its end. e^30 bounds that; a head that
+    // decays faster scales its state in every chunk before it adds terms.
+    const float per_chunk = fabsf(ld) * kChunk;
+    const int frame = per_chunk <= 30.0f ? (per_chunk * kFrame <= 30.0f ? kFrame : (int)(30.0f / per_chunk)) : 0;
 
     if (warp == kWork / kWarp) {
         tmem_alloc(&t.tmem, P::kTmem);
@@ -217,6 +227,11 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     if (!FOLD && tid < 2 * kChunk) {
         const int gap = rev ? kChunk - tid : tid - kChunk;
         t.score[tid] = gap < 0 ? 0.0f : decay_pow(ld, gap) * a.in_scale * a.out_scale;
+    }
+    if (!FOLD && tid >= 2 * kChunk && tid < 2 * kChunk + kFrame) {
+        const int u = tid - 2 * kChunk;
+        t.up[u] = decay_pow(ld, u * kChunk);
+        t.down[u] = frame == 0 ? 1.0f : decay_pow(ld, -(u + 1) * kChunk);
     }
     if (tid < kChunk) {
         if (!FOLD) t.age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1) * a.out_scale;
@@ -252,7 +267,6 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     };
 
     const int64_t ssize = (int64_t)D * D;
-    bf16* const o = static_cast<bf16*>(a.o) + h * a.o_head;
     auto addr = [&](int t) { return rev ? (int)a.tokens - 1 - t : t; };
     auto offset = [&](int n) { return (int)offset_at(a, n); };
     auto seq_state = [&](int n) { return ((rev ? a.seqs - 1 - n : n) * a.heads + h) * ssize; };
@@ -263,14 +277,13 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     // tokens of no sequence get zeros
     auto blank = [&](int from, int to) {
         if (!FOLD && writer)
-            for (int x = from + tid / D; x < to; x += kWork / D) o[(int64_t)addr(x) * a.o_tok + tid % D] = __float2bfloat16_rn(0.0f);
+            for (int x = from + tid / D; x < to; x += kWork / D) static_cast<bf16*>(a.o)[h * a.o_head + (int64_t)addr(x) * a.o_tok + tid % D] = __float2bfloat16_rn(0.0f);
     };
-    int covered = t0;
     auto start = [&](int n, int begin, int end) {
         Chunk c;
         c.n = n;
-        c.at = begin > t0 ? begin : t0;
-        c.end = end < t1 ? end : t1;
+        c.at = begin > t.t0 ? begin : t.t0;
+        c.end = end < t.t1 ? end : t.t1;
         c.stop = end;
         c.m = c.end - c.at < kChunk ? c.end - c.at : kChunk;
         c.first = true;
@@ -279,29 +292,25 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     };
     // the first chunk of sequence n or a later one; pieces without tokens are
     // settled on the way
-    auto seek = [&](int n) {
+    auto seek = [&](int n, int covered) {  // covered: outputs are settled up to there
         Chunk c = {};
         for (; n < a.seqs; ++n) {
             const int begin = offset(n), end = offset(n + 1);
-            if (a.by_seq ? n > w : begin >= t1 && w != a.windows - 1) break;
+            if (a.by_seq ? n > t.w : begin >= t.t1 && t.w != a.windows - 1) break;
             if (begin > covered) {
-                blank(covered, begin < t1 ? begin : t1);
+                blank(covered, begin < t.t1 ? begin : t.t1);
                 covered = begin;
             }
             c = start(n, begin, end);
-            if (c.at < c.end) {
-                covered = c.end;
-                return c;
-            }
-            if (writer && a.s_out && begin >= t0) {  // an empty sequence passes its state on
+            if (c.at < c.end) return c;
+            if (writer && a.s_out && begin >= t.t0) {  // an empty sequence passes its state on
                 for (int i = tid; i < D * D; i += kWork)
                     a.s_out[seq_state(n) + i] = !a.s_in ? 0.0f
                                                 : a.s_in[seq_state(n) + (a.s_in_t ? (i % D) * D + i / D : i)];
             }
         }
         c.valid = false;
-        if (covered < t1) blank(covered, t1);
-        covered = t1;
+        if (covered < t.t1) blank(covered, t.t1);
         return c;
     };
     auto next = [&](const Chunk& c) {
@@ -313,23 +322,23 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             return x;
         }
         // at the window's end only empty sequences at the axis' end are left
-        if (!FOLD && (c.end < t1 || w == a.windows - 1)) return seek(c.n + 1);
+        if (!FOLD && (c.end < t.t1 || t.w == a.windows - 1)) return seek(c.n + 1, c.end);
         x.valid = false;
         return x;
     };
 
-    int n = (int)first_sequence<kMmaThreads>(a, w, t0, &t.count);
+    int n = (int)first_sequence<kMmaThreads>(a, t.w, t.t0, &t.count);
     if (!FOLD) griddep_wait();  // the carries; and nothing is written before
     Chunk c = {};
     int32_t kind = kNone;
     if (FOLD) {
-        while (n < a.seqs && offset(n + 1) <= t1) ++n;
-        const int begin = n < a.seqs ? offset(n) : t1;
-        kind = begin >= t1 ? kNone : (begin >= t0 ? kFresh : kThrough);
-        if (tid == 0 && h == 0) a.tail[w] = kind;
+        while (n < a.seqs && offset(n + 1) <= t.t1) ++n;
+        const int begin = n < a.seqs ? offset(n) : t.t1;
+        kind = begin >= t.t1 ? kNone : (begin >= t.t0 ? kFresh : kThrough);
+        if (tid == 0 && h == 0) a.tail[t.w] = kind;
         if (kind != kNone) c = start(n, begin, offset(n + 1));
     } else {
-        c = seek(n);
+        c = seek(n, t.t0);
     }
     // parts of w V that a chunk's terms need
     auto parts_of = [&](const Chunk& c) {
@@ -338,14 +347,14 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     // where the state before a piece comes from; null: zero
     auto source = [&](const Chunk& c, bool* transposed) -> const float* {
         *transposed = false;
-        const bool here = FOLD ? kind == kFresh : offset(c.n) >= t0;
+        const bool here = FOLD ? kind == kFresh : offset(c.n) >= t.t0;
         if (!here) {
             *transposed = a.carry_t;
-            return FOLD ? nullptr : a.carry + ((int64_t)w * a.heads + h) * ssize;
+            return FOLD ? nullptr : a.carry + ((int64_t)t.w * a.heads + h) * ssize;
         }
         if (!a.s_in) return nullptr;
         // another block may already have written this sequence's result in place
-        if (!FOLD && a.stash && c.end < c.stop) return a.stash + ((int64_t)w * a.heads + h) * ssize;
+        if (!FOLD && a.stash && c.end < c.stop) return a.stash + ((int64_t)t.w * a.heads + h) * ssize;
         *transposed = a.s_in_t;
         return a.s_in + seq_state(c.n);
     };
@@ -432,7 +441,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 // V^T P^T
 #pragma unroll
                 for (int s = 0; s < kChunk / 16; ++s)
-                    mma_ss(tmem + P::kR, dv + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), s > 0, leader);
+                    mma_ss(tmem + P::kR, dv + (s * 2048 >> 4), dp + (s * 32 >> 4), mma_idesc(128, 64, true, false), !zero || s > 0, leader);
                 mma_commit(&t.values, leader);
             }
             // the next chunk's tiles, each as soon as its buffer has been used
@@ -456,15 +465,15 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
         const int part = warp / 4;               // which quarter of the columns
         const int dv = row % D;                  // state column (copies at D = 64)
         const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
-        const Factor whole = decay_factor(ld, kChunk);
-        uint32_t stage = 0, phase = 0, scores = 0, values = 0, update = 0;
+        uint32_t stage = 0, phase = 0;  // phase: of the stage; without stages, of every barrier of a chunk
+        uint32_t update = 0;
         // S before a piece; false where it is zero
         auto load_state = [&](const Chunk& c) {
             bool tr;
             const float* src = source(c, &tr);
             if (!src) return false;
             // a fold ages its state once, not chunk by chunk
-            const float age = FOLD ? decay_pow(ld, t1 - c.at) : 1.0f;
+            const float age = FOLD ? decay_pow(ld, t.t1 - c.at) : 1.0f;
 #pragma unroll 1
             for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += 16) {
                 uint32_t r[16];
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
 #pragma unroll
                 for (int i = 0; i < 16; ++i, p += tr ? 1 : D) r[i] = __float_as_uint(*p);
                 if (FOLD && a.stash && row < D) {
-                    float* keep = a.stash + ((int64_t)w * a.heads + h) * ssize + k0 * D + dv;
+                    float* keep = a.stash + ((int64_t)t.w * a.heads + h) * ssize + k0 * D + dv;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) keep[i * D] = __uint_as_float(r[i]);
                 }
@@ -484,7 +493,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             tmem_wait_st();
             return true;
         };
-        auto store_state = [&](float* dst) {
+        auto store_state = [&](float* dst, float factor) {
             if (row < D) {
 #pragma unroll 1
                 for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += 16) {
@@ -493,39 +502,47 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                     tmem_wait_ld(r);
                     float* to = dst + k0 * D + dv;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) to[i * D] = __uint_as_float(r[i]);
+                    for (int i = 0; i < 16; ++i) to[i * D] = __uint_as_float(r[i]) * factor;
                 }
             }
             __syncwarp();
         };
-        // S^T as a bf16 operand, and scaled by g^m
+        int in_frame = 0;  // chunks since the frame began
+        // S^T as a bf16 operand before a chunk of m tokens
         auto pass_state = [&](int m) {
-            const Factor f = m == kChunk ? whole : decay_factor(ld, m);
-            const uint64_t lo = pair(f.lo, f.lo), hi = pair(f.hi, f.hi);
             constexpr int N = D / kSplit < kCols ? D / kSplit : kCols;
+            if (frame > 0 && in_frame < frame) {
+                const float w = t.up[in_frame];
+                const uint64_t ww = pair(w, w);
 #pragma unroll 1
-            for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += N) {
-                uint32_t r[N], p[N / 2];
-                tmem_ld(r, lanes + P::kS + k0);
-                tmem_wait_ld(r);
+                for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += N) {
+                    uint32_t r[N], p[N / 2];
+                    tmem_ld(r, lanes + P::kS + k0);
+                    tmem_wait_ld(r);
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) p[i] = bf16x2_of(pair_of(r[2 * i], r[2 * i + 1]));
-                tmem_st(lanes + P::kB + k0 / 2, p);
-                if (f.hi == 1.0f) {
-#pragma unroll
-                    for (int i = 0; i < N / 2; ++i) {
-                        const uint64_t x = pair_of(r[2 * i], r[2 * i + 1]);
-                        const float2 y = unpair(fma2(x, lo, x));
-                        r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N / 2; ++i) {
-                        const float2 y = unpair(mul2(pair_of(r[2 * i], r[2 * i + 1]), hi));
-                        r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
-                    }
+                    for (int i = 0; i < N / 2; ++i) p[i] = bf16x2_of(mul2(pair_of(r[2 * i], r[2 * i + 1]), ww));
+                    tmem_st(lanes + P::kB + k0 / 2, p);
                 }
-                tmem_st(lanes + P::kS + k0, r);
+            } else {
+                // a fast head takes its operand before, a frame's end after scaling
+                in_frame = 0;
+                const Factor f = decay_factor(ld, frame == 0 ? m : frame * kChunk);
+                const uint64_t lo = pair(f.lo, f.lo), hi = pair(f.hi, f.hi);
+#pragma unroll 1
+                for (int k0 = part * (D / kSplit); k0 < (part + 1) * (D / kSplit); k0 += N) {
+                    uint32_t r[N], p[N / 2];
+                    tmem_ld(r, lanes + P::kS + k0);
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        const uint64_t x = pair_of(r[2 * i], r[2 * i + 1]), y = fma2(x, hi, mul2(x, lo));
+                        p[i] = bf16x2_of(frame == 0 ? x : y);
+                        const float2 z = unpair(y);
+                        r[2 * i] = __float_as_uint(z.x), r[2 * i + 1] = __float_as_uint(z.y);
+                    }
+                    tmem_st(lanes + P::kB + k0 / 2, p);
+                    tmem_st(lanes + P::kS + k0, r);
+                }
             }
             tmem_wait_st();
         };
@@ -537,14 +554,17 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
         auto split_values = [&](const Chunk& c, auto whole_chunk, auto three) {
             constexpr bool kFull = decltype(whole_chunk)::value, kThree = decltype(three)::value;
             const int r0 = rev ? kChunk - c.m : 0, shift = rev ? -r0 : kChunk - c.m;
-            const float age = FOLD ? decay_pow(ld, t1 - c.at - c.m) : 1.0f;
+            // what the terms are divided by, or have left to the fold's end
+            const float age = FOLD                    ? decay_pow(ld, t.t1 - c.at - c.m)
+                              : kFull || frame == 0 ? t.down[in_frame]
+                                                    : decay_pow(ld, -(in_frame * kChunk + c.m));
 #pragma unroll
             for (int i = 0; i < kChunk / kRowStep; ++i) {
                 const int r = v_row + i * kRowStep;
                 uint4 in = *reinterpret_cast<const uint4*>(v_at + stage * P::kTileBytes + i * kRowStep * 128);
                 float w = t.wrow[kFull ? r : (r + shift) & (kChunk - 1)];
                 if (!kFull && (unsigned)(r - r0) >= (unsigned)c.m) in = make_uint4(0, 0, 0, 0);
-                if (FOLD) w *= age;
+                w *= age;
                 const uint64_t ww = pair(w, w);
                 uint32_t* const x = &in.x;
                 uint32_t y[2][4], z[4];
@@ -575,7 +595,6 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
         }
         while (c.valid) {
             const bool full = c.m == kChunk;
-            const int r0 = rev ? kChunk - c.m : 0;  // rows r0 .. r0 + m - 1 hold the chunk
             // ---- w V ----
             wait_at(&t.v[stage], phase);
             if (full) {
@@ -596,11 +615,9 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 else split_values(c, No{}, No{});
             }
             arrive(&t.wv);
-            const Chunk c2 = next(c);
-            uint32_t inter[kCols];
             if (!FOLD) {
                 // ---- scores, and the state's part of the outputs ----
-                wait(&t.scores, scores);
+                wait_at(&t.scores, phase);
                 tc_fence_after();
                 if (row < kChunk) {
                     // a row, weighted by g^(i-j) (later tokens: zero)
@@ -624,54 +641,64 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                     }
                 }
                 if (!zero) {
-                    tmem_ld(inter, lanes + P::kR + part * kCols);
-                    tmem_wait_ld(inter);
+                    // the state's part, aged, back into the accumulator: the
+                    // values' product adds to it, and no registers hold it meanwhile
+                    uint32_t r[kCols];
+                    tmem_ld(r, lanes + P::kR + part * kCols);
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 4) {
+                        const float4 g = *reinterpret_cast<const float4*>(&t.age[part * kCols + i]);
+                        const float2 x = unpair(mul2(pair_of(r[i], r[i + 1]), pair(g.x, g.y)));
+                        const float2 y = unpair(mul2(pair_of(r[i + 2], r[i + 3]), pair(g.z, g.w)));
+                        r[i] = __float_as_uint(x.x), r[i + 1] = __float_as_uint(x.y);
+                        r[i + 2] = __float_as_uint(y.x), r[i + 3] = __float_as_uint(y.y);
+                    }
+                    tmem_st(lanes + P::kR + part * kCols, r);
+                    tmem_wait_st();
                 }
                 arrive(&t.ready);
             }
             // ---- the state after the chunk; that before the next one ----
-            wait(&t.update, update);
+            if (FOLD) wait(&t.update, update);
+            else wait_at(&t.update, phase);
             tc_fence_after();
             if (c.at + c.m == c.end) {
-                if (FOLD) store_state(a.carry + ((int64_t)w * a.heads + h) * ssize);
-                else if (a.s_out && c.end == c.stop) store_state(a.s_out + seq_state(c.n));
+                if (FOLD) store_state(a.carry + ((int64_t)t.w * a.heads + h) * ssize, 1.0f);
+                else if (a.s_out && c.end == c.stop)
+                    store_state(a.s_out + seq_state(c.n), frame == 0 ? 1.0f : decay_pow(ld, in_frame * kChunk + c.m));
             }
+            const int m = c.m, base = low(c);
+            c = next(c);
+            in_frame = c.first ? 0 : in_frame + 1;
             bool zero2 = false;
-            if (c2.valid && c2.first) zero2 = !load_state(c2);
+            if (c.valid && c.first) zero2 = !load_state(c);
             if (!FOLD) {
-                if (c2.valid && !zero2) pass_state(c2.m);
+                if (c.valid && !zero2) pass_state(c.m);
                 // ---- outputs ----
-                wait(&t.values, values);
+                wait_at(&t.values, phase);
                 tc_fence_after();
                 uint32_t r[kCols];
                 tmem_ld(r, lanes + P::kR + part * kCols);
                 tmem_wait_ld(r);
-                if (c2.valid) arrive(&t.state);  // the accumulator is free
+                if (c.valid) arrive(&t.state);  // the accumulator is free
                 if (row < D) {
-                    bf16* const out = o + (int64_t)(low(c) + part * kCols) * a.o_tok + dv;
+                    bf16* const out = static_cast<bf16*>(a.o) + h * a.o_head + (int64_t)(base + part * kCols) * a.o_tok + dv;
                     const int tok = (int)a.o_tok;
                     uint32_t z[kCols / 2];
 #pragma unroll
-                    for (int i = 0; i < kCols; i += 4) {
-                        const float4 g = *reinterpret_cast<const float4*>(&t.age[part * kCols + i]);
-                        uint64_t x = pair_of(r[i], r[i + 1]), y = pair_of(r[i + 2], r[i + 3]);
-                        if (!zero) {
-                            x = fma2(pair_of(inter[i], inter[i + 1]), pair(g.x, g.y), x);
-                            y = fma2(pair_of(inter[i + 2], inter[i + 3]), pair(g.z, g.w), y);
-                        }
-                        z[i / 2] = bf16x2_of(x), z[i / 2 + 1] = bf16x2_of(y);
-                    }
+                    for (int i = 0; i < kCols / 2; ++i) z[i] = bf16x2_of(pair_of(r[2 * i], r[2 * i + 1]));
                     auto put = [&](int i) {
                         const unsigned short x = (unsigned short)(i % 2 ? z[i / 2] >> 16 : z[i / 2]);
                         *reinterpret_cast<unsigned short*>(out + (int64_t)tok * i) = x;
                     };
-                    if (full) {
+                    if (m == kChunk) {
 #pragma unroll
                         for (int i = 0; i < kCols; ++i) put(i);
                     } else {
 #pragma unroll
                         for (int i = 0; i < kCols; ++i)
-                            if ((unsigned)(part * kCols + i - r0) < (unsigned)c.m) put(i);
+                            if ((unsigned)(part * kCols + i - (rev ? kChunk - m : 0)) < (unsigned)m) put(i);
                     }
                 }
                 __syncwarp();
@@ -679,7 +706,6 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             if (P::kStages == 2) stage ^= 1;
             if (stage == 0) phase ^= 1;
             zero = zero2;
-            c = c2;
         }
     }
     tc_fence_before();
