@@ -62,8 +62,9 @@
  * Logging. With AK_LOG set in the environment (and not "0"), every call
  *   prints one line to stderr naming the path it takes: the first-pass grid
  *   of a reduction, the dims kernel with its shape, tile and split, the
- *   scan kernel with its tile count, findall's tile count. The variable is
- *   read on every call.
+ *   scan kernel with its tile count, findall's tile count, the kernel and the
+ *   division of the token axis of linear attention. The variable is read on
+ *   every call.
  */
 #ifndef AK_H
 #define AK_H
@@ -464,7 +465,7 @@ ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t
  * equal calls give equal bits. In bf16 calls weighted scores and the state
  * are rounded to bf16 where they enter a product with q or v. A NaN or
  * infinity reaches the later tokens of its sequence and head, and may reach
- * up to 127 earlier ones.
+ * up to 63 earlier ones; other sequences and heads never.
  *
  * ak_linear_attention_backward: the gradients of sum(o * do) +
  * sum(state_out * dstate_out), from the forward call's inputs; dq, dk, dv as

@@ -40,28 +40,14 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 #define AK_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define AK_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
 
-// 32 consecutive columns of this warp's 32 lanes (warp w of a warpgroup: lanes
+// 16 consecutive columns of this warp's 32 lanes (warp w of a warpgroup: lanes
 // 32 w .. 32 w + 31): thread = lane, register = column. The registers hold
 // the values only after tmem_wait_ld(r).
-__device__ __forceinline__ void tmem_ld(uint32_t (&r)[32], uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : AK_R8(r, 0), AK_R8(r, 8), AK_R8(r, 16), AK_R8(r, 24)
-        : "r"(addr));
-}
 __device__ __forceinline__ void tmem_ld(uint32_t (&r)[16], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : AK_R8(r, 0), AK_R8(r, 8)
         : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        AK_W8(r, 0), AK_W8(r, 8), AK_W8(r, 16), AK_W8(r, 24)
-        : "memory");
 }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -75,10 +61,6 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[8]) {
 // Waits for this thread's TMEM loads; the registers pass through the
 // statement so that no use of them moves in front of it.
 #define AK_RW8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : AK_RW8(r, 0), AK_RW8(r, 8), AK_RW8(r, 16), AK_RW8(r, 24)::"memory");
-}
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : AK_RW8(r, 0), AK_RW8(r, 8)::"memory");
 }
@@ -130,25 +112,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t leader) {
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
         "r"(leader)
         : "memory");
-}
-
-// --------------------------------------------------------------------------
-// register-level products, for tiles too small for tcgen05
-// --------------------------------------------------------------------------
-
-// Four 8 x 8 bf16 matrices from shared memory: lane l gives the address of
-// row l % 8 of matrix l / 8.
-__device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-// c (16 x 8, f32) += a (16 x 16, bf16) b (16 x 8, bf16)
-__device__ __forceinline__ void mma_16x8x16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 }  // namespace ak

@@ -7,12 +7,12 @@
 // (a reversed call: g^i in place of g^(i+1), g^(m-j) of g^(m-1-j), see
 // linattn.cuh). Everything is held transposed, M = dv = the 128 TMEM lanes:
 //   P    = Q K^T                    64 x 64 scores, weighted, bf16
-//   O^T  = V^T P^T  and  S^T Q^T    one accumulator (R) in turn, combined in registers
+//   O^T  = S^T Q^T, aged, + V^T P^T in one accumulator (R)
 //   S^T += (w V)^T K                the float32 state, which stays in TMEM
-// so that S^T, read out once a chunk to be scaled, goes back to TMEM as the
-// bf16 A operand of its product with Q^T without passing shared memory, and
-// 256 columns (128 S, 64 bf16 S, 64 R) let two blocks share an SM: while one
-// waits for its chain of products the other uses the tensor core.
+// so that S^T, read out once a chunk, goes back to TMEM as the bf16 A operand
+// of its product with Q^T without passing shared memory, and 256 columns (128
+// S; 64 bf16 S, then the scores; 64 R) let two blocks share an SM: while one
+// waits for its chain of products the other works.
 //
 // Precision. Scores and the state are rounded to bf16 (once each) where they
 // enter a product whose result is rounded to bf16 anyway. The state itself is
@@ -21,19 +21,25 @@
 // 2^-25; the third is spent where the final state is asked for and the term
 // will still weigh more than 2^-8 in it.
 //
-// What bounds it: shared memory, whose 128 bytes a cycle serve the tensor
-// core's operands, TMA and the working warps alike. A chunk of 64 tokens at
-// D = 128 needs about 2000 cycles of it (tiles in 384, w V 384, its products
-// 512, scores 450, the other two products 320), against 2700 that its 64 KB
-// take from HBM at an SM's share.
+// What bounds it. Measured at 16384 tokens, 32 heads of 128 in 16 sequences:
+// 133 us, 4.3 TB/s of the tensors' bytes, 0.63 of the copy bandwidth; issue
+// slots half busy, the tensor pipe a fifth. Shared memory and TMEM accesses
+// pass one 128-byte-a-cycle path: a chunk needs about 1700 cycles of it for
+// TMEM (S read 512, its bf16 form 256, R 512, scores 128, and S written back
+// 512 when a frame ends) and 1900 for shared memory (tiles in 384, w V 384,
+// the products' operands 1100), against 2700 that its 64 KB take from HBM at
+// an SM's share. The rest is the chain of a chunk's steps at two blocks an
+// SM. What cost time: registers spilled in the chunk loop (154 us with 60
+// bytes spilled, 133 with none), branches around single elements (each
+// serialises its load), eight working warps (193 us against 166 at the time).
+// Loading the next tiles earlier made no difference.
 //
 // Seventeen warps: sixteen do the elementwise work (on TMEM, four to a
 // quarter of the lanes, a quarter of the columns each); the last issues
 // copies and products, each as soon as its operands are there and its target
 // is free. A chunk's chain is S^T Q^T, Q K^T, weights, V^T P^T; beside the
 // first two run the outputs of the chunk before and w V, beside the last the
-// state's pass for the next chunk; the update runs beside the weights, so the
-// key tile is free half a chunk before its successor is needed.
+// state's pass for the next chunk; the update runs beside the weights.
 //
 // A chunk of fewer than 64 tokens keeps its first row at row 0, in a reversed
 // call its last row at row 63: the weights then depend on the row alone.

@@ -340,6 +340,46 @@ def test_step_follows_the_prompt_form():
     _close(torch.cat(outs), want[20:], _bound("f32", [30], 64, want, mass)[20:], "o")
 
 
+@pytest.mark.parametrize("dtype,dim", [("f32", 64), ("bf16", 64)])
+def test_rows_further_apart_than_32_bits(dtype, dim):
+    """Token strides that put the last rows beyond element 2^31, inputs, outputs and gradients."""
+    t, step, h = 130, 17_000_000, 2
+    q, k, v, do, ld, off, _, _ = _inputs(13, dtype, [t], h, dim, dim, state=False)
+    d = DT[dtype]
+    buf = torch.empty(t * step, dtype=d, device="cuda")
+
+    def put(x, at):
+        y = torch.as_strided(buf, (t, h, dim), (step, dim, 1), at)
+        return y.copy_(_dev(x, d)) if x is not None else y
+
+    w = h * dim
+    a = [put(x, i * w) for i, x in enumerate((q, k, v))]
+    o, _ = ak.ak_linear_attention(*a, _dev(ld), out=put(None, 3 * w), scale=0.4)
+    want, _, mass = attention(q, k, v, ld, off, None, 0.4)
+    _close(o, want, _bound(dtype, [t], dim, want, mass), "o")
+    g = ak.ak_linear_attention_backward(put(do, 4 * w), *a, _dev(ld), dq=put(None, 5 * w), dk=put(None, 6 * w),
+                                        dv=put(None, 7 * w), scale=0.4)
+    want = attention_gradients(do, q, k, v, ld, off, None, None, 0.4)
+    mass = _mass_gradients(do, q, k, v, ld, off, None, None, 0.4)
+    for i in range(3):
+        _close(g[i], want[i], _bound(dtype, [t], dim, want[i], mass[i]), "gradient %d" % i)
+
+
+def test_step_in_a_pool_of_more_than_2_31_values():
+    h, dim, slots = 32, 128, 4200
+    pool = torch.empty(slots, h, dim, dim, device="cuda")
+    rng = np.random.default_rng(14)
+    q, k, v, _, ld, _, _, _ = _inputs(14, "f32", [2], h, dim, dim, state=False)
+    s = rng.normal(0, 1, (2, h, dim, dim)).astype(np.float32)
+    at = [slots - 1, 3]
+    pool[at] = _dev(s)
+    o = ak.ak_linear_attention_step(_dev(q), _dev(k), _dev(v), _dev(ld), pool,
+                                    slots=torch.tensor(at, dtype=torch.int32, device="cuda"))
+    new = np.exp(ld.astype(np.float64))[None, :, None, None] * s + k[..., :, None].astype(np.float64) * v[..., None, :]
+    _close(pool[at], new, 4 * 2.0**-24 * (np.abs(new) + np.abs(s)), "state")
+    _close(o, np.einsum("bhi,bhij->bhj", q, new), (dim + 16) * 2.0**-24 * np.einsum("bhi,bhij->bhj", np.abs(q), np.abs(new)), "o")
+
+
 def test_other_stream_graph_and_workspace():
     q, k, v, _, ld, off, s0, _ = _inputs(9, "bf16", [400], 2, 64, 64)
     d = torch.bfloat16

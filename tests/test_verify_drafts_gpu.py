@@ -123,3 +123,19 @@ def test_emitted_tokens_follow_the_target():
     t, _ = _run(p, q, d, None, rng.random((n, 1), dtype=np.float32), rng.exponential(1, (n, vocab)).astype(np.float32) + 1e-12)
     seen = np.bincount(t[:, 0], minlength=vocab)
     assert (np.abs(seen - n * p1) <= 5 * np.sqrt(n * p1 * (1 - p1)) + 1).all()
+
+
+def test_rows_beyond_2_31_values():
+    n, k, vocab = 3000, 5, 128000
+    p = torch.zeros(n, k + 1, vocab, device="cuda")
+    ps, qs, d, u, e = _case(15, 2, k, vocab)
+    p[-2:] = torch.tensor(ps, device="cuda")
+    drafts = torch.full((n, k), -1, dtype=torch.int32, device="cuda")
+    drafts[-2:] = torch.tensor(d, device="cuda").int()
+    uniform = torch.zeros(n, k, device="cuda")
+    uniform[-2:] = torch.tensor(u, device="cuda")
+    noise = torch.ones(n, vocab, device="cuda")
+    noise[-2:] = torch.tensor(e, device="cuda")
+    t, a = ak.ak_verify_drafts(p, drafts, uniform, noise)
+    _same((t[-2:].cpu().numpy(), a[-2:].cpu().numpy()), verify(ps, None, d, None, u, e))
+    assert (a[:-2] == 0).all() and (t[:-2] == -1).all()
