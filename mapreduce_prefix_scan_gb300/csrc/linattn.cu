@@ -34,8 +34,8 @@ __device__ __forceinline__ T from_f(float v) {
 // kTile that keeps g^-j below e^40. That is 2 DK fused operations a column
 // and token: bound by the FMA pipe for long inputs and by the chain of tokens
 // for few heads (hence the windows). 2049 tokens, 8 heads of 80, float32:
-// 91 us in three launches (fold 35, join 6, main 56 by themselves), where the
-// next tile's loads used to be waited for 145.
+// 85 us in three launches, where waiting for each tile's loads took 145 and
+// asking after every token whether a block ends 91.
 constexpr int kTile = 16;
 constexpr int kGroups = 4;
 constexpr int kThreads = 32 * kGroups;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
             for (int i = 0; i < kLoadsV; ++i) s_v[grp + i * kGroups][col] = fv[i] * s_inv[grp + i * kGroups];
             __syncthreads();
             if (tb + kTile < to) fetch(tb + kTile, (int)(to - tb - kTile < kTile ? to - tb - kTile : kTile));
-            for (int t = 0; t < m; ++t) {
+            auto token = [&](int t) {
                 const float vv = s_v[t][col];
                 float acc[4] = {};
 #pragma unroll
@@ -154,14 +154,26 @@ __global__ void __launch_bounds__(kThreads) k_tokens(const __grid_constant__ Bat
                     }
                 }
                 if (!FOLD) s_o[t][grp][col] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                const int e = t & (block - 1);
-                const bool last = tb + t == to - 1;
-                if (last || e == block - 1) {
-                    // after the last token a forward state is S, not g S
-                    const int power = last && !a.reverse ? e : e + 1;
-                    const Factor f = power == block ? whole : Factor{decay_pow(ld, power), 0.0f};
+            };
+            auto scale = [&](Factor f) {
 #pragma unroll
-                    for (int i = 0; i < R; ++i) s[i] = s[i] * f;
+                for (int i = 0; i < R; ++i) s[i] = s[i] * f;
+            };
+            if (block == kTile && tb + kTile < to) {
+                // a whole tile in one block, with more to come: nothing to ask between its tokens
+#pragma unroll 4
+                for (int t = 0; t < kTile; ++t) token(t);
+                scale(whole);
+            } else {
+                for (int t = 0; t < m; ++t) {
+                    token(t);
+                    const int e = t & (block - 1);
+                    const bool last = tb + t == to - 1;
+                    if (last || e == block - 1) {
+                        // after the last token a forward state is S, not g S
+                        const int power = last && !a.reverse ? e : e + 1;
+                        scale(power == block ? whole : Factor{decay_pow(ld, power), 0.0f});
+                    }
                 }
             }
             if (!FOLD) {
