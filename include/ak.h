@@ -479,6 +479,9 @@ ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t
  * [0, nslots) marks padding: its output is 0. Indices must not repeat.
  *
  * opts->target_blocks: windows the token axis is cut into (0 = automatic).
+ * opts->check also reports a bounded device-side wait that ran out (only a
+ * hardware fault makes one). Outputs overlap neither each other nor an input,
+ * except as stated.
  * ------------------------------------------------------------------------- */
 typedef struct ak_heads {
     void* data;
@@ -493,7 +496,9 @@ typedef struct ak_linattn {
     int32_t reserved; /* must be 0 */
 } ak_linattn;
 
-/* Enough for the forward and the backward pass of a shape. */
+/* Enough for the forward and the backward pass of a shape. Where it is 256
+ * bytes they only report a wait that ran out, and a call without opts->check
+ * may pass NULL. */
 ak_status ak_linear_attention_workspace_size(const ak_linattn* shape, const ak_opts* opts, size_t* bytes);
 ak_status ak_linear_attention(const ak_linattn* shape, const ak_heads* q, const ak_heads* k, const ak_heads* v,
                               const float* log_decay, const int32_t* offsets, const float* state_in,

@@ -441,7 +441,7 @@ static Division divide(const LinattnCall& c, int64_t slots, int64_t lanes) {
     const int64_t per = (units + want - 1) / want;
     d.window = per * unit;
     d.windows = std::max<int64_t>(1, (c.tokens + d.window - 1) / d.window);
-    if (c.windows > 0 || !c.offsets || c.seqs < 2 || c.seqs > kMaxWindows) return d;
+    if (c.windows > 0 || c.seqs < 2 || c.seqs > kMaxWindows) return d;
     const double work = (double)(units + c.seqs) * lanes / slots;  // steps of 64 tokens, spread evenly
     const double longest = (double)((c.max_len + unit - 1) / unit);
     // (the longest start first, see linattn_mma.cu)
@@ -476,14 +476,10 @@ static size_t carry_bytes(const LinattnCall& c, const Division& d, int calls) {
 
 size_t linattn_workspace(const LinattnCall& c, const DeviceInfo& dev) {
     size_t most = 0;
-    LinattnCall x = c;
-    for (int known = 0; known < 2; ++known) {  // the query does not know whether offsets will be given
-        const int32_t one = 0;
-        x.offsets = known ? &one : nullptr;
-        for (int calls = 1; calls <= la::kMaxCalls; calls += 2) {
-            most = std::max(most, carry_bytes(x, divide_chunks(x, dev, calls), calls));
-            most = std::max(most, carry_bytes(x, divide_tokens(x, dev, calls), calls));
-        }
+    for (int calls = 1; calls <= la::kMaxCalls; calls += 2) {  // the forward pass, the backward pass
+        if (c.dtype == AK_BF16 && c.dk == c.dv && (c.dk == 64 || c.dk == 128))
+            most = std::max(most, carry_bytes(c, divide_chunks(c, dev, calls), calls));
+        most = std::max(most, carry_bytes(c, divide_tokens(c, dev, calls), calls));  // rows that TMA cannot take
     }
     return kWsHeader + most;
 }

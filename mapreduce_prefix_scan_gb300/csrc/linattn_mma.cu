@@ -22,8 +22,8 @@
 // will still weigh more than 2^-8 in it.
 //
 // What bounds it. Measured at 16384 tokens, 32 heads of 128 in 16 sequences:
-// 133 us, 4.3 TB/s of the tensors' bytes, 0.63 of the copy bandwidth; issue
-// slots half busy, the tensor pipe a fifth. Shared memory and TMEM accesses
+// 130 us, 4.4 TB/s of the tensors' bytes, 0.65 of the copy bandwidth; issue
+// slots half busy, the tensor pipe a quarter. Shared memory and TMEM accesses
 // pass one 128-byte-a-cycle path: a chunk needs about 1700 cycles of it for
 // TMEM (S read 512, its bf16 form 256, R 512, scores 128, and S written back
 // 512 when a frame ends) and 1900 for shared memory (tiles in 384, w V 384,
@@ -142,11 +142,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -161,10 +156,16 @@ __device__ __forceinline__ uint32_t bf16x2_of(uint64_t x) {
     memcpy(&r, &y, 4);
     return r;
 }
-// The negatives of two bf16 values (a product with them is exact).
-__device__ __forceinline__ uint64_t minus_bf16x2(uint32_t x) {
-    const uint32_t n = x ^ 0x80008000u;
-    return pair(__uint_as_float(n << 16), __uint_as_float(n & 0xffff0000u));
+__device__ __forceinline__ uint64_t pair_of_bf16x2(uint32_t x) { return pair_of(x << 16, x & 0xffff0000u); }
+
+// A wait that the first poll did not end: until the limit, after which the
+// block records that it gave up (and no longer waits for anything).
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t phase, int* failed, const ChunkBatch& batch) {
+    if (*(volatile int*)failed) return;
+    if (!mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) {
+        *(volatile int*)failed = 1;
+        if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
+    }
 }
 
 template <int D, int PARTS, bool FOLD>
@@ -251,12 +252,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     // Bounded waits: a warp that gives up records it; all skip their further
     // waits and leave by the ordinary way.
     auto wait_at = [&](uint64_t* bar, uint32_t phase) {
-        if (!mbar_try_wait(bar, phase) && !*(volatile int*)&t.failed) {
-            if (!mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) {
-                *(volatile int*)&t.failed = 1;
-                if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
-            }
-        }
+        if (!mbar_try_wait(bar, phase)) wait_long(bar, phase, &t.failed, batch);
         __syncwarp();  // whole warps go on to the tensor-memory instructions
     };
     auto wait = [&](uint64_t* bar, uint32_t& phase) {
@@ -571,16 +567,16 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 float w = t.wrow[kFull ? r : (r + shift) & (kChunk - 1)];
                 if (!kFull && (unsigned)(r - r0) >= (unsigned)c.m) in = make_uint4(0, 0, 0, 0);
                 w *= age;
-                const uint64_t ww = pair(w, w);
+                const uint64_t ww = pair(w, w), minus = pair(-1.0f, -1.0f);
                 uint32_t* const x = &in.x;
                 uint32_t y[2][4], z[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    uint64_t wv = mul2(pair_of(x[e] << 16, x[e] & 0xffff0000u), ww);
+                    uint64_t wv = mul2(pair_of_bf16x2(x[e]), ww);
                     y[0][e] = bf16x2_of(wv);
-                    wv = add2(wv, minus_bf16x2(y[0][e]));
+                    wv = fma2(pair_of_bf16x2(y[0][e]), minus, wv);  // what the part leaves, exactly
                     y[1][e] = bf16x2_of(wv);
-                    if (kThree) z[e] = bf16x2_of(add2(wv, minus_bf16x2(y[1][e])));
+                    if (kThree) z[e] = bf16x2_of(fma2(pair_of_bf16x2(y[1][e]), minus, wv));
                 }
                 unsigned char* const to = v_at + (P::kW - P::kV) + i * kRowStep * 128;
                 *reinterpret_cast<uint4*>(to) = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
@@ -591,6 +587,13 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
         using Yes = std::true_type;
         using No = std::false_type;
         const float* const score_at = t.score + kChunk + row - part * kCols;
+        // a warp's quarter of the scores' columns may lie after all of its rows
+        const bool masked = rev ? (part + 1) * kCols <= row - lane : part * kCols > row - lane + 31;
+        const bool scored = row < kChunk && !masked;
+        if (!FOLD && row < kChunk && masked)
+#pragma unroll
+            for (int y = 0; y < kCols / 8; ++y)
+                *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, part * (kCols / 8) + y)) = make_uint4(0, 0, 0, 0);
         bool zero = true;
         if (c.valid) {
             zero = !load_state(c);
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 // ---- scores, and the state's part of the outputs ----
                 wait_at(&t.scores, phase);
                 tc_fence_after();
-                if (row < kChunk) {
+                if (scored) {
                     // a row, weighted by g^(i-j) (later tokens: zero)
                     uint32_t r[kCols];
                     tmem_ld(r, lanes + P::kX + part * kCols);
@@ -689,14 +692,14 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 tmem_wait_ld(r);
                 if (c.valid) arrive(&t.state);  // the accumulator is free
                 if (row < D) {
-                    bf16* const out = static_cast<bf16*>(a.o) + h * a.o_head + (int64_t)(base + part * kCols) * a.o_tok + dv;
-                    const int tok = (int)a.o_tok;
+                    bf16* out = static_cast<bf16*>(a.o) + h * a.o_head + (int64_t)(base + part * kCols) * a.o_tok + dv;
+                    const int64_t tok = a.o_tok;
                     uint32_t z[kCols / 2];
 #pragma unroll
                     for (int i = 0; i < kCols / 2; ++i) z[i] = bf16x2_of(pair_of(r[2 * i], r[2 * i + 1]));
                     auto put = [&](int i) {
                         const unsigned short x = (unsigned short)(i % 2 ? z[i / 2] >> 16 : z[i / 2]);
-                        *reinterpret_cast<unsigned short*>(out + (int64_t)tok * i) = x;
+                        *reinterpret_cast<unsigned short*>(out) = x, out += tok;
                     };
                     if (m == kChunk) {
 #pragma unroll
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                     } else {
 #pragma unroll
                         for (int i = 0; i < kCols; ++i)
-                            if ((unsigned)(part * kCols + i - (rev ? kChunk - m : 0)) < (unsigned)m) put(i);
+                            { if ((unsigned)(part * kCols + i - (rev ? kChunk - m : 0)) < (unsigned)m) put(i); else out += tok; }
                     }
                 }
                 __syncwarp();

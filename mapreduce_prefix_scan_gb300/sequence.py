@@ -251,6 +251,8 @@ def ak_linear_attention_workspace_size(tokens: int, heads: int, dk: int, dv: int
 def _workspace(a, device, workspace, opts, stream):
     b = ctypes.c_size_t()
     _check(_abi.load().ak_linear_attention_workspace_size(a, opts, b), "ak_linear_attention_workspace_size")
+    if b.value <= 256 and workspace is None and opts is None:
+        return None, 0
     return _workspace_ptr(b.value, device, workspace, stream)
 
 
