@@ -19,7 +19,9 @@
 // float32 and may be an output: w V is split into bf16 parts whose products
 // are exact in the float32 accumulation. Two parts keep 2^-17 of a term, three
 // 2^-25; the third is spent where the final state is asked for and the term
-// will still weigh more than 2^-8 in it.
+// will still weigh more than 2^-8 in it. The accumulation itself cuts off low
+// bits instead of rounding them: measured, 1.6e-8 of the state for each of
+// these products, over the tokens that the decay remembers.
 //
 // What bounds it. Measured at 16384 tokens, 32 heads of 128 in 16 sequences:
 // 130 us, 4.4 TB/s of the tensors' bytes, 0.65 of the copy bandwidth; issue
