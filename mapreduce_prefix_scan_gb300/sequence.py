@@ -137,11 +137,13 @@ def ak_batch_layout(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
         counts = _empty(2, torch.int32, dev, stream)
     else:
         p_cnt = _flat(counts, torch.int32, 2, "counts")
+    # a single row's stride says nothing; rows that overlap are the entry point's to refuse
+    stride = block_table.stride(0) if n > 1 else width
     wp, wb = None, 0
     if n > 4096 or workspace is not None:  # smaller batches need none
         wp, wb = _workspace_ptr(ak_batch_layout_workspace_size(n), dev, workspace, stream)
     _check(_abi.load().ak_batch_layout(
-        inputs[0], inputs[1], n, block_table.data_ptr(), max(block_table.stride(0), width), width, inputs[2], nfree,
+        inputs[0], inputs[1], n, block_table.data_ptr(), stride, width, inputs[2], nfree,
         block_size, max_tokens, p_off or offsets.data_ptr(), p_slots or slots.data_ptr(), p_pos or positions.data_ptr(),
         p_req or requests.data_ptr(), p_cnt or counts.data_ptr(), wp, wb, _opts(opts), _stream_of(stream, ctx_lens)),
         "ak_batch_layout")
