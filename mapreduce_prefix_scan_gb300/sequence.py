@@ -81,12 +81,14 @@ def _dense_rows(t):
 
 
 def _workspace_ptr(nbytes, device, workspace, stream):
+    """Pointer and size of a call's workspace, and the tensor that holds it: the caller keeps that until the entry
+    point has returned, or the allocator may hand the memory out before the last launch is queued."""
     if workspace is not None:
         size = workspace.numel() * workspace.element_size()
         _need(size >= nbytes, "workspace too small")
-        return workspace.data_ptr(), size
+        return workspace.data_ptr(), size, workspace
     ws = _empty(nbytes, torch.uint8, device, stream)
-    return ws.data_ptr(), nbytes
+    return ws.data_ptr(), nbytes, ws
 
 
 # ---------------------------------------------------------------------------
@@ -139,9 +141,9 @@ def ak_batch_layout(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
         p_cnt = _flat(counts, torch.int32, 2, "counts")
     # a single row's stride says nothing; rows that overlap are the entry point's to refuse
     stride = block_table.stride(0) if n > 1 else width
-    wp, wb = None, 0
+    wp, wb, _keep = None, 0, None
     if n > 4096 or workspace is not None:  # smaller batches need none
-        wp, wb = _workspace_ptr(ak_batch_layout_workspace_size(n), dev, workspace, stream)
+        wp, wb, _keep = _workspace_ptr(ak_batch_layout_workspace_size(n), dev, workspace, stream)
     _check(_abi.load().ak_batch_layout(
         inputs[0], inputs[1], n, block_table.data_ptr(), stride, width, inputs[2], nfree,
         block_size, max_tokens, p_off or offsets.data_ptr(), p_slots or slots.data_ptr(), p_pos or positions.data_ptr(),
@@ -254,7 +256,7 @@ def _workspace(a, device, workspace, opts, stream):
     b = ctypes.c_size_t()
     _check(_abi.load().ak_linear_attention_workspace_size(a, opts, b), "ak_linear_attention_workspace_size")
     if b.value <= 256 and workspace is None and opts is None:
-        return None, 0
+        return None, 0, None
     return _workspace_ptr(b.value, device, workspace, stream)
 
 
@@ -275,7 +277,7 @@ def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     op = _opts(opts)
     hq, hk, hv, ho = _heads(q, sk, dt, "q"), _heads(k, sk, dt, "k"), _heads(v, sv, dt, "v"), _heads(out, sv, dt, "out")
     s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(state_out, ss, "state_out")
-    wp, wb = _workspace(a, q.device, workspace, op, stream)
+    wp, wb, _keep = _workspace(a, q.device, workspace, op, stream)
     _check(_abi.load().ak_linear_attention(a, hq, hk, hv, ld, off, s0, ho, s1, wp, wb, op, _stream_of(stream, q)),
            "ak_linear_attention")
     return out, state_out
@@ -307,7 +309,7 @@ def ak_linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Ten
     hdo, hq, hk, hv, hdq, hdk, hdv = hs
     s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(dstate_out, ss, "dstate_out")
     s2 = _state_ptr(dstate, ss, "dstate")
-    wp, wb = _workspace(a, dev, workspace, op, stream)
+    wp, wb, _keep = _workspace(a, dev, workspace, op, stream)
     _check(_abi.load().ak_linear_attention_backward(a, hdo, hq, hk, hv, ld, off, s0, s1, hdq, hdk, hdv,
                                                     s2, wp, wb, op, _stream_of(stream, q)),
            "ak_linear_attention_backward")

@@ -2,6 +2,8 @@
 tensors stand in for device memory, and nothing is launched."""
 from __future__ import annotations
 
+import weakref
+
 import pytest
 import torch
 
@@ -87,3 +89,32 @@ def test_table_strides_are_handed_over_as_they_are(host):
     for table, stride in ((wide[:, 1:8], 9), (_int(5, 7), 7), (_int(1, 7), 7), (wide[:1, :4], 4), (wide[:, :1], 9)):
         _layout(table, table.shape[0])
         assert L.calls["ak_batch_layout"][4] == stride and L.calls["ak_batch_layout"][5] == table.shape[1]
+
+
+def _attention(t=70, h=2, d=64, dtype=torch.float32):
+    rows = lambda: _cuda(torch.zeros(t, h, d, dtype=dtype))
+    return rows(), rows(), rows(), _cuda(torch.zeros(h))
+
+
+CALLS = {
+    "ak_batch_layout": lambda: _layout(_int(5000, 3), 5000),
+    "ak_linear_attention": lambda: ak.ak_linear_attention(*_attention()),
+    "ak_linear_attention_backward": lambda: ak.ak_linear_attention_backward(_attention()[0], *_attention()),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_workspace_lives_until_the_entry_point_returns(host, monkeypatch, name):
+    """It is released to the allocator only after every launch has been queued."""
+    made, alive = [], []
+
+    def empty(size, dtype, device, stream):
+        t = _cuda(torch.empty(size, dtype=dtype))
+        if dtype is torch.uint8:
+            made.append((t.data_ptr(), weakref.ref(t)))
+        return t
+
+    monkeypatch.setattr(sequence, "_empty", empty)
+    host(_Library(sizes=4096, during=lambda _, args: alive.extend(ref() is not None for p, ref in made if p in args)))
+    CALLS[name]()
+    assert alive == [True]
