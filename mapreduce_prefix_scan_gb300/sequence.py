@@ -67,10 +67,10 @@ def _need(cond, message):
         raise ValueError(message)
 
 
-def _flat(t, dtype, numel, name):
-    """Pointer of a contiguous CUDA tensor of `numel` elements of `dtype`."""
-    if not (t.dtype is dtype and t.numel() == numel and t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name}: a contiguous CUDA tensor of {numel} {dtype} values is needed, "
+def _flat(t, dtype, numel, name, on):
+    """Pointer of a contiguous tensor of `numel` elements of `dtype` on the call's device (its index; -1: none)."""
+    if not (t.dtype is dtype and t.numel() == numel and t.get_device() == on >= 0 and t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous tensor of {numel} {dtype} values on the call's CUDA device is needed, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
@@ -80,11 +80,13 @@ def _dense_rows(t):
     return t.stride(-1) == 1 or t.shape[-1] <= 1 or t.numel() == 0
 
 
-def _workspace_ptr(nbytes, device, workspace, stream):
+def _workspace_ptr(nbytes, device, workspace, stream, on):
     """Pointer and size of a call's workspace, and the tensor that holds it: the caller keeps that until the entry
     point has returned, or the allocator may hand the memory out before the last launch is queued."""
     if workspace is not None:
         size = workspace.numel() * workspace.element_size()
+        _need(workspace.get_device() == on >= 0 and workspace.is_contiguous(),
+              "workspace: a contiguous tensor on the call's CUDA device is needed")
         _need(size >= nbytes, "workspace too small")
         return workspace.data_ptr(), size, workspace
     ws = _empty(nbytes, torch.uint8, device, stream)
@@ -112,38 +114,39 @@ def ak_batch_layout(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     order from ``free_blocks``. Token arrays hold ``max_tokens`` entries, -1 / 0
     / -1 past the batch's end."""
     n, width = block_table.shape
-    dev = ctx_lens.device
-    if not (block_table.dtype is torch.int32 and block_table.is_cuda and _dense_rows(block_table)):
-        raise ValueError("block_table: a [requests, width] int32 CUDA tensor with contiguous rows is needed")
+    dev, on = ctx_lens.device, ctx_lens.get_device()
+    if not (block_table.dtype is torch.int32 and block_table.get_device() == on >= 0 and _dense_rows(block_table)):
+        raise ValueError("block_table: a [requests, width] int32 tensor with contiguous rows on the call's CUDA device is "
+                         "needed")
     nfree = free_blocks.numel()
-    inputs = (_flat(ctx_lens, torch.int32, n, "ctx_lens"), _flat(new_lens, torch.int32, n, "new_lens"),
-              _flat(free_blocks, torch.int32, nfree, "free_blocks"))
+    inputs = (_flat(ctx_lens, torch.int32, n, "ctx_lens", on), _flat(new_lens, torch.int32, n, "new_lens", on),
+              _flat(free_blocks, torch.int32, nfree, "free_blocks", on))
     p_off = p_slots = p_pos = p_req = p_cnt = None
     if offsets is None:
         offsets = _empty(n + 1, torch.int32, dev, stream)
     else:
-        p_off = _flat(offsets, torch.int32, n + 1, "offsets")
+        p_off = _flat(offsets, torch.int32, n + 1, "offsets", on)
     if slots is None:
         slots = _empty(max_tokens, torch.int64, dev, stream)
     else:
-        p_slots = _flat(slots, torch.int64, max_tokens, "slots")
+        p_slots = _flat(slots, torch.int64, max_tokens, "slots", on)
     if positions is None:
         positions = _empty(max_tokens, torch.int32, dev, stream)
     else:
-        p_pos = _flat(positions, torch.int32, max_tokens, "positions")
+        p_pos = _flat(positions, torch.int32, max_tokens, "positions", on)
     if requests is None:
         requests = _empty(max_tokens, torch.int32, dev, stream)
     else:
-        p_req = _flat(requests, torch.int32, max_tokens, "requests")
+        p_req = _flat(requests, torch.int32, max_tokens, "requests", on)
     if counts is None:
         counts = _empty(2, torch.int32, dev, stream)
     else:
-        p_cnt = _flat(counts, torch.int32, 2, "counts")
+        p_cnt = _flat(counts, torch.int32, 2, "counts", on)
     # a single row's stride says nothing; rows that overlap are the entry point's to refuse
     stride = block_table.stride(0) if n > 1 else width
     wp, wb, _keep = None, 0, None
     if n > 4096 or workspace is not None:  # smaller batches need none
-        wp, wb, _keep = _workspace_ptr(ak_batch_layout_workspace_size(n), dev, workspace, stream)
+        wp, wb, _keep = _workspace_ptr(ak_batch_layout_workspace_size(n), dev, workspace, stream, on)
     _check(_abi.load().ak_batch_layout(
         inputs[0], inputs[1], n, block_table.data_ptr(), stride, width, inputs[2], nfree,
         block_size, max_tokens, p_off or offsets.data_ptr(), p_slots or slots.data_ptr(), p_pos or positions.data_ptr(),
@@ -168,33 +171,33 @@ def ak_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
     and how many drafts were kept."""
     n, k = draft_tokens.shape
     vocab = target_probs.shape[-1]
-    dev, dt = target_probs.device, target_probs.dtype
+    dev, dt, on = target_probs.device, target_probs.dtype, target_probs.get_device()
     kind = _FLOAT.get(dt)
     if kind is None:
         raise ValueError("probabilities are float32 or bfloat16")
-    if not (target_probs.shape == (n, k + 1, vocab) and target_probs.is_cuda and _dense_rows(target_probs)):
+    if not (target_probs.shape == (n, k + 1, vocab) and on >= 0 and _dense_rows(target_probs)):
         raise ValueError("target_probs: a [requests, k + 1, vocab] CUDA tensor with contiguous rows is needed")
-    if not (noise.dtype is torch.float32 and noise.shape == (n, vocab) and noise.is_cuda and _dense_rows(noise)):
-        raise ValueError("noise: a [requests, vocab] float32 CUDA tensor with contiguous rows is needed")
+    if not (noise.dtype is torch.float32 and noise.shape == (n, vocab) and noise.get_device() == on and _dense_rows(noise)):
+        raise ValueError("noise: a [requests, vocab] float32 tensor with contiguous rows on the target's device is needed")
     q, qs = None, (0, 0)
     if draft_probs is not None:
-        if not (draft_probs.dtype is dt and draft_probs.shape == (n, k, vocab) and draft_probs.is_cuda and
+        if not (draft_probs.dtype is dt and draft_probs.shape == (n, k, vocab) and draft_probs.get_device() == on and
                 _dense_rows(draft_probs)):
-            raise ValueError("draft_probs: a [requests, k, vocab] CUDA tensor of the target's type with contiguous "
-                             "rows is needed")
+            raise ValueError("draft_probs: a [requests, k, vocab] tensor of the target's type and device with "
+                             "contiguous rows is needed")
         q, qs = (draft_probs.data_ptr() if k else None), draft_probs.stride()
-    drafts = _flat(draft_tokens, torch.int32, n * k, "draft_tokens")
-    u = _flat(uniform, torch.float32, n * k, "uniform")
-    m = None if draft_counts is None else _flat(draft_counts, torch.int32, n, "draft_counts")
+    drafts = _flat(draft_tokens, torch.int32, n * k, "draft_tokens", on)
+    u = _flat(uniform, torch.float32, n * k, "uniform", on)
+    m = None if draft_counts is None else _flat(draft_counts, torch.int32, n, "draft_counts", on)
     p_tok = p_acc = None
     if tokens is None:
         tokens = _empty((n, k + 1), torch.int32, dev, stream)
     else:
-        p_tok = _flat(tokens, torch.int32, n * (k + 1), "tokens")
+        p_tok = _flat(tokens, torch.int32, n * (k + 1), "tokens", on)
     if accepted is None:
         accepted = _empty(n, torch.int32, dev, stream)
     else:
-        p_acc = _flat(accepted, torch.int32, n, "accepted")
+        p_acc = _flat(accepted, torch.int32, n, "accepted", on)
     ps = target_probs.stride()
     _check(_abi.load().ak_verify_drafts(
         target_probs.data_ptr(), ps[0], ps[1], q, qs[0], qs[1], kind, drafts, m, u, noise.data_ptr(), noise.stride(0),
@@ -207,19 +210,20 @@ def ak_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
 # linear attention with a decay for each head
 # ---------------------------------------------------------------------------
 
-def _heads(t: torch.Tensor, shape, dtype, name) -> ak_heads:
+def _heads(t: torch.Tensor, shape, dtype, name, on) -> ak_heads:
     s = t.stride()
-    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and (s[2] == 1 or shape[2] == 1)):
-        raise ValueError(f"{name}: a {list(shape)} {dtype} CUDA tensor with a contiguous last dimension is needed, "
-                         f"got {list(t.shape)} {t.dtype} with strides {list(s)} on {t.device}")
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == on >= 0 and (s[2] == 1 or shape[2] == 1)):
+        raise ValueError(f"{name}: a {list(shape)} {dtype} tensor on q's CUDA device with a contiguous last dimension is "
+                         f"needed, got {list(t.shape)} {t.dtype} with strides {list(s)} on {t.device}")
     return ak_heads(t.data_ptr(), s[0], s[1])
 
 
-def _state_ptr(t, shape, name):
+def _state_ptr(t, shape, name, on):
     if t is None:
         return None
-    if not (t.is_cuda and t.dtype == torch.float32 and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{name}: a contiguous {list(shape)} float32 CUDA tensor is needed, got {list(t.shape)} {t.dtype}")
+    if not (t.get_device() == on >= 0 and t.dtype == torch.float32 and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {list(shape)} float32 tensor on q's CUDA device is needed, "
+                         f"got {list(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -229,7 +233,7 @@ def _geometry(q, k, v, log_decay, offsets, scale, max_len):
     sk = q.shape
     t, h, dk = sk
     dv = v.shape[2]
-    dt = q.dtype
+    dt, on = q.dtype, q.get_device()
     kind = _FLOAT.get(dt)
     if kind is None:
         raise ValueError("q, k and v are float32 or bfloat16")
@@ -237,10 +241,10 @@ def _geometry(q, k, v, log_decay, offsets, scale, max_len):
     if offsets is not None:
         n = offsets.numel() - 1
         _need(n >= 0, "offsets: at least one value is needed")
-        off = _flat(offsets, torch.int32, n + 1, "offsets")
+        off = _flat(offsets, torch.int32, n + 1, "offsets", on)
     a = ak_linattn(t, n, max_len or 0, h, dk, dv, kind, scale, 0)
-    ld = _flat(log_decay, torch.float32, h, "log_decay")
-    return a, (t, h, dk), (t, h, dv), (n, h, dk, dv), dt, ld, off
+    ld = _flat(log_decay, torch.float32, h, "log_decay", on)
+    return a, (t, h, dk), (t, h, dv), (n, h, dk, dv), dt, ld, off, on
 
 
 def ak_linear_attention_workspace_size(tokens: int, heads: int, dk: int, dv: int, *, seqs: int = 1, max_len=None,
@@ -252,12 +256,12 @@ def ak_linear_attention_workspace_size(tokens: int, heads: int, dk: int, dv: int
     return b.value
 
 
-def _workspace(a, device, workspace, opts, stream):
+def _workspace(a, device, workspace, opts, stream, on):
     b = ctypes.c_size_t()
     _check(_abi.load().ak_linear_attention_workspace_size(a, opts, b), "ak_linear_attention_workspace_size")
     if b.value <= 256 and workspace is None and opts is None:
         return None, 0, None
-    return _workspace_ptr(b.value, device, workspace, stream)
+    return _workspace_ptr(b.value, device, workspace, stream, on)
 
 
 def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
@@ -269,15 +273,15 @@ def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     every head over packed sequences (``offsets`` int32, None: one sequence),
     from ``state`` [sequences, heads, dk, dv] float32 or zero. Returns ``(out,
     state_out)``, the latter None unless given or asked for by ``final_state``."""
-    a, sk, sv, ss, dt, ld, off = _geometry(q, k, v, log_decay, offsets, scale, max_len)
+    a, sk, sv, ss, dt, ld, off, on = _geometry(q, k, v, log_decay, offsets, scale, max_len)
     if out is None:
         out = _empty(sv, dt, q.device, stream)
     if state_out is None and final_state:
         state_out = _empty(ss, torch.float32, q.device, stream)
     op = _opts(opts)
-    hq, hk, hv, ho = _heads(q, sk, dt, "q"), _heads(k, sk, dt, "k"), _heads(v, sv, dt, "v"), _heads(out, sv, dt, "out")
-    s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(state_out, ss, "state_out")
-    wp, wb, _keep = _workspace(a, q.device, workspace, op, stream)
+    hq, hk, hv, ho = [_heads(x, s, dt, n, on) for x, s, n in ((q, sk, "q"), (k, sk, "k"), (v, sv, "v"), (out, sv, "out"))]
+    s0, s1 = _state_ptr(state, ss, "state", on), _state_ptr(state_out, ss, "state_out", on)
+    wp, wb, _keep = _workspace(a, q.device, workspace, op, stream, on)
     _check(_abi.load().ak_linear_attention(a, hq, hk, hv, ld, off, s0, ho, s1, wp, wb, op, _stream_of(stream, q)),
            "ak_linear_attention")
     return out, state_out
@@ -293,7 +297,7 @@ def ak_linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Ten
     state, from the output's gradient ``do`` and the final state's
     ``dstate_out`` (or None). Returns ``(dq, dk, dv, dstate)``; ``dstate`` is
     None where the forward call had no ``state`` and none is given."""
-    a, sk, sv, ss, dt, ld, off = _geometry(q, k, v, log_decay, offsets, scale, max_len)
+    a, sk, sv, ss, dt, ld, off, on = _geometry(q, k, v, log_decay, offsets, scale, max_len)
     dev = q.device
     if dq is None:
         dq = _empty(sk, dt, dev, stream)
@@ -304,12 +308,12 @@ def ak_linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Ten
     if dstate is None and state is not None:
         dstate = _empty(ss, torch.float32, dev, stream)
     op = _opts(opts)
-    hs = [_heads(x, s, dt, n) for x, s, n in ((do, sv, "do"), (q, sk, "q"), (k, sk, "k"), (v, sv, "v"),
+    hs = [_heads(x, s, dt, n, on) for x, s, n in ((do, sv, "do"), (q, sk, "q"), (k, sk, "k"), (v, sv, "v"),
                                               (dq, sk, "dq"), (dk, sk, "dk"), (dv, sv, "dv"))]
     hdo, hq, hk, hv, hdq, hdk, hdv = hs
-    s0, s1 = _state_ptr(state, ss, "state"), _state_ptr(dstate_out, ss, "dstate_out")
-    s2 = _state_ptr(dstate, ss, "dstate")
-    wp, wb, _keep = _workspace(a, dev, workspace, op, stream)
+    s0, s1 = _state_ptr(state, ss, "state", on), _state_ptr(dstate_out, ss, "dstate_out", on)
+    s2 = _state_ptr(dstate, ss, "dstate", on)
+    wp, wb, _keep = _workspace(a, dev, workspace, op, stream, on)
     _check(_abi.load().ak_linear_attention_backward(a, hdo, hq, hk, hv, ld, off, s0, s1, hdq, hdk, hdv,
                                                     s2, wp, wb, op, _stream_of(stream, q)),
            "ak_linear_attention_backward")
@@ -323,13 +327,13 @@ def ak_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     ``state[slots]`` ([slots, heads, dk, dv] float32; ``slots`` int32, None: request
     b uses state[b]) in place and returns the outputs. Slots outside the pool
     mark padding and give zeros."""
-    a, sk, sv, ss, dt, ld, _ = _geometry(q, k, v, log_decay, None, scale, None)
+    a, sk, sv, ss, dt, ld, _, on = _geometry(q, k, v, log_decay, None, scale, None)
     if out is None:
         out = _empty(sv, dt, q.device, stream)
-    hq, hk, hv, ho = _heads(q, sk, dt, "q"), _heads(k, sk, dt, "k"), _heads(v, sv, dt, "v"), _heads(out, sv, dt, "out")
+    hq, hk, hv, ho = [_heads(x, s, dt, n, on) for x, s, n in ((q, sk, "q"), (k, sk, "k"), (v, sv, "v"), (out, sv, "out"))]
     pool = state.shape[0]
-    sp = _state_ptr(state, (pool,) + ss[1:], "state")
-    at = None if slots is None else _flat(slots, torch.int32, sk[0], "slots")
+    sp = _state_ptr(state, (pool,) + ss[1:], "state", on)
+    at = None if slots is None else _flat(slots, torch.int32, sk[0], "slots", on)
     _need(slots is not None or pool >= sk[0], "state: one matrix for each request and head is needed")
     _check(_abi.load().ak_linear_attention_step(a, hq, hk, hv, ld, sp, at, pool, ho, _opts(opts),
                                                 _stream_of(stream, q)),

@@ -13,7 +13,7 @@ from mapreduce_prefix_scan_gb300 import sequence
 
 class _Cuda(torch.Tensor):
     """Host memory under a device's name."""
-    where = torch.device("cuda", 0)
+    index = 0
 
     @property
     def is_cuda(self):
@@ -21,7 +21,14 @@ class _Cuda(torch.Tensor):
 
     @property
     def device(self):
-        return self.where
+        return torch.device("cuda", self.index)
+
+    def get_device(self):
+        return self.index
+
+
+class _OtherCuda(_Cuda):
+    index = 1
 
 
 def _cuda(t):
@@ -118,3 +125,55 @@ def test_a_workspace_lives_until_the_entry_point_returns(host, monkeypatch, name
     host(_Library(sizes=4096, during=lambda _, args: alive.extend(ref() is not None for p, ref in made if p in args)))
     CALLS[name]()
     assert alive == [True]
+
+
+def _verify(n=3, k=2, vocab=11, **kw):
+    a = dict(target_probs=torch.zeros(n, k + 1, vocab), draft_tokens=torch.zeros(n, k, dtype=torch.int32),
+             uniform=torch.zeros(n, k), noise=torch.ones(n, vocab), draft_probs=torch.zeros(n, k, vocab),
+             draft_counts=torch.zeros(n, dtype=torch.int32), tokens=torch.zeros(n, k + 1, dtype=torch.int32),
+             accepted=torch.zeros(n, dtype=torch.int32))
+    return {name: kw.get(name, _cuda(x)) for name, x in a.items()}
+
+
+def _named_calls():
+    """Each entry point with all of its tensor arguments by name."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    rows, state = (lambda: torch.zeros(9, 2, 64)), (lambda: torch.zeros(2, 2, 64, 64))
+    qkv = lambda: dict(q=rows(), k=rows(), v=rows(), log_decay=torch.zeros(2))
+    ws = lambda: torch.zeros(4096, dtype=torch.uint8)
+    return {
+        "ak_batch_layout": (dict(ctx_lens=i32(3), new_lens=i32(3), block_table=i32(3, 4), free_blocks=i32(5), offsets=i32(4),
+                                 slots=torch.zeros(8, dtype=torch.int64), positions=i32(8), requests=i32(8), counts=i32(2),
+                                 workspace=ws()), dict(block_size=16, max_tokens=8)),
+        "ak_verify_drafts": (_verify(), {}),
+        "ak_linear_attention": (dict(qkv(), offsets=i32(3), state=state(), out=rows(), state_out=state(), workspace=ws()), {}),
+        "ak_linear_attention_backward": (dict(qkv(), do=rows(), offsets=i32(3), state=state(), dstate_out=state(), dq=rows(),
+                                              dk=rows(), dv=rows(), dstate=state(), workspace=ws()), {}),
+        "ak_linear_attention_step": (dict(qkv(), state=torch.zeros(9, 2, 64, 64), slots=i32(9), out=rows()), {}),
+    }
+
+
+ARGUMENTS = [(call, name) for call, (tensors, _) in _named_calls().items() for name in tensors]
+
+
+@pytest.mark.parametrize("call,name", ARGUMENTS)
+def test_an_argument_on_another_device_is_refused(host, call, name):
+    L = host(_Library())
+    tensors, rest = _named_calls()[call]
+    tensors = {n: _cuda(t) for n, t in tensors.items()}
+    getattr(ak, call)(**tensors, **rest)  # all on one device
+    assert L.calls.pop(call)
+    for stray in (tensors[name].as_subclass(torch.Tensor), tensors[name].as_subclass(_OtherCuda)):
+        with pytest.raises(ValueError):
+            getattr(ak, call)(**dict(tensors, **{name: stray}), **rest)
+    assert not L.calls
+
+
+def test_a_workspace_that_is_not_its_own_memory_is_refused(host):
+    L = host(_Library(sizes=4096))
+    for ws in (_cuda(torch.zeros(1, dtype=torch.uint8)).expand(4096), _cuda(torch.zeros(8192, dtype=torch.uint8))[::2]):
+        with pytest.raises(ValueError):
+            ak.ak_linear_attention(*_attention(), workspace=ws)
+    assert not L.calls
+    ak.ak_linear_attention(*_attention(), workspace=_cuda(torch.zeros(4096, dtype=torch.uint8)))
+    assert L.calls
