@@ -75,6 +75,14 @@ def _flat(t, dtype, numel, name, on):
     return t.data_ptr()
 
 
+def _matrix(t, dtype, rows, cols, name, on):
+    """_flat for [rows, cols] (or its flat form): another shape of as many elements would be read in the wrong order."""
+    at = _flat(t, dtype, rows * cols, name, on)
+    if t.shape != (rows, cols) and t.dim() != 1 and rows > 1 and cols > 1:
+        raise ValueError(f"{name}: the shape {[rows, cols]} is needed, got {list(t.shape)}")
+    return at
+
+
 def _dense_rows(t):
     """Whether the last dimension is contiguous (strides of empty and one-element dimensions mean nothing)."""
     return t.stride(-1) == 1 or t.shape[-1] <= 1 or t.numel() == 0
@@ -187,13 +195,13 @@ def ak_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
                              "contiguous rows is needed")
         q, qs = (draft_probs.data_ptr() if k else None), draft_probs.stride()
     drafts = _flat(draft_tokens, torch.int32, n * k, "draft_tokens", on)
-    u = _flat(uniform, torch.float32, n * k, "uniform", on)
+    u = _matrix(uniform, torch.float32, n, k, "uniform", on)
     m = None if draft_counts is None else _flat(draft_counts, torch.int32, n, "draft_counts", on)
     p_tok = p_acc = None
     if tokens is None:
         tokens = _empty((n, k + 1), torch.int32, dev, stream)
     else:
-        p_tok = _flat(tokens, torch.int32, n * (k + 1), "tokens", on)
+        p_tok = _matrix(tokens, torch.int32, n, k + 1, "tokens", on)
     if accepted is None:
         accepted = _empty(n, torch.int32, dev, stream)
     else:

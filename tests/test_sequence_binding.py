@@ -135,6 +135,20 @@ def _verify(n=3, k=2, vocab=11, **kw):
     return {name: kw.get(name, _cuda(x)) for name, x in a.items()}
 
 
+def test_arrays_of_another_shape_with_as_many_elements_are_refused(host):
+    """[drafts, requests] in place of [requests, drafts] would be read in the wrong order."""
+    L = host(_Library())
+    for name, shape in (("uniform", (2, 3)), ("tokens", (1, 9)), ("uniform", (3, 2, 1)), ("tokens", (9, 1))):
+        good = _verify()[name]
+        with pytest.raises(ValueError):
+            ak.ak_verify_drafts(**_verify(**{name: good.reshape(shape)}))
+    assert not L.calls
+    ak.ak_verify_drafts(**_verify())
+    ak.ak_verify_drafts(**_verify(uniform=_cuda(torch.zeros(6)), tokens=_cuda(torch.zeros(9, dtype=torch.int32))))  # flat
+    ak.ak_verify_drafts(**_verify(k=1, uniform=_cuda(torch.zeros(1, 3))))  # one order only
+    assert L.calls
+
+
 def _named_calls():
     """Each entry point with all of its tensor arguments by name."""
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
