@@ -272,6 +272,51 @@ def _workspace(a, device, workspace, opts, stream, on):
     return _workspace_ptr(b.value, device, workspace, stream, on)
 
 
+def _tracked(*tensors) -> bool:
+    """Whether autograd records what is done with any of these (None allowed)."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class _Attention(torch.autograd.Function):
+    """ak_linear_attention with its gradients in the graph."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, state, offsets, rest, final_state, workspace):
+        ctx.save_for_backward(q, k, v, log_decay, state, offsets)
+        ctx.rest = rest
+        ctx.set_materialize_grads(False)
+        return ak_linear_attention(q, k, v, log_decay, state=state, offsets=offsets, final_state=final_state,
+                                   workspace=workspace, **rest)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, dstate_out):
+        q, k, v, log_decay, state, offsets = ctx.saved_tensors
+        if ctx.needs_input_grad[3]:
+            raise RuntimeError("ak_linear_attention has no gradient for log_decay: pass log_decay.detach()")
+        if do is None:
+            do = torch.zeros_like(v)
+        elif not _dense_rows(do):
+            do = do.contiguous()
+        dstate_out = None if dstate_out is None else dstate_out.contiguous()
+        grads = ak_linear_attention_backward(do, q, k, v, log_decay, state=state, offsets=offsets, dstate_out=dstate_out,
+                                             **ctx.rest)
+        return (*grads[:3], None, grads[3], None, None, None, None)
+
+
+class _Untracked(torch.autograd.Function):
+    """Results of a call that has no gradient, for inputs that ask for one: a backward pass through them is an error."""
+
+    @staticmethod
+    def forward(ctx, results, why, *inputs):
+        ctx.why = why
+        return tuple(None if t is None else t.detach() for t in results)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(ctx.why)
+
+
 def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
                         offsets: torch.Tensor | None = None, state: torch.Tensor | None = None, scale: float = 1.0,
                         max_len: int | None = None, out: torch.Tensor | None = None,
@@ -280,7 +325,19 @@ def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     """``S_t = exp(log_decay) S_{t-1} + k_t v_t^T``, ``o_t = scale S_t^T q_t`` for
     every head over packed sequences (``offsets`` int32, None: one sequence),
     from ``state`` [sequences, heads, dk, dv] float32 or zero. Returns ``(out,
-    state_out)``, the latter None unless given or asked for by ``final_state``."""
+    state_out)``, the latter None unless given or asked for by ``final_state``.
+    Gradients of q, k, v and ``state`` are recorded as usual, of results that the
+    call allocates on the current stream; ``log_decay`` has none."""
+    if _tracked(q, k, v, log_decay, state):
+        if out is None and state_out is None and stream is None:
+            return _Attention.apply(q, k, v, log_decay, state, offsets, dict(scale=scale, max_len=max_len, opts=opts),
+                                    final_state, workspace)
+        with torch.no_grad():
+            results = ak_linear_attention(q, k, v, log_decay, offsets=offsets, state=state, scale=scale, max_len=max_len,
+                                          out=out, state_out=state_out, final_state=final_state, workspace=workspace,
+                                          opts=opts, stream=stream)
+        return _Untracked.apply(results, "ak_linear_attention into given memory or on a given stream is not recorded: "
+                                "no gradient", q, k, v, log_decay, state)
     a, sk, sv, ss, dt, ld, off, on = _geometry(q, k, v, log_decay, offsets, scale, max_len)
     if out is None:
         out = _empty(sv, dt, q.device, stream)
@@ -334,7 +391,12 @@ def ak_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     """One token of each of ``q.shape[0]`` requests: updates the matrices
     ``state[slots]`` ([slots, heads, dk, dv] float32; ``slots`` int32, None: request
     b uses state[b]) in place and returns the outputs. Slots outside the pool
-    mark padding and give zeros."""
+    mark padding and give zeros. It has no gradient."""
+    if _tracked(q, k, v, log_decay, state):
+        with torch.no_grad():
+            out = ak_linear_attention_step(q, k, v, log_decay, state, slots=slots, scale=scale, out=out, opts=opts,
+                                           stream=stream)
+        return _Untracked.apply((out,), "ak_linear_attention_step has no gradient", q, k, v, log_decay, state)[0]
     a, sk, sv, ss, dt, ld, _, on = _geometry(q, k, v, log_decay, None, scale, None)
     if out is None:
         out = _empty(sv, dt, q.device, stream)

@@ -59,6 +59,10 @@ def host(monkeypatch):
     """The binding over host memory; the fixture's value installs a stand-in for the library."""
     monkeypatch.setattr(sequence, "_empty", lambda size, dtype, device, stream: _cuda(torch.empty(size, dtype=dtype)))
     monkeypatch.setattr(sequence, "_stream_of", lambda stream, t: 0)
+    # (autograd's engine hands on plain tensors)
+    backward, named = sequence.ak_linear_attention_backward, lambda t: None if t is None else _cuda(t)
+    monkeypatch.setattr(sequence, "ak_linear_attention_backward", lambda do, *a, dstate_out=None, **kw: backward(
+        named(do), *a, dstate_out=named(dstate_out), **kw))
 
     def use(library):
         monkeypatch.setattr(sequence._abi, "load", lambda: library)
@@ -191,3 +195,69 @@ def test_a_workspace_that_is_not_its_own_memory_is_refused(host):
     assert not L.calls
     ak.ak_linear_attention(*_attention(), workspace=_cuda(torch.zeros(4096, dtype=torch.uint8)))
     assert L.calls
+
+
+def _backward(*results):
+    """A gradient of ones, with strides of zero as that of a sum has."""
+    torch.autograd.backward(results, [_cuda(torch.ones(1)).expand(x.shape) for x in results])
+
+
+def _with_grad(*tensors):
+    return [t.requires_grad_() for t in tensors]
+
+
+def test_gradients_are_recorded(host):
+    """A call on tensors that ask for gradients runs the backward entry point on its inputs, its output's gradient and
+    its final state's."""
+    L = host(_Library(sizes=4096))
+    q, k, v, ld = _attention()
+    _with_grad(q, k, v)
+    state = _cuda(torch.zeros(1, 2, 64, 64)).requires_grad_()
+    o, final = ak.ak_linear_attention(q, k, v, ld, state=state, final_state=True, scale=0.5, max_len=64)
+    assert o.requires_grad and final.requires_grad and "ak_linear_attention_backward" not in L.calls
+    _backward(o, final)
+    a = L.calls["ak_linear_attention_backward"]
+    assert (a[0].scale, a[0].max_len, a[0].tokens) == (0.5, 64, 70) and a[1].token_stride == 128
+    assert [x.data for x in a[2:5]] == [x.data_ptr() for x in (q, k, v)] and a[5] == ld.data_ptr() and a[7] == state.data_ptr()
+    assert a[8] is not None and a[12] is not None
+    assert [x.data for x in a[9:12]] == [x.grad.data_ptr() for x in (q, k, v)]
+    assert all(x.grad.shape == x.shape for x in (q, k, v, state))
+    # an output alone; a final state alone
+    for pick in (0, 1):
+        L.calls.clear()
+        got = ak.ak_linear_attention(q, k, v, ld, final_state=True)
+        _backward(got[pick])
+        assert L.calls["ak_linear_attention_backward"][1].data and (L.calls["ak_linear_attention_backward"][8] is None) == (pick == 0)
+
+
+def test_a_shared_head_gets_the_sum_of_its_gradients(host):
+    host(_Library())
+    q, k, v, ld = _attention(h=4)
+    one = _cuda(torch.zeros(70, 1, 64)).requires_grad_()
+    o, _ = ak.ak_linear_attention(q, one.expand(70, 4, 64), v, ld)
+    _backward(o)
+    assert one.grad.shape == one.shape
+
+
+def test_what_has_no_gradient_says_so(host):
+    host(_Library())
+    q, k, v, ld = _attention()
+    _with_grad(q, k, v)
+    out, state = _cuda(torch.empty(70, 2, 64)), _cuda(torch.zeros(1, 2, 64, 64))
+    pool = _cuda(torch.zeros(70, 2, 64, 64))
+    for make in (lambda: ak.ak_linear_attention(q, k, v, ld, out=out)[0],
+                 lambda: ak.ak_linear_attention(q, k, v, ld, state=state, state_out=state)[0],
+                 lambda: ak.ak_linear_attention(q, k, v, ld, stream=7)[0],
+                 lambda: ak.ak_linear_attention(q, k, v, ld.clone().requires_grad_())[0],
+                 lambda: ak.ak_linear_attention_step(q, k, v, ld, pool),
+                 lambda: ak.ak_linear_attention_step(q, k, v, ld, pool, out=out)):
+        o = make()
+        assert o.requires_grad
+        with pytest.raises(RuntimeError, match="gradient"):
+            _backward(o)
+    assert not (out.requires_grad or state.requires_grad or pool.requires_grad)
+    # without a record nothing changes
+    with torch.no_grad():
+        assert ak.ak_linear_attention(q, k, v, ld, out=out)[0] is out
+        assert ak.ak_linear_attention_step(q, k, v, ld, pool, out=out) is out
+    assert ak.ak_linear_attention(*_attention(), out=out)[0] is out
