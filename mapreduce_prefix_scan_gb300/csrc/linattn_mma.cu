@@ -111,7 +111,7 @@ struct Plan {
     static constexpr int kW = kP + (FOLD ? 0 : kChunk * kChunk * 2);
     static constexpr int kSmall = kW + PARTS * kTileBytes;
     static constexpr int kUsed = kSmall + (int)(FOLD ? offsetof(Small, age) : sizeof(Small));
-    // two blocks an SM share its TMEM: no third one may become resident
+    // two blocks of the main pass share an SM's TMEM: a third would only wait for it
     static constexpr int kSmem = kUsed < 80 * 1024 && !FOLD ? 80 * 1024 : kUsed;
     // columns: S, its bf16 form, accumulator, scores (over the bf16 form at D = 128)
     static constexpr uint32_t kS = 0, kB = D, kR = D + D / 2, kX = D == 128 ? kB : kR + 64;
@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     const uint32_t sbase = smem_addr(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = tid % kWarp;
     const int h = blockIdx.x;
-    if (FOLD) griddep_launch_dependents();
     if (tid == 0) t.w = blockIdx.y;
     if (!FOLD && a.ranked) {
         // block w takes the w-th longest sequence: the long ones start first
@@ -250,6 +249,9 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, t.tmem, 0);
+    // Only now: the main pass's blocks take TMEM before they wait for this
+    // pass, which must not wait for theirs.
+    if (FOLD) griddep_launch_dependents();
 
     // Bounded waits: a warp that gives up records it; all skip their further
     // waits and leave by the ordinary way.
