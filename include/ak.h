@@ -143,7 +143,8 @@ typedef struct ak_opts {
     int32_t reserved;         /* must be 0 */
     int64_t wait_limit_ns;    /* bound of each device-side wait of the scan; 0 = 1 s. Without
                                  `check` a wait that runs out is not reported by the call
-                                 itself: read it with ak_scan_status */
+                                 itself: read it with ak_scan_status. (Linear attention
+                                 takes at least 0.1 s, see there.) */
     int64_t debug_skip_publish_tile; /* fault injection for tests: the scan tile with this
                                  index never publishes its state, so its successors'
                                  bounded waits run out; -1 = off */
@@ -484,9 +485,12 @@ ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t
  * [0, nslots) marks padding: its output is 0. Indices must not repeat.
  *
  * opts->target_blocks: windows the token axis is cut into (0 = automatic).
- * opts->check also reports a bounded device-side wait that ran out (only a
- * hardware fault makes one). Outputs overlap neither each other nor an input,
- * except as stated.
+ * opts->check also reports a bounded device-side wait that ran out
+ * (AK_ERR_TIMEOUT; the results are then undefined). The waits are for a
+ * block's own copies and products, microseconds apart: one runs out if the
+ * device faults, or is taken away from the block for longer than
+ * opts->wait_limit_ns (0.1 s at least). Outputs overlap neither each other nor
+ * an input, except as stated.
  * ------------------------------------------------------------------------- */
 typedef struct ak_heads {
     void* data;

@@ -74,6 +74,11 @@ struct ChunkBatch {
     uint64_t wait_limit_ns;
 };
 
+// A wait here is for this block's own copies and products: microseconds, or as
+// long as the device is taken away from the block. A shorter limit than this
+// would end sound calls.
+constexpr uint64_t kLeastWait = 100'000'000;
+
 constexpr int kFrame = 16;  // chunks of a frame at most
 
 // Barriers and tables of a block.
@@ -82,6 +87,7 @@ struct Small {
     // the state, the scores, of the values, the update), working warps (state
     // operand ready and accumulator read, w V ready, scores ready)
     uint64_t qk[2], v[2], inter, scores, values, update, state, wv, ready;
+    uint64_t drained;  // everything issued before a wait ran out
     int64_t count;
     uint32_t tmem;
     int failed, w, t0, t1;  // w: window or sequence of the block, t0, t1: its span
@@ -161,13 +167,14 @@ __device__ __forceinline__ uint32_t bf16x2_of(uint64_t x) {
 __device__ __forceinline__ uint64_t pair_of_bf16x2(uint32_t x) { return pair_of(x << 16, x & 0xffff0000u); }
 
 // A wait that the first poll did not end: until the limit, after which the
-// block records that it gave up (and no longer waits for anything).
-__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t phase, int* failed, const ChunkBatch& batch) {
-    if (*(volatile int*)failed) return;
-    if (!mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) {
-        *(volatile int*)failed = 1;
-        if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
-    }
+// block records that it gave up, and none of its waits waits any longer.
+// Whether what was waited for is there.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t phase, int* failed, const ChunkBatch& batch) {
+    if (*(volatile int*)failed) return false;
+    if (mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) return true;
+    *(volatile int*)failed = 1;
+    if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
+    return false;
 }
 
 template <int D, int PARTS, bool FOLD>
@@ -225,6 +232,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             mbar_init(&t.state, kWork / kWarp);
             mbar_init(&t.wv, kWork / kWarp);
             mbar_init(&t.ready, kWork / kWarp);
+            mbar_init(&t.drained, 1);
             fence_barrier_init();
             t.failed = 0;
             tma_prefetch_map(&maps.k);
@@ -254,9 +262,12 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     if (FOLD) griddep_launch_dependents();
 
     // Bounded waits: a warp that gives up records it; all skip their further
-    // waits and leave by the ordinary way.
+    // waits and leave by the ordinary way. `leader` is the thread that issues
+    // copies and products (in the warp that does): it no longer does once a
+    // wait of its own has run out.
+    uint32_t leader = lane == 0;
     auto wait_at = [&](uint64_t* bar, uint32_t phase) {
-        if (!mbar_try_wait(bar, phase)) wait_long(bar, phase, &t.failed, batch);
+        if (!mbar_try_wait(bar, phase) && !wait_long(bar, phase, &t.failed, batch)) leader = 0;
         __syncwarp();  // whole warps go on to the tensor-memory instructions
     };
     auto wait = [&](uint64_t* bar, uint32_t& phase) {
@@ -369,12 +380,12 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
         // ------------------------------------------------------------------
         // copies and products
         // ------------------------------------------------------------------
-        const uint32_t leader = lane == 0;
         uint32_t stage = 0, phase = 0, state = 0, inter = 0, wv = 0, ready = 0, values = 0, update = 0;
         const uint64_t dq = smem_desc(sbase + P::kQ, 16), dp = smem_desc(sbase + P::kP, 16);
         const uint64_t dkk = smem_desc(sbase + P::kK, 16), dk = smem_desc(sbase + P::kK, 8192);
         const uint64_t dv = smem_desc(sbase + P::kV, D == 128 ? 8192 : 0);
         const uint64_t dw = smem_desc(sbase + P::kW, D == 128 ? 8192 : 0);
+        uint32_t qk_loads = 0, v_loads = 0;  // that the leader has issued
         auto load = [&](const Chunk& c, uint64_t* bar, uint32_t expect, const CUtensorMap* map, int head, int at) {
             if (leader) {
                 if (expect) mbar_arrive_expect_tx(bar, expect);
@@ -384,11 +395,16 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             __syncwarp();
         };
         // q announces its own bytes and those of k, which comes later
-        auto load_q = [&](const Chunk& c) { load(c, &t.qk[0], 2 * P::kTileBytes, &maps.q, maps.q_h, P::kQ); };
+        auto load_q = [&](const Chunk& c) {
+            qk_loads += leader;
+            load(c, &t.qk[0], 2 * P::kTileBytes, &maps.q, maps.q_h, P::kQ);
+        };
         auto load_k = [&](const Chunk& c, int st) {
+            if (FOLD) qk_loads += leader;
             load(c, &t.qk[st], FOLD ? P::kTileBytes : 0, &maps.k, maps.k_h, P::kK + st * P::kTileBytes);
         };
         auto load_v = [&](const Chunk& c, int st) {
+            v_loads += leader;
             load(c, &t.v[st], P::kTileBytes, &maps.v, maps.v_h, P::kV + st * P::kTileBytes);
         };
         if (c.valid) {
@@ -463,6 +479,19 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             zero = false;
             c = c2;
         }
+        if (lane == 0 && !leader) {
+            // A wait ran out. What is in flight ends (or runs into the limit
+            // once more) before the block gives up the memory it writes to.
+            const uint64_t until = globaltimer_ns() + batch.wait_limit_ns;
+            mma_commit(&t.drained, 1);
+            mbar_wait(&t.drained, 0, until);
+            for (uint32_t i = 1; i <= P::kStages; ++i) {
+                const uint32_t x = v_loads - i, y = qk_loads - i;  // each stage's last load
+                if (i <= v_loads) mbar_wait(&t.v[x % P::kStages], x / P::kStages & 1, until);
+                if (i <= qk_loads) mbar_wait(&t.qk[y % P::kStages], y / P::kStages & 1, until);
+            }
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------------
         // elementwise work
@@ -816,7 +845,7 @@ ak_status launch_chunks(const Batch& b, uint64_t* error_word, uint64_t epoch, ui
     }
     c.error_word = error_word;
     c.epoch = epoch;
-    c.wait_limit_ns = wait_limit_ns;
+    c.wait_limit_ns = std::max(wait_limit_ns, kLeastWait);
     if (b.a[0].dk == 128) return final ? launch_passes<128, 3>(c, stream) : launch_passes<128, 2>(c, stream);
     return final ? launch_passes<64, 3>(c, stream) : launch_passes<64, 2>(c, stream);
 }

@@ -24,3 +24,16 @@ def test_a_fold_has_its_tensor_memory_before_the_main_pass_may_start():
     assert allocated < body.index("__syncthreads()", allocated) < started
     assert body.count("griddep_launch_dependents(") == 1
     assert "return;" not in body[:allocated]
+
+
+def test_nothing_is_issued_after_a_wait_that_ran_out():
+    """Copies and products are issued by `leader` alone, which a wait of its own that ran out takes away; and the block
+    gives up its tensor memory only after it has waited for the products and copies in flight."""
+    body = _kernel("linattn_mma.cu", "k_chunks")
+    assert re.search(r"!wait_long\([^;]*\)\) leader = 0;", body)
+    walk = body[body.index("while (c.valid)"):]
+    issued = re.findall(r"mma_(?:ss|ts|commit)\((?:[^;]*?)(\w+)\);", walk)
+    assert len(issued) >= 8 and [x for x in issued if x != "leader"] == ["1"]  # the last one waits for all of them
+    loads = [m.start() for m in re.finditer(r"tma_load_3d\(", body)]
+    assert loads and all("if (leader) {" in body[at - 300:at] for at in loads)
+    assert walk.index("mma_commit(&t.drained, 1)") < walk.index("mbar_wait(&t.drained") < walk.index("tmem_free(")
