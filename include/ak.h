@@ -470,8 +470,9 @@ ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t
  * Within the types' rounding the order of summation is fixed by the shape:
  * equal calls give equal bits. In bf16 calls weighted scores and the state
  * are rounded to bf16 where they enter a product with q or v. A NaN or
- * infinity reaches the later tokens of its sequence and head, and may reach
- * up to 63 earlier ones; other sequences and heads never.
+ * infinity in q reaches its own output; in k, v or a state it reaches, as a NaN
+ * or infinity, what the recurrence takes it to: its sequence and head from its
+ * token on. In gradients likewise, those of k and v backwards in time.
  *
  * ak_linear_attention_backward: the gradients of sum(o * do) +
  * sum(state_out * dstate_out), from the forward call's inputs; dq, dk, dv as

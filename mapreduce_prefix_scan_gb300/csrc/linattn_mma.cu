@@ -99,6 +99,9 @@ struct Small {
     float score[2 * kChunk];
     float up[kFrame], down[kFrame];  // g^64u, and g^-64(u+1) or 1 (see `frame`)
     int len[kRanked];
+    // by the chunk's parity and column: where the first value that is not
+    // finite stands (see `spoil`)
+    int bad[2 * 128];
 };
 
 template <int D, int PARTS, bool FOLD>
@@ -165,6 +168,41 @@ __device__ __forceinline__ uint32_t bf16x2_of(uint64_t x) {
     return r;
 }
 __device__ __forceinline__ uint64_t pair_of_bf16x2(uint32_t x) { return pair_of(x << 16, x & 0xffff0000u); }
+
+// Adds up zeros, or NaN where a value is a NaN or infinite: x times zero.
+__device__ __forceinline__ void add_zeros(uint32_t& sum, uint32_t x) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
+}
+
+// V^T P^T multiplies a value also by the zero weights of the tokens before it.
+// Values that are not finite are therefore taken out of the tile (w V, and with
+// it the state, has them), and `poison` makes the outputs of their column NaN
+// from their token on. `bad` holds the chunk's end less their place in it,
+// which lies above the chunk's first token: what earlier chunks left there
+// never does, and of one chunk's places the first is the largest. A thread
+// looks through `pieces` pieces of its own, `step` rows apart.
+__device__ __noinline__ void spoil(unsigned char* at, int pieces, int step, int* bad, int end, int sign) {
+#pragma unroll 1
+    for (int i = 0; i < pieces; ++i, at += step * 128, end -= sign * step) {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+            unsigned short* const x = reinterpret_cast<unsigned short*>(at) + e;
+            if ((*x & 0x7f80) != 0x7f80) continue;
+            atomicMax(&bad[e], end);
+            *x = 0;
+        }
+    }
+}
+// The same of a row of scores, `n` of them from column j0 on: those of later
+// tokens have a zero weight, and become zero.
+__device__ __noinline__ void mask_scores(unsigned char* p, int row, int j0, int n, bool rev) {
+#pragma unroll 1
+    for (int j = j0; j < j0 + n; ++j)
+        if (rev ? j < row : j > row) *reinterpret_cast<unsigned short*>(p + swz128(row, j / 8) + j % 8 * 2) = 0;
+}
+__device__ __noinline__ void poison(bf16* out, int64_t tok, int first, int last) {
+    for (int i = first; i < last; ++i) *reinterpret_cast<unsigned short*>(out + i * tok) = 0x7fc0;
+}
 
 // A wait that the first poll did not end: until the limit, after which the
 // block records that it gave up, and none of its waits waits any longer.
@@ -249,6 +287,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
         t.up[u] = decay_pow(ld, u * kChunk);
         t.down[u] = frame == 0 ? 1.0f : decay_pow(ld, -(u + 1) * kChunk);
     }
+    if (!FOLD && tid < 2 * 128) t.bad[tid] = 0;
     if (tid < kChunk) {
         if (!FOLD) t.age[tid] = decay_pow(ld, rev ? kChunk - 1 - tid : tid + 1) * a.out_scale;
         t.wrow[tid] = decay_pow(ld, rev ? tid + 1 : kChunk - 1 - tid) * a.in_scale;
@@ -593,6 +632,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             const float age = FOLD                    ? decay_pow(ld, t.t1 - c.at - c.m)
                               : kFull || frame == 0 ? t.down[in_frame]
                                                     : decay_pow(ld, -(in_frame * kChunk + c.m));
+            uint32_t zeros = 0;
 #pragma unroll
             for (int i = 0; i < kChunk / kRowStep; ++i) {
                 const int r = v_row + i * kRowStep;
@@ -603,6 +643,9 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 const uint64_t ww = pair(w, w), minus = pair(-1.0f, -1.0f);
                 uint32_t* const x = &in.x;
                 uint32_t y[2][4], z[4];
+                if (!FOLD)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) add_zeros(zeros, x[e]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint64_t wv = mul2(pair_of_bf16x2(x[e]), ww);
@@ -616,6 +659,9 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 *reinterpret_cast<uint4*>(to + P::kTileBytes) = make_uint4(y[1][0], y[1][1], y[1][2], y[1][3]);
                 if (kThree) *reinterpret_cast<uint4*>(to + 2 * P::kTileBytes) = make_uint4(z[0], z[1], z[2], z[3]);
             }
+            if (!FOLD && (zeros & 0x7fff7fffu))
+                spoil(v_at, kChunk / kRowStep, kRowStep, t.bad + phase * 128 + tid % (D / 8) * 8,
+                      c.at + c.m - (rev ? kChunk - 1 - v_row : v_row), rev ? -1 : 1);
         };
         using Yes = std::true_type;
         using No = std::false_type;
@@ -666,21 +712,20 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                     uint32_t r[kCols];
                     tmem_ld(r, lanes + P::kX + part * kCols);
                     tmem_wait_ld(r);
+                    uint32_t zeros = 0;
 #pragma unroll
                     for (int y = 0; y < kCols / 8; ++y) {
                         uint32_t p[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int j = y * 8 + e * 2;
-                            const float w0 = score_at[-j], w1 = score_at[-j - 1];
-                            if (!full) {  // a masked column may hold anything
-                                if (w0 == 0.0f) r[j] = 0;
-                                if (w1 == 0.0f) r[j + 1] = 0;
-                            }
-                            p[e] = bf16x2_of(mul2(pair_of(r[j], r[j + 1]), pair(w0, w1)));
+                            p[e] = bf16x2_of(mul2(pair_of(r[j], r[j + 1]), pair(score_at[-j], score_at[-j - 1])));
+                            add_zeros(zeros, p[e]);
                         }
                         *reinterpret_cast<uint4*>(sm + P::kP + swz128(row, part * (kCols / 8) + y)) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
+                    // (the warp stays whole for what follows; rows without such scores have zeros there already)
+                    if (__any_sync(0xffffffffu, zeros & 0x7fff7fffu)) mask_scores(sm + P::kP, row, part * kCols, kCols, rev);
                 }
                 if (!zero) {
                     // the state's part, aged, back into the accumulator: the
@@ -741,6 +786,13 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
 #pragma unroll
                         for (int i = 0; i < kCols; ++i)
                             { if ((unsigned)(part * kCols + i - (rev ? kChunk - m : 0)) < (unsigned)m) put(i); else out += tok; }
+                    }
+                    // place of the column's first value that was not finite, or beyond the chunk
+                    const int at = rev ? (int)a.tokens - kChunk - base : base;
+                    const int bad = t.bad[phase * 128 + dv];
+                    if (bad > at) {
+                        const int place = at + m - bad, low = (rev ? kChunk - m : place) - part * kCols;
+                        poison(out - kCols * tok, tok, max(low, 0), min((rev ? kChunk - place : m) - part * kCols, kCols));
                     }
                 }
                 __syncwarp();
