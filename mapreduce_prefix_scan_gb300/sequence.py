@@ -68,8 +68,8 @@ def _need(cond, message):
 
 
 def _flat(t, dtype, numel, name, on):
-    """Pointer of a contiguous tensor of `numel` elements of `dtype` on the call's device (its index; -1: none)."""
-    if not (t.dtype is dtype and t.numel() == numel and t.get_device() == on >= 0 and t.is_contiguous()):
+    """Pointer of a contiguous tensor of `numel` elements of `dtype` on the call's device (its index, not -1)."""
+    if not (t.dtype is dtype and t.numel() == numel and t.get_device() == on and t.is_contiguous()):
         raise ValueError(f"{name}: a contiguous tensor of {numel} {dtype} values on the call's CUDA device is needed, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
@@ -93,7 +93,7 @@ def _workspace_ptr(nbytes, device, workspace, stream, on):
     point has returned, or the allocator may hand the memory out before the last launch is queued."""
     if workspace is not None:
         size = workspace.numel() * workspace.element_size()
-        _need(workspace.get_device() == on >= 0 and workspace.is_contiguous(),
+        _need(workspace.get_device() == on and workspace.is_contiguous(),
               "workspace: a contiguous tensor on the call's CUDA device is needed")
         _need(size >= nbytes, "workspace too small")
         return workspace.data_ptr(), size, workspace
@@ -220,7 +220,7 @@ def ak_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
 
 def _heads(t: torch.Tensor, shape, dtype, name, on) -> ak_heads:
     s = t.stride()
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == on >= 0 and (s[2] == 1 or shape[2] == 1)):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == on and (s[2] == 1 or shape[2] == 1)):
         raise ValueError(f"{name}: a {list(shape)} {dtype} tensor on q's CUDA device with a contiguous last dimension is "
                          f"needed, got {list(t.shape)} {t.dtype} with strides {list(s)} on {t.device}")
     return ak_heads(t.data_ptr(), s[0], s[1])
@@ -229,7 +229,7 @@ def _heads(t: torch.Tensor, shape, dtype, name, on) -> ak_heads:
 def _state_ptr(t, shape, name, on):
     if t is None:
         return None
-    if not (t.get_device() == on >= 0 and t.dtype == torch.float32 and t.shape == shape and t.is_contiguous()):
+    if not (t.get_device() == on and t.dtype == torch.float32 and t.shape == shape and t.is_contiguous()):
         raise ValueError(f"{name}: a contiguous {list(shape)} float32 tensor on q's CUDA device is needed, "
                          f"got {list(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
@@ -243,8 +243,8 @@ def _geometry(q, k, v, log_decay, offsets, scale, max_len):
     dv = v.shape[2]
     dt, on = q.dtype, q.get_device()
     kind = _FLOAT.get(dt)
-    if kind is None:
-        raise ValueError("q, k and v are float32 or bfloat16")
+    if kind is None or on < 0:
+        raise ValueError("q, k and v are float32 or bfloat16 CUDA tensors")
     n, off = 1, None
     if offsets is not None:
         n = offsets.numel() - 1
@@ -272,9 +272,10 @@ def _workspace(a, device, workspace, opts, stream, on):
     return _workspace_ptr(b.value, device, workspace, stream, on)
 
 
-def _tracked(*tensors) -> bool:
-    """Whether autograd records what is done with any of these (None allowed)."""
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+def _tracked(q, k, v, log_decay, state) -> bool:
+    """Whether autograd records what is done with any of these."""
+    return (q.requires_grad or k.requires_grad or v.requires_grad or log_decay.requires_grad or
+            (state is not None and state.requires_grad)) and torch.is_grad_enabled()
 
 
 class _Attention(torch.autograd.Function):
@@ -344,7 +345,8 @@ def ak_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     if state_out is None and final_state:
         state_out = _empty(ss, torch.float32, q.device, stream)
     op = _opts(opts)
-    hq, hk, hv, ho = [_heads(x, s, dt, n, on) for x, s, n in ((q, sk, "q"), (k, sk, "k"), (v, sv, "v"), (out, sv, "out"))]
+    hq, hk = _heads(q, sk, dt, "q", on), _heads(k, sk, dt, "k", on)
+    hv, ho = _heads(v, sv, dt, "v", on), _heads(out, sv, dt, "out", on)
     s0, s1 = _state_ptr(state, ss, "state", on), _state_ptr(state_out, ss, "state_out", on)
     wp, wb, _keep = _workspace(a, q.device, workspace, op, stream, on)
     _check(_abi.load().ak_linear_attention(a, hq, hk, hv, ld, off, s0, ho, s1, wp, wb, op, _stream_of(stream, q)),
@@ -400,7 +402,8 @@ def ak_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     a, sk, sv, ss, dt, ld, _, on = _geometry(q, k, v, log_decay, None, scale, None)
     if out is None:
         out = _empty(sv, dt, q.device, stream)
-    hq, hk, hv, ho = [_heads(x, s, dt, n, on) for x, s, n in ((q, sk, "q"), (k, sk, "k"), (v, sv, "v"), (out, sv, "out"))]
+    hq, hk = _heads(q, sk, dt, "q", on), _heads(k, sk, dt, "k", on)
+    hv, ho = _heads(v, sv, dt, "v", on), _heads(out, sv, dt, "out", on)
     pool = state.shape[0]
     sp = _state_ptr(state, (pool,) + ss[1:], "state", on)
     at = None if slots is None else _flat(slots, torch.int32, sk[0], "slots", on)
