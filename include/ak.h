@@ -423,7 +423,8 @@ ak_status ak_batch_layout(const int32_t* ctx_lens, const int32_t* new_lens, int6
  *                 noise_stride apart
  *   tokens        device, nreq * (k + 1) int32
  *   accepted      device, nreq int32
- * Differences and quotients are rounded to float32. Candidates need a weight
+ * The product u_j q_j(d_j) is compared exactly; differences and quotients are
+ * rounded to float32. Candidates need a weight
  * above zero; scores that are NaN are passed over. If the difference leaves
  * no candidate (p = q up to rounding), p alone decides; if that leaves none,
  * x is -1. k may be 0. No workspace.

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_verify(const VerifyC
             if (ok) {
                 const float pv = as_f(p[j * c.p_row + t]);
                 const float qv = q ? as_f(q[j * c.q_row + t]) : 1.0f;
-                ok = __fmul_rn(u, qv) < pv;
+                ok = (double)u * qv < pv;  // exact: a rounded product may equal p and not be it
             }
             const unsigned refused = __ballot_sync(0xffffffffu, !ok && j < m);
             if (refused) {
