@@ -463,11 +463,20 @@ ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t
  *   state_in   device, seqs*heads matrices, dk x dv with dv contiguous, or NULL
  *   state_out  device, the states after each sequence's last token, or NULL;
  *              may be state_in
- * The tensor core's float32 accumulation cuts off rather than rounds: states
- * of bf16 calls come out too small by about 1.6e-8 for every 16 tokens and
- * each of three parts that the decay still remembers (0.9e-6 at a memory of
- * 256 tokens, 3e-5 without decay over 16000 tokens in one window; more windows
- * keep it smaller, and float32 calls do not have it).
+ * The tensor core's float32 accumulation cuts off rather than rounds, so
+ * states of bf16 calls (heads of 64 and 128) come out too small: by up to 4e-8
+ * for each of the three products that add 16 tokens, as far back as the decay
+ * remembers and no further than the window's start. On normal inputs, relative
+ * and in norm: up to 4e-7 + 7.5e-9 M with M the tokens remembered, at most
+ * those of a window. Measured: 1.2e-6 at a memory of 256 tokens; without decay
+ * 3.5e-6 over 1000 tokens, 5e-5 over 16000 and 1.9e-4 over 64000 in one window,
+ * 4.2e-6 over 16000 in 30 windows. A caller who needs more cuts the axis
+ * (opts->target_blocks = tokens / 1000: below 8e-6 at any length), or passes
+ * float32 tensors, whose states round to nearest (2.3e-6 over 16000 tokens in
+ * one window).
+ * Range: within a block of tokens terms are held divided by up to e^30 of decay
+ * (e^40 in float32 calls and for other head sizes), so products k v above 1e25
+ * (1e21) in size may overflow where the recurrence would not.
  * Within the types' rounding the order of summation is fixed by the shape:
  * equal calls give equal bits. In bf16 calls weighted scores and the state
  * are rounded to bf16 where they enter a product with q or v. A NaN or
