@@ -33,10 +33,17 @@ class BatchLayout(NamedTuple):
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream_of(stream, t) -> int:
+    """The stream of a call on t's device, which has to be the current one: the kernels run there."""
+    on = t.get_device()
+    if _device() != on:
+        raise ValueError(f"the call's tensors are on device {on}, the current CUDA device is {_device()}")
     if stream is None:
         if _current is not None:
-            return _current(t.get_device())
+            return _current(on)
         return torch.cuda.current_stream(t.device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

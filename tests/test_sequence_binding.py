@@ -35,6 +35,9 @@ def _cuda(t):
     return t.as_subclass(_Cuda)
 
 
+STREAM_OF = sequence._stream_of
+
+
 class _Library:
     """Records every entry point's arguments; `sizes` are the answers of the workspace queries."""
 
@@ -261,3 +264,20 @@ def test_what_has_no_gradient_says_so(host):
         assert ak.ak_linear_attention(q, k, v, ld, out=out)[0] is out
         assert ak.ak_linear_attention_step(q, k, v, ld, pool, out=out) is out
     assert ak.ak_linear_attention(*_attention(), out=out)[0] is out
+
+
+@pytest.mark.parametrize("call", _named_calls())
+@pytest.mark.parametrize("current,refused", [(0, False), (1, True)])
+def test_tensors_of_a_device_that_is_not_current_are_refused(host, monkeypatch, call, current, refused):
+    """The kernels run on the current device, whatever stream they are given."""
+    L = host(_Library())
+    monkeypatch.setattr(sequence, "_stream_of", STREAM_OF)
+    monkeypatch.setattr(sequence, "_device", lambda: current, raising=False)
+    tensors, rest = _named_calls()[call]
+    tensors = {n: _cuda(t) for n, t in tensors.items()}
+    if refused:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            getattr(ak, call)(**tensors, **rest, stream=7)
+    else:
+        getattr(ak, call)(**tensors, **rest, stream=7)
+    assert (call in L.calls) != refused
