@@ -428,11 +428,28 @@ struct Division {
 // (heads, calls of the launch, column slices). One wave of equal windows
 // leaves no block waiting for a last one, and longer windows have fewer
 // states to pass on. By sequence there is no fold of window states and no
-// join (about a third of the main pass), but the longest sequence, or the
-// last ones to start, set the time: that is taken where it ends sooner.
+// join, but the longest sequence, or the last ones to start, set the time:
+// that is taken where it ends sooner. Times are estimated in steps of 64
+// tokens. Fold and join cost half of the main pass where it is long (32771
+// tokens, 16 heads of 128: 49 and 11 us beside 122) and more where it is
+// short: 0.7 of the work over all, and `fixed` steps of launches and join, 6
+// of the chunk kernel's (2.5 us) or 4 of the token kernel's (10 us).
+// Both sides measured at 102 shapes (8 to 64 heads, 2 to 300 sequences, 4096 to
+// 19200 tokens, bf16 heads of 64 and 128 and float32 of 64, forward and
+// backward), us by sequence / by windows:
+//   bf16, 32 heads of 128, 16 sequences, 16384 tokens   145 / 176
+//   the same of 8 sequences                             184 / 187
+//   the same of 2 sequences, 4096 tokens                154 / 68
+//   bf16, 8 heads of 64, 16 sequences, 8192 tokens      33 / 42
+//   float32, 64 heads of 64, 2 sequences, 4096 tokens   388 / 555
+// The faster one is taken, or one within 3 % of it, at 94 of them; the others
+// lose 4 to 6 %, and 19 and 23 % backward over 300 sequences, which blocks do
+// not sort. (With 1.35 of the work and 4 steps for both kernels 12 lost, by up
+// to 43 %; with 6 steps for the token kernel 2049 tokens of 5 sequences, 8 heads
+// of 80, took 120 us by sequence in place of 88 by windows.)
 constexpr int64_t kMaxWindows = 65535;  // a grid's second extent
 
-static Division divide(const LinattnCall& c, int64_t slots, int64_t lanes) {
+static Division divide(const LinattnCall& c, int64_t slots, int64_t lanes, int fixed) {
     const int64_t unit = 64;
     Division d = {};
     const int64_t units = std::max<int64_t>(1, (c.tokens + unit - 1) / unit);
@@ -444,10 +461,10 @@ static Division divide(const LinattnCall& c, int64_t slots, int64_t lanes) {
     if (c.windows > 0 || c.seqs < 2 || c.seqs > kMaxWindows) return d;
     const double work = (double)(units + c.seqs) * lanes / slots;  // steps of 64 tokens, spread evenly
     const double longest = (double)((c.max_len + unit - 1) / unit);
-    // (the longest start first, see linattn_mma.cu)
+    // (the longest start first, see linattn_mma.cu; unsorted, a long one may start last)
     const double seq_steps = std::max(longest, work + (c.seqs <= la::kRanked ? 0.15 : 0.5) * longest);
     const double window_steps = d.windows == 1 ? (double)(units + c.seqs) * std::max<int64_t>(1, lanes / slots)
-                                               : std::max(1.35 * work, (double)per) + 4;
+                                               : std::max(1.7 * work, (double)per) + fixed;
     if (seq_steps <= window_steps) {
         d.by_seq = true;
         // (sorting takes a block about 2 us, which a few chunks do not earn back)
@@ -461,10 +478,10 @@ static int64_t token_slices(int dv) { return (dv + 31) / 32; }
 
 // Divisions of the two kernels (the pointers decide between them later).
 static Division divide_chunks(const LinattnCall& c, const DeviceInfo& dev, int calls) {
-    return divide(c, 2 * dev.sm_count, (int64_t)c.heads * calls);
+    return divide(c, 2 * dev.sm_count, (int64_t)c.heads * calls, 6);
 }
 static Division divide_tokens(const LinattnCall& c, const DeviceInfo& dev, int calls) {
-    return divide(c, 3 * dev.sm_count, (int64_t)c.heads * calls * token_slices(std::max(c.dk, c.dv)));
+    return divide(c, 3 * dev.sm_count, (int64_t)c.heads * calls * token_slices(std::max(c.dk, c.dv)), 4);
 }
 
 static size_t carry_bytes(const LinattnCall& c, const Division& d, int calls) {
