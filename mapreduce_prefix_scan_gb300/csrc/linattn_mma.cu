@@ -206,13 +206,12 @@ __device__ __noinline__ void poison(bf16* out, int64_t tok, int first, int last)
 
 // A wait that the first poll did not end: until the limit, after which the
 // block records that it gave up, and none of its waits waits any longer.
-// Whether what was waited for is there.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t phase, int* failed, const ChunkBatch& batch) {
-    if (*(volatile int*)failed) return false;
-    if (mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) return true;
-    *(volatile int*)failed = 1;
-    if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
-    return false;
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t phase, int* failed, const ChunkBatch& batch) {
+    if (*(volatile int*)failed) return;
+    if (!mbar_wait(bar, phase, globaltimer_ns() + batch.wait_limit_ns)) {
+        *(volatile int*)failed = 1;
+        if (batch.error_word) *(volatile uint64_t*)batch.error_word = batch.epoch;
+    }
 }
 
 template <int D, int PARTS, bool FOLD>
@@ -301,12 +300,10 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
     if (FOLD) griddep_launch_dependents();
 
     // Bounded waits: a warp that gives up records it; all skip their further
-    // waits and leave by the ordinary way. `leader` is the thread that issues
-    // copies and products (in the warp that does): it no longer does once a
-    // wait of its own has run out.
-    uint32_t leader = lane == 0;
+    // waits and leave by the ordinary way, the issuing warp before it asks for
+    // another chunk.
     auto wait_at = [&](uint64_t* bar, uint32_t phase) {
-        if (!mbar_try_wait(bar, phase) && !wait_long(bar, phase, &t.failed, batch)) leader = 0;
+        if (!mbar_try_wait(bar, phase)) wait_long(bar, phase, &t.failed, batch);
         __syncwarp();  // whole warps go on to the tensor-memory instructions
     };
     auto wait = [&](uint64_t* bar, uint32_t& phase) {
@@ -419,12 +416,15 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
         // ------------------------------------------------------------------
         // copies and products
         // ------------------------------------------------------------------
+        const uint32_t leader = lane == 0;
         uint32_t stage = 0, phase = 0, state = 0, inter = 0, wv = 0, ready = 0, values = 0, update = 0;
         const uint64_t dq = smem_desc(sbase + P::kQ, 16), dp = smem_desc(sbase + P::kP, 16);
         const uint64_t dkk = smem_desc(sbase + P::kK, 16), dk = smem_desc(sbase + P::kK, 8192);
         const uint64_t dv = smem_desc(sbase + P::kV, D == 128 ? 8192 : 0);
         const uint64_t dw = smem_desc(sbase + P::kW, D == 128 ? 8192 : 0);
-        uint32_t qk_loads = 0, v_loads = 0;  // that the leader has issued
+        // A wait ran out: no barrier is used for another copy then, whose last
+        // one may still be under way. Asked once a chunk.
+        auto lost = [&] { return __shfl_sync(0xffffffffu, *(volatile int*)&t.failed, 0) != 0; };
         auto load = [&](const Chunk& c, uint64_t* bar, uint32_t expect, const CUtensorMap* map, int head, int at) {
             if (leader) {
                 if (expect) mbar_arrive_expect_tx(bar, expect);
@@ -434,16 +434,11 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             __syncwarp();
         };
         // q announces its own bytes and those of k, which comes later
-        auto load_q = [&](const Chunk& c) {
-            qk_loads += leader;
-            load(c, &t.qk[0], 2 * P::kTileBytes, &maps.q, maps.q_h, P::kQ);
-        };
+        auto load_q = [&](const Chunk& c) { load(c, &t.qk[0], 2 * P::kTileBytes, &maps.q, maps.q_h, P::kQ); };
         auto load_k = [&](const Chunk& c, int st) {
-            if (FOLD) qk_loads += leader;
             load(c, &t.qk[st], FOLD ? P::kTileBytes : 0, &maps.k, maps.k_h, P::kK + st * P::kTileBytes);
         };
         auto load_v = [&](const Chunk& c, int st) {
-            v_loads += leader;
             load(c, &t.v[st], P::kTileBytes, &maps.v, maps.v_h, P::kV + st * P::kTileBytes);
         };
         if (c.valid) {
@@ -480,6 +475,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             }
             const int parts = parts_of(c);
             const Chunk c2 = next(c);
+            if (FOLD && lost()) break;
             if (FOLD && c2.valid) {  // the other stage was used up with the update before
                 load_v(c2, stage ^ 1);
                 load_k(c2, stage ^ 1);
@@ -506,6 +502,7 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
                 mma_commit(&t.values, leader);
             }
             // the next chunk's tiles, each as soon as its buffer has been used
+            if (!FOLD && lost()) break;
             if (!FOLD && c2.valid) load_q(c2);
             wait(&t.update, update);
             if (!FOLD) {
@@ -518,16 +515,16 @@ __global__ void __launch_bounds__(Plan<D, PARTS, FOLD>::kThreads, 2) k_chunks(co
             zero = false;
             c = c2;
         }
-        if (lane == 0 && !leader) {
-            // A wait ran out. What is in flight ends (or runs into the limit
-            // once more) before the block gives up the memory it writes to.
+        if (lost()) {
+            // What is in flight ends (or runs into the limit once more) before
+            // the block gives up the memory that it writes to: products, and
+            // the copies of the chunk that was left.
             const uint64_t until = globaltimer_ns() + batch.wait_limit_ns;
-            mma_commit(&t.drained, 1);
+            mma_commit(&t.drained, leader);
             mbar_wait(&t.drained, 0, until);
-            for (uint32_t i = 1; i <= P::kStages; ++i) {
-                const uint32_t x = v_loads - i, y = qk_loads - i;  // each stage's last load
-                if (i <= v_loads) mbar_wait(&t.v[x % P::kStages], x / P::kStages & 1, until);
-                if (i <= qk_loads) mbar_wait(&t.qk[y % P::kStages], y / P::kStages & 1, until);
+            if (c.valid) {
+                mbar_wait(&t.v[stage], phase, until);
+                mbar_wait(&t.qk[stage], phase, until);
             }
         }
         __syncwarp();

@@ -26,14 +26,15 @@ def test_a_fold_has_its_tensor_memory_before_the_main_pass_may_start():
     assert "return;" not in body[:allocated]
 
 
-def test_nothing_is_issued_after_a_wait_that_ran_out():
-    """Copies and products are issued by `leader` alone, which a wait of its own that ran out takes away; and the block
-    gives up its tensor memory only after it has waited for the products and copies in flight."""
+def test_no_further_chunk_is_asked_for_after_a_wait_that_ran_out():
+    """The issuing warp leaves its walk before it arms a barrier for another chunk's copies, whose last copies may still
+    be under way; and the block gives up its tensor memory only after it has waited for the products and copies in
+    flight."""
     body = _kernel("linattn_mma.cu", "k_chunks")
-    assert re.search(r"!wait_long\([^;]*\)\) leader = 0;", body)
     walk = body[body.index("while (c.valid)"):]
-    issued = re.findall(r"mma_(?:ss|ts|commit)\((?:[^;]*?)(\w+)\);", walk)
-    assert len(issued) >= 8 and [x for x in issued if x != "leader"] == ["1"]  # the last one waits for all of them
-    loads = [m.start() for m in re.finditer(r"tma_load_3d\(", body)]
-    assert loads and all("if (leader) {" in body[at - 300:at] for at in loads)
-    assert walk.index("mma_commit(&t.drained, 1)") < walk.index("mbar_wait(&t.drained") < walk.index("tmem_free(")
+    asked = [m.start() for m in re.finditer(r"load_[qv]\(c2", walk)]  # these announce a chunk's bytes
+    left = [m.start() for m in re.finditer(r"if \(!?FOLD && lost\(\)\) break;", walk)]
+    assert len(left) == 2 and min(left) < min(asked)
+    assert walk.index("!FOLD && lost()") < walk.index("load_q(c2)")
+    assert walk.index("if (lost())") < walk.index("mma_commit(&t.drained") < walk.index("mbar_wait(&t.drained")
+    assert walk.index("mbar_wait(&t.qk[stage]") < walk.index("tmem_free(")
