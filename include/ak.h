@@ -487,7 +487,9 @@ ak_status ak_verify_drafts(const void* target_probs, int64_t target_req, int64_t
  * ak_linear_attention_backward: the gradients of sum(o * do) +
  * sum(state_out * dstate_out), from the forward call's inputs; dq, dk, dv as
  * q, k, v are described; dstate_in (may be NULL) receives the gradient of
- * state_in. log_decay and scale are constants of the model and get none.
+ * state_in. log_decay and scale are constants of the model and get none. A
+ * head that the inputs share gets its gradient for each head that reads it
+ * (dq, dk and dv have no head stride of 0); their sum is the caller's.
  * dstate_in is neither dstate_out nor state_in.
  *
  * ak_linear_attention_step: one token for each of `tokens` requests (seqs,

@@ -431,7 +431,7 @@ struct Division {
 // join, but the longest sequence, or the last ones to start, set the time:
 // that is taken where it ends sooner. Times are estimated in steps of 64
 // tokens. Fold and join cost half of the main pass where it is long (32771
-// tokens, 16 heads of 128: 49 and 11 us beside 122) and more where it is
+// tokens, 16 heads of 128: 52 and 10 us beside 123) and more where it is
 // short: 0.7 of the work over all, and `fixed` steps of launches and join, 6
 // of the chunk kernel's (2.5 us) or 4 of the token kernel's (10 us).
 // Both sides measured at 102 shapes (8 to 64 heads, 2 to 300 sequences, 4096 to

@@ -19,21 +19,25 @@
 // float32 and may be an output: w V is split into bf16 parts whose products
 // are exact in the float32 accumulation. Two parts keep 2^-17 of a term, three
 // 2^-25; the third is spent where the final state is asked for and the term
-// will still weigh more than 2^-8 in it. The accumulation itself cuts off low
-// bits instead of rounding them: measured, 1.6e-8 of the state for each of
-// these products, over the tokens that the decay remembers.
+// will still weigh more than 2^-8 in it (states of 2 to 300 tokens: 2.4e-6
+// relative with two parts, 0.05e-6 to 1.1e-6 with three). The accumulation
+// itself cuts off low bits instead of rounding them: measured, 2e-8 to 4e-8 of
+// the state for each of these products, over the tokens that the decay
+// remembers in a window.
 //
 // What bounds it. Measured at 16384 tokens, 32 heads of 128 in 16 sequences:
-// 130 us, 4.4 TB/s of the tensors' bytes, 0.65 of the copy bandwidth; issue
-// slots half busy, the tensor pipe a quarter. Shared memory and TMEM accesses
+// 134 us, 4.2 TB/s of the tensors' bytes, 0.62 of the copy bandwidth; issue
+// slots half busy, the tensor pipe 0.29. Shared memory and TMEM accesses
 // pass one 128-byte-a-cycle path: a chunk needs about 1700 cycles of it for
 // TMEM (S read 512, its bf16 form 256, R 512, scores 128, and S written back
 // 512 when a frame ends) and 1900 for shared memory (tiles in 384, w V 384,
 // the products' operands 1100), against 2700 that its 64 KB take from HBM at
 // an SM's share. The rest is the chain of a chunk's steps at two blocks an
 // SM. What cost time: registers spilled in the chunk loop (154 us with 60
-// bytes spilled, 133 with none), branches around single elements (each
-// serialises its load), eight working warps (193 us against 166 at the time).
+// bytes spilled, 133 with 4; now none at head size 128 and 8 bytes at 64),
+// branches around single elements (each serialises its load), eight working
+// warps (193 us against 166 at the time), masking each score by a selection
+// (8 us, against none for the sum of zeros that finds rows which need it).
 // Loading the next tiles earlier made no difference.
 //
 // Seventeen warps: sixteen do the elementwise work (on TMEM, four to a

@@ -19,9 +19,11 @@
 // combine in distributed shared memory. One launch, no workspace, and the
 // same result in any order of combination.
 //
-// Bound by HBM for many requests (192 of 128000 float32: 46 us, 0.88 of the
-// copy bandwidth) and by the chain of dependent loads (draft -> p, q at the
-// draft -> row, then the cluster's exchange) for few (4 of 32003: 6.0 us).
+// Bound by HBM for many requests (192 of 128000 float32: 47 us, 0.85 of the
+// copy bandwidth; bf16 37 us, 0.73, its elements' divisions beside its bytes;
+// certain drafts, with a row less to read, 44 and 40) and by the chain of
+// dependent loads (draft -> p, q at the draft -> row, then the cluster's
+// exchange) for few (4 of 32003: 6.0 us).
 #include <algorithm>
 #include <cooperative_groups.h>
 
