@@ -18,11 +18,14 @@
  *                   ones (tile-scan PR #202, first paragraph and paragraph
  *                   "Alternatives").
  *
- * Four more carry the same scans and folds into sequence models: the
+ * More of them carry the same scans and folds into sequence models: the
  * layout of a batch from its request lengths (ak_batch_layout), linear
  * attention with a decay for each head (ak_linear_attention, its gradients
- * and its single-token step), and the verification of drafted tokens
- * (ak_verify_drafts).
+ * and its single-token step), a recurrence with a gate for every token and
+ * channel (ak_gated_recurrence, likewise), the verification of drafted tokens
+ * (ak_verify_drafts), the step of a beam search (ak_beam_select,
+ * ak_beam_reorder), and the forking, freeing, compacting and copying of a
+ * paged cache's blocks (ak_blocks_*).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -535,6 +538,181 @@ ak_status ak_linear_attention_backward(const ak_linattn* shape, const ak_heads* 
 ak_status ak_linear_attention_step(const ak_linattn* shape, const ak_heads* q, const ak_heads* k, const ak_heads* v,
                                    const float* log_decay, float* state, const int32_t* slots, int64_t nslots,
                                    const ak_heads* o, const ak_opts* opts, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated linear recurrence: the scan whose state is a vector, with a gate for
+ * every token and channel. For each channel and sequence
+ *   h_t = a_t * h_{t-1} + b_t * x_t
+ *   AK_RECURRENCE_DECAY  a = exp(gate), b = 1          (gate: a log decay, <= 0)
+ *   AK_RECURRENCE_GATE   a = sigmoid(gate), b = 1 - a  (gate: a logit)
+ * Sequences are packed along the token axis as in ak_linear_attention; h
+ * starts from state_in, or zero.
+ *
+ * ak_rows describes one [tokens][channels] array: element (t, i) at
+ * t*token_stride + i (stride in elements, >= 0; 0 shares one row among all
+ * tokens in an input).
+ *
+ * ak_recurrence, the shape of a call:
+ *   dtype     AK_F32 or AK_BF16: of x, gate, h and their gradients; states are
+ *             float32, and so is all arithmetic
+ *   form      ak_recurrence_form
+ *   tokens, seqs, channels (>= 1)
+ *
+ *   offsets    device, seqs + 1 int32, non-decreasing; NULL: one sequence of
+ *              all tokens (seqs = 1). Values are clamped to [0, tokens].
+ *              Output rows of tokens outside every sequence are set to 0.
+ *   state_in   device, seqs rows of channels float, or NULL
+ *   state_out  device, the states after each sequence's last token, or NULL;
+ *              may be state_in. A sequence without tokens hands its state on.
+ * The order of summation is fixed by the shape: equal calls give equal bits.
+ * A gate of -infinity forgets what was before; a NaN or infinity reaches, as a
+ * NaN or infinity, what the recurrence takes it to: its sequence and channel from its
+ * token on (in gradients backwards in time). Log decays above 0 grow the state;
+ * factors of up to 128 tokens are multiplied first, so those of 1e38 and more over as
+ * many tokens give infinities or NaN where the recurrence might not.
+ *
+ * ak_gated_recurrence_backward: the gradients of sum(h * dh) +
+ * sum(state_out * dstate_out), from the forward call's inputs and its output
+ * h; dstate_in (may be NULL) receives the gradient of state_in. In a bf16 call
+ * the gates' gradients see h as it was stored, rounded to bf16 (in the gate
+ * form: h before every fourth token). x is not read in the decay form and may
+ * be NULL there. A row that an input shares among tokens gets its gradient
+ * for each token (dx and dgate have no stride of 0); their sum is the caller's.
+ *
+ * ak_gated_recurrence_step: one token for each of `tokens` requests (seqs and
+ * offsets unused), the state updated in place. Request b uses row slots[b] of
+ * nslots in `state` (slots NULL: b). An index outside [0, nslots) marks padding: its
+ * output is 0. Indices must not repeat.
+ *
+ * Outputs overlap neither each other nor an input, except as stated. No workspace.
+ * ------------------------------------------------------------------------- */
+typedef enum ak_recurrence_form { AK_RECURRENCE_DECAY = 0, AK_RECURRENCE_GATE = 1 } ak_recurrence_form;
+
+typedef struct ak_rows {
+    void* data;
+    int64_t token_stride;
+} ak_rows;
+
+typedef struct ak_recurrence {
+    int64_t tokens, seqs, channels;
+    int32_t dtype; /* ak_dtype */
+    int32_t form;  /* ak_recurrence_form */
+} ak_recurrence;
+
+ak_status ak_gated_recurrence(const ak_recurrence* shape, const ak_rows* x, const ak_rows* gate,
+                              const int32_t* offsets, const float* state_in, const ak_rows* h, float* state_out,
+                              const ak_opts* opts, void* stream);
+ak_status ak_gated_recurrence_backward(const ak_recurrence* shape, const ak_rows* dh, const ak_rows* x,
+                                       const ak_rows* gate, const ak_rows* h, const int32_t* offsets,
+                                       const float* state_in, const float* dstate_out, const ak_rows* dx,
+                                       const ak_rows* dgate, float* dstate_in, const ak_opts* opts, void* stream);
+ak_status ak_gated_recurrence_step(const ak_recurrence* shape, const ak_rows* x, const ak_rows* gate, float* state,
+                                   const int32_t* slots, int64_t nslots, const ak_rows* h, const ak_opts* opts,
+                                   void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ak_beam_select: one step of a beam search over `batch` requests. Beam k of a
+ * request has the summed log probability scores[k] and the logits x_k of its next
+ * token; its candidates are
+ *   token v, total scores[k] + x_k(v) - log sum_w exp x_k(w), length lengths[k] + 1
+ *   if the beam has ended (done[k] != 0): end_token alone, total scores[k],
+ *   length lengths[k]; its logits are not read
+ * and the request's best `keep` of all its beams' candidates, by
+ * total / length^penalty, are its next beams, in decreasing order (ties: the
+ * lowest beam, then token).
+ *
+ *   logits     device, element (r, k, v) at r*batch_stride + k*beam_stride + v;
+ *              AK_F32 or AK_BF16
+ *   scores     device, batch * beams float
+ *   done       device, batch * beams bytes; NULL: none has ended
+ *   lengths    device, batch * beams int32; NULL: all 0
+ *   end_token  the token that ends a beam, or -1
+ *   penalty    finite; 0: candidates are ranked by their totals
+ *   beams, keep  1 .. 32 (a first step has one beam and keeps several)
+ *   out_scores, out_tokens, out_parents  device, batch * keep: total, token
+ *              and the beam it extends
+ *   out_done, out_lengths  device, likewise, or NULL
+ * Sums of exponentials are float32 with compensation; logarithms, totals and
+ * their comparison are 64-bit, out_scores rounded from them. A
+ * logit of -infinity, and what has no finite rank, is no candidate; a row
+ * that holds a NaN or +infinity, or a beam whose score is not finite, has none.
+ * Where a request has fewer than `keep` candidates the rest of its beams get score
+ * -infinity, token and parent -1, length 0 and done 1. No workspace.
+ *
+ * ak_beam_reorder: state[b] = state[parents[b]] for the `beams` (1 .. 32) rows of
+ * each request, in place: rows of inner_bytes at
+ *   o*outer_stride + r*batch_stride + k*beam_stride   (bytes; o < outer, r < batch)
+ * A row whose parent is outside [0, beams) stays as it is. Rows do not overlap.
+ * ------------------------------------------------------------------------- */
+ak_status ak_beam_select(const void* logits, int64_t batch_stride, int64_t beam_stride, ak_dtype dtype, int64_t batch,
+                         int32_t beams, int64_t vocab, int32_t keep, const float* scores, const uint8_t* done,
+                         const int32_t* lengths, int32_t end_token, float penalty, float* out_scores,
+                         int32_t* out_tokens, int32_t* out_parents, uint8_t* out_done, int32_t* out_lengths,
+                         const ak_opts* opts, void* stream);
+ak_status ak_beam_reorder(void* state, int64_t outer, int64_t outer_stride, int64_t batch, int64_t batch_stride,
+                          int32_t beams, int64_t beam_stride, int64_t inner_bytes, const int32_t* parents,
+                          const ak_opts* opts, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Blocks of a paged cache that requests share. A request of lens[r] tokens
+ * holds the first ceil(lens[r] / block_size) entries of its row of the block
+ * table (at most table_width; further entries mean nothing), and several requests may hold
+ * the same block. An entry outside [0, nblocks) holds none. Nothing is kept between
+ * calls: how often a block is held is what the table says.
+ *
+ * ak_blocks_count: refs[i] = held entries that are i, for nblocks blocks.
+ *
+ * ak_blocks_fork: row r of the result goes on from row parents[r] (nnew rows from
+ * nreq; a parent outside [0, nreq): an empty row): its length and its held
+ * entries, -1 past them. Where the last block is partly filled, the row
+ * will write into it next, so rows may not share it: of those that end in the
+ * same block the lowest keeps it, if no other row holds it in another place,
+ * and every other takes a block from free_blocks, front to back in row order,
+ * enters it, and its copy is listed: pairs[i] = (from, to). counts[0] is how many copies
+ * are wanted; past the free list (or at an entry of it outside [0, nblocks))
+ * the table gets -1 and no pair is listed. Unused pairs are (-1, -1). refs as
+ * ak_blocks_count would give for the result.
+ *   out_table  device, nnew rows of table_width, out_stride apart; out_lens
+ *              nnew int32; refs nblocks int32; pairs nnew * 2 int32; counts 1 int32
+ *
+ * ak_blocks_free: the blocks i with refs[i] <= 0 in increasing order, -1 past
+ * them (free_blocks: nblocks int32), and their number (counts: 1 int32). The
+ * list is one for ak_batch_layout and ak_blocks_fork.
+ *
+ * ak_blocks_compact: moves the n blocks in use (refs > 0) to 0 .. n-1: the
+ * i-th of them that lies at n or past it, to the i-th free one before n. out_table
+ * is the table with its held entries renamed (out_table may be block_table),
+ * pairs (nblocks / 2 of them, unused ones (-1, -1)) the moves, counts[0] their number,
+ * counts[1] n.
+ *
+ * ak_blocks_copy: copies blocks within a cache: for each pair (from, to) the
+ * inner_bytes at o*outer_stride + from*block_stride to those at o*outer_stride +
+ * to*block_stride, for all o < outer. Pairs with an id outside [0, nblocks)
+ * are passed over, and those past count[0] (device; NULL: all npairs). No block that
+ * is copied to is in another pair (those of fork and compact are such).
+ *
+ * Outputs overlap neither each other nor an input, except as stated. nblocks, nreq,
+ * nnew below 2^30.
+ * ------------------------------------------------------------------------- */
+ak_status ak_blocks_count(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lens,
+                          int64_t nreq, int32_t block_size, int64_t nblocks, int32_t* refs, const ak_opts* opts,
+                          void* stream);
+ak_status ak_blocks_fork_workspace_size(int64_t nnew, int64_t nblocks, const ak_opts* opts, size_t* bytes);
+ak_status ak_blocks_fork(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lens,
+                         int64_t nreq, const int32_t* parents, int64_t nnew, const int32_t* free_blocks, int64_t nfree,
+                         int32_t block_size, int64_t nblocks, int32_t* out_table, int64_t out_stride,
+                         int32_t* out_lens, int32_t* refs, int32_t* pairs, int32_t* counts, void* workspace,
+                         size_t workspace_bytes, const ak_opts* opts, void* stream);
+ak_status ak_blocks_free(const int32_t* refs, int64_t nblocks, int32_t* free_blocks, int32_t* counts,
+                         const ak_opts* opts, void* stream);
+ak_status ak_blocks_compact_workspace_size(int64_t nblocks, const ak_opts* opts, size_t* bytes);
+ak_status ak_blocks_compact(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lens,
+                            int64_t nreq, const int32_t* refs, int32_t block_size, int64_t nblocks,
+                            int32_t* out_table, int64_t out_stride, int32_t* pairs, int32_t* counts, void* workspace,
+                            size_t workspace_bytes, const ak_opts* opts, void* stream);
+ak_status ak_blocks_copy(void* cache, int64_t outer, int64_t outer_stride, int64_t nblocks, int64_t block_stride,
+                         int64_t inner_bytes, const int32_t* pairs, int64_t npairs, const int32_t* count,
+                         const ak_opts* opts, void* stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,7 @@ OPS = {"add": 0, "mul": 1, "max": 2, "min": 3, "matmul": 4}
 STORES = {"overwrite": 0, "init": 1, "fold": 2}
 SHAPES = {"auto": 0, "thread": 1, "tiled": 2, "columns": 3}
 FLAG_DIMS_CLUSTER = 1
+FORMS = {"decay": 0, "gate": 1}
 
 # every symbol include/ak.h declares
 EXPORTS = ("ak_opts_default", "ak_status_string", "ak_dtype_size", "ak_last_cuda_error",
@@ -29,7 +30,10 @@ EXPORTS = ("ak_opts_default", "ak_status_string", "ak_dtype_size", "ak_last_cuda
            "ak_accumulate", "ak_scan_status", "ak_findall_workspace_size", "ak_findall", "ak_dims_select",
            "ak_reduce_noalloc", "ak_batch_layout_workspace_size", "ak_batch_layout", "ak_verify_drafts",
            "ak_linear_attention_workspace_size", "ak_linear_attention", "ak_linear_attention_backward",
-           "ak_linear_attention_step")
+           "ak_linear_attention_step", "ak_gated_recurrence", "ak_gated_recurrence_backward",
+           "ak_gated_recurrence_step", "ak_beam_select", "ak_beam_reorder", "ak_blocks_count",
+           "ak_blocks_fork_workspace_size", "ak_blocks_fork", "ak_blocks_free", "ak_blocks_compact_workspace_size",
+           "ak_blocks_compact", "ak_blocks_copy")
 
 
 class ak_opts(ctypes.Structure):
@@ -48,6 +52,15 @@ class ak_linattn(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int64), ("max_len", ctypes.c_int64),
                 ("heads", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ak_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64)]
+
+
+class ak_recurrence(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("form", ctypes.c_int32)]
 
 
 _lib = None
@@ -100,6 +113,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.ak_linear_attention.argtypes = [PL, PH, PH, PH, P, P, P, PH, P, P, SZ, PO, P]
     L.ak_linear_attention_backward.argtypes = [PL, PH, PH, PH, PH, P, P, P, P, PH, PH, PH, P, P, SZ, PO, P]
     L.ak_linear_attention_step.argtypes = [PL, PH, PH, PH, P, P, P, I64, PH, PO, P]
+    PR, PA = ctypes.POINTER(ak_recurrence), ctypes.POINTER(ak_rows)
+    L.ak_gated_recurrence.argtypes = [PR, PA, PA, P, P, PA, P, PO, P]
+    L.ak_gated_recurrence_backward.argtypes = [PR, PA, PA, PA, PA, P, P, P, PA, PA, P, PO, P]
+    L.ak_gated_recurrence_step.argtypes = [PR, PA, PA, P, P, I64, PA, PO, P]
+    F32 = ctypes.c_float
+    L.ak_beam_select.argtypes = [P, I64, I64, I32, I64, I32, I64, I32, P, P, P, I32, F32, P, P, P, P, P, PO, P]
+    L.ak_beam_reorder.argtypes = [P, I64, I64, I64, I64, I32, I64, I64, P, PO, P]
+    L.ak_blocks_count.argtypes = [P, I64, I32, P, I64, I32, I64, P, PO, P]
+    L.ak_blocks_fork_workspace_size.argtypes = [I64, I64, PO, PSZ]
+    L.ak_blocks_fork.argtypes = [P, I64, I32, P, I64, P, I64, P, I64, I32, I64, P, I64, P, P, P, P, P, SZ, PO, P]
+    L.ak_blocks_free.argtypes = [P, I64, P, P, PO, P]
+    L.ak_blocks_compact_workspace_size.argtypes = [I64, PO, PSZ]
+    L.ak_blocks_compact.argtypes = [P, I64, I32, P, I64, P, I32, I64, P, I64, P, P, P, SZ, PO, P]
+    L.ak_blocks_copy.argtypes = [P, I64, I64, I64, I64, I64, P, I64, P, PO, P]
+    for f in EXPORTS[-12:]:
+        getattr(L, f).restype = I32
     for f in ("ak_reduce_workspace_size", "ak_reduce", "ak_reduce2", "ak_reduce_dims_workspace_size", "ak_reduce_dims",
               "ak_accumulate_workspace_size", "ak_accumulate", "ak_scan_status", "ak_findall_workspace_size",
               "ak_findall", "ak_dims_select", "ak_reduce_noalloc", "ak_batch_layout_workspace_size",

@@ -354,6 +354,82 @@ ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stre
 ak_status run_linattn_step(const LinattnCall& c, float* state, const int32_t* slots, int64_t nslots,
                            cudaStream_t stream);
 
+// gated_recurrence.cu
+struct RecurrenceCall {
+    ak_dtype dtype;
+    int form;  // ak_recurrence_form
+    int64_t tokens, seqs, channels;
+    ak_rows x, gate;
+    ak_rows out;              // forward, step
+    ak_rows dh, h, dx, dgate; // backward
+    const int32_t* offsets;
+    const float* state_in;
+    float* state_out;
+    const float* dstate_out;  // gradient of the final state, or null
+    float* dstate_in;         // gradient of the initial state, or null
+};
+ak_status run_recurrence(const RecurrenceCall& c, cudaStream_t stream);
+ak_status run_recurrence_backward(const RecurrenceCall& c, cudaStream_t stream);
+ak_status run_recurrence_step(const RecurrenceCall& c, float* state, const int32_t* slots, int64_t nslots,
+                              cudaStream_t stream);
+
+// beam_search.cu
+struct BeamCall {
+    const void* logits;
+    int64_t batch_stride, beam_stride;  // elements
+    ak_dtype dtype;
+    int64_t batch, vocab;
+    int32_t beams, keep, end;
+    float penalty;
+    const float* scores;
+    const uint8_t* done;
+    const int32_t* lengths;
+    float* out_scores;
+    int32_t *out_tokens, *out_parents;
+    uint8_t* out_done;
+    int32_t* out_lengths;
+    int32_t slices;  // of a row; filled in by run_beam_select
+};
+ak_status run_beam_select(BeamCall c, cudaStream_t stream);
+struct ReorderCall {
+    void* state;
+    int64_t outer, batch, inner;  // inner: bytes
+    int32_t beams;
+    int64_t outer_stride, batch_stride, beam_stride;  // bytes
+    const int32_t* parents;
+};
+ak_status run_beam_reorder(const ReorderCall& c, cudaStream_t stream);
+
+// blocks.cu
+struct BlocksCall {
+    const int32_t* table;
+    int64_t rows, table_stride;  // rows: of the result, where the call has one
+    int32_t width, block_size;
+    const int32_t* lens;
+    int64_t old_rows;
+    const int32_t* parents;
+    const int32_t* free_blocks;
+    int64_t nfree, blocks;
+    int32_t* refs;
+    int32_t* out_table;
+    int64_t out_stride;
+    int32_t *out_lens, *pairs, *counts, *out_free, *work;
+};
+size_t blocks_fork_workspace(int64_t rows, int64_t blocks);
+size_t blocks_compact_workspace(int64_t blocks);
+ak_status run_blocks_count(const BlocksCall& c, cudaStream_t stream);
+ak_status run_blocks_fork(BlocksCall c, void* ws, cudaStream_t stream);
+ak_status run_blocks_free(const BlocksCall& c, cudaStream_t stream);
+ak_status run_blocks_compact(BlocksCall c, void* ws, cudaStream_t stream);
+struct BlocksCopyCall {
+    void* cache;
+    int64_t outer, outer_stride, blocks, block_stride, inner;  // strides and inner in bytes
+    const int32_t* pairs;
+    int64_t npairs;
+    const int32_t* count;
+};
+ak_status run_blocks_copy(const BlocksCopyCall& c, cudaStream_t stream);
+
 // ---------------------------------------------------------------------------
 // helpers of the entry points (api.cu)
 // ---------------------------------------------------------------------------

@@ -1,0 +1,508 @@
+// beam_search.cu -- the step of a beam search over all beams and the
+// vocabulary, and the reordering of states by its parents.
+//
+// Request r has beams of summed log probabilities s_k and logits x_k(v). Its
+// candidates are
+//   s_k + x_k(v) - log sum_w exp x_k(w)   for a beam that goes on
+//   s_k, as token `end`                   for one that has ended
+// ranked by their value over length^penalty; the best `keep` follow, ties by
+// the lowest beam, then token.
+//
+// Within a beam the order of candidates is that of its logits, so one pass
+// over a row gives its sum and its best `keep` logits, and the request's
+// answer is among them. A cluster of blocks takes a request, a block a row
+// or a slice of one at a time:
+//  - pass: each thread folds its columns (groups of four, kThreads groups
+//    apart) to a maximum, its column and a sum of exponentials; no list is
+//    kept beside it, so an element costs a conversion, a maximum, a
+//    difference, an exponential and two sums;
+//  - the `keep`-th best of the threads' maxima is a bound below which nothing
+//    can be chosen, and only the (at most `keep`) threads whose maximum
+//    reaches it hold candidates: their columns are read once more, from L2;
+//  - lists of 32 lie in the lanes of a warp and are merged as bitonic
+//    sequences; the cluster's first block merges the rows.
+// Keys order by (logit, lowest column), so the answer does not depend on the
+// order in which threads find them.
+//
+// Decisions lie next to one another: logits differ by little, and so do the
+// beams' sums. Sums of exponentials are float32 with a running compensation,
+// the logarithm, the totals and the ranks are 64-bit.
+#include <algorithm>
+#include <atomic>
+#include <cooperative_groups.h>
+
+#include "ak_common.cuh"
+#include "ak_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace ak {
+namespace bs {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / kWarp;
+constexpr int kMaxBeams = 32;     // of a request, before and after: a list is a warp
+constexpr int kMaxParts = 16;     // blocks of a cluster
+constexpr int kUnroll = 4;        // groups of four in flight
+constexpr int kBatch = kThreads * 4;  // elements of a candidates' batch
+
+// Orders floats as unsigned integers; -0 and 0 are one value.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
+// A logit and its column; larger is better, 0 is none.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t col) {
+    return x > -INFINITY ? (uint64_t)ordered(x) << 32 | (0xffffffffu - col) : 0;
+}
+
+// What the merge of the rows sorts: the rank, then the lowest beam and token.
+struct Pick {
+    uint64_t rank;   // 0: none
+    uint64_t place;  // ~(beam << 32 | token)
+    float total;
+    __device__ __forceinline__ bool over(const Pick& o) const {
+        return rank > o.rank || (rank == o.rank && place > o.place);
+    }
+};
+
+__device__ __forceinline__ bool over(uint64_t a, uint64_t b) { return a > b; }
+__device__ __forceinline__ bool over(const Pick& a, const Pick& b) { return a.over(b); }
+__device__ __forceinline__ uint64_t from_lane(uint64_t v, int mask) { return __shfl_xor_sync(0xffffffffu, v, mask); }
+__device__ __forceinline__ Pick from_lane(const Pick& v, int mask) {
+    Pick o;
+    o.rank = __shfl_xor_sync(0xffffffffu, v.rank, mask);
+    o.place = __shfl_xor_sync(0xffffffffu, v.place, mask);
+    o.total = __shfl_xor_sync(0xffffffffu, v.total, mask);
+    return o;
+}
+
+// Of this lane's and another's value the larger (or the smaller).
+template <class K>
+__device__ __forceinline__ void exchange(K& v, int mask, bool larger) {
+    const K o = from_lane(v, mask);
+    if (over(o, v) == larger) v = o;
+}
+
+// Lanes 0 .. 31 in decreasing order.
+template <class K>
+__device__ __forceinline__ void warp_sort(K& v, int lane) {
+#pragma unroll
+    for (int k = 2; k <= kWarp; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) exchange(v, j, ((lane & k) == 0) == ((lane & j) == 0));
+}
+
+// The best 32 of two lists in decreasing order, `o` given reversed (lane 31's first).
+template <class K>
+__device__ __forceinline__ void warp_merge(K& v, const K& reversed, int lane) {
+    if (over(reversed, v)) v = reversed;
+#pragma unroll
+    for (int j = kWarp / 2; j > 0; j >>= 1) exchange(v, j, (lane & j) == 0);
+}
+
+// Adds 32 values in any order to a list.
+template <class K>
+__device__ __forceinline__ void warp_take(K& list, K v, int lane) {
+    warp_sort(v, lane);
+    warp_merge(list, from_lane(v, kWarp - 1), lane);
+}
+
+// Warp 0's list becomes the best 32 of all warps' lists. Ends in sync.
+template <class K>
+__device__ __forceinline__ void block_merge(K& list, K (*s_lists)[kWarp], int lane, int warp) {
+#pragma unroll
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+        if (warp >= half && warp < 2 * half) s_lists[warp][lane] = list;
+        __syncthreads();
+        if (warp < half) warp_merge(list, s_lists[warp + half][kWarp - 1 - lane], lane);
+        __syncthreads();
+    }
+}
+
+template <class T>
+struct alignas(4 * sizeof(T)) Group {
+    uint32_t w[sizeof(T)];
+};
+__device__ __forceinline__ float get(const Group<float>& f, int i) { return __uint_as_float(f.w[i]); }
+__device__ __forceinline__ float get(const Group<bf16>& f, int i) {
+    return __uint_as_float(i % 2 ? f.w[i / 2] & 0xffff0000u : f.w[i / 2] << 16);
+}
+__device__ __forceinline__ Group<float> ld_group(const float* p) {
+    Group<float> f;
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+        : "=r"(f.w[0]), "=r"(f.w[1]), "=r"(f.w[2]), "=r"(f.w[3]) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ Group<bf16> ld_group(const bf16* p) {
+    Group<bf16> f;
+    asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(f.w[0]), "=r"(f.w[1]) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(bf16 v) { return __bfloat162float(v); }
+
+// Columns [col, col + 4) of a row of `vocab`, -infinity past its end. The
+// columns of a group are the same whatever the row's alignment: equal rows
+// give equal sums.
+template <class T>
+__device__ __forceinline__ void load_group(float (&x)[4], const T* row, uint32_t col, uint32_t end, bool wide) {
+    if (wide && col + 4 <= end) {
+        const Group<T> g = ld_group(row + col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = get(g, i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = col + i < end ? as_float(row[col + i]) : -INFINITY;
+    }
+}
+
+// A row's (or slice's) share of the answer, in the first block's shared memory.
+struct Share {
+    float top;         // the largest logit, or -infinity
+    double sum;        // of exp(x - top)
+    uint64_t keys[kMaxBeams];
+};
+
+struct Shared {
+    uint64_t lists[kWarps][kWarp];
+    Pick picks[kWarps][kWarp];
+    uint64_t found[kBatch];
+    int nfound, nchosen;
+    int chosen[kMaxBeams];
+    uint64_t bound;
+    float tops[kWarps];
+    double sums[kWarps];
+    double norm[kMaxBeams];   // length^penalty of a beam's candidates
+    Share share[kMaxBeams];   // of the rows' slices (first block)
+    double base[kMaxBeams];   // s_k - log sum exp, less the largest logit
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sum += x with what rounding loses kept in `lost`.
+__device__ __forceinline__ void add(float& sum, float& lost, float x) {
+    const float t = sum + x, v = t - sum;
+    lost += (sum - (t - v)) + (x - v);
+    sum = t;
+}
+
+// Folds columns [first, last) of a row and writes its share.
+template <class T>
+__device__ void fold_row(const T* row, uint32_t first, uint32_t last, int keep, Shared& s, Share* out) {
+    const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
+    const bool wide = (reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) == 0;
+    float top = -INFINITY, ref = 0.0f, sum = 0.0f, lost = 0.0f;
+    uint32_t at = 0;
+    for (uint64_t c0 = first + tid * 4u; c0 < last; c0 += (uint64_t)kThreads * 4 * kUnroll) {
+        float x[kUnroll][4];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const uint64_t col = c0 + (uint64_t)u * kThreads * 4;
+            if (col < last) load_group(x[u], row, (uint32_t)col, last, wide);
+            else x[u][0] = x[u][1] = x[u][2] = x[u][3] = -INFINITY;
+        }
+        float m = x[0][0];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, x[u][i]);
+        if (m > top) {
+            const float f = exp2f((ref - m) * kLog2e);
+            if (top > -INFINITY) sum *= f, lost *= f;
+            top = ref = m;
+            bool found = false;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!found && x[u][i] == m) {
+                        found = true;
+                        at = (uint32_t)c0 + u * kThreads * 4 + i;
+                    }
+        }
+        float e = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"((x[u][i] - ref) * kLog2e));
+            e += (y[0] + y[1]) + (y[2] + y[3]);
+        }
+        add(sum, lost, e);
+    }
+    // ---- the block's maximum and sum
+    float best = top;
+#pragma unroll
+    for (int d = kWarp / 2; d > 0; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+    if (lane == 0) s.tops[warp] = best;
+    if (tid == 0) s.nchosen = 0;
+    // ---- the threads' best, and the bound
+    const uint64_t mine = key_of(top, at);
+    uint64_t list = mine;
+    warp_sort(list, lane);
+    __syncthreads();
+    best = s.tops[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) best = fmaxf(best, s.tops[w]);
+    // a NaN among the logits is in `sum` alone
+    double sm = top > -INFINITY ? ((double)sum + lost) * expf(top - best) : (double)sum;
+#pragma unroll
+    for (int d = kWarp / 2; d > 0; d >>= 1) sm += __shfl_xor_sync(0xffffffffu, sm, d);
+    if (lane == 0) s.sums[warp] = sm;
+    block_merge(list, s.lists, lane, warp);
+    if (warp == 0) {
+        const uint64_t b = __shfl_sync(0xffffffffu, list, keep - 1);
+        if (lane == 0) s.bound = b;
+    }
+    __syncthreads();
+    const uint64_t bound = s.bound;
+    // (fewer than `keep` threads with a candidate: each of them is looked through)
+    if (mine && mine >= bound) s.chosen[atomicAdd(&s.nchosen, 1)] = tid;
+    __syncthreads();
+    // ---- the chosen threads' columns again, a batch of groups at a time
+    const int chosen = s.nchosen;
+    const uint32_t groups = (last - first + 3) / 4, per = (groups + kThreads - 1) / kThreads;  // of a thread, at most
+    list = 0;
+    for (uint32_t g0 = 0; g0 < per * (uint32_t)chosen; g0 += kThreads) {
+        if (tid == 0) s.nfound = 0;
+        __syncthreads();
+        const uint32_t g = g0 + tid;
+        if (g < per * (uint32_t)chosen) {
+            const uint64_t col = first + ((uint64_t)(g % per) * kThreads + s.chosen[g / per]) * 4;
+            if (col < last) {
+                float x[4];
+                load_group(x, row, (uint32_t)col, last, wide);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t k = key_of(x[i], (uint32_t)col + i);
+                    if (k && k >= bound) s.found[atomicAdd(&s.nfound, 1)] = k;
+                }
+            }
+        }
+        __syncthreads();
+        const int n = s.nfound;
+        for (int b = warp * kWarp; b < n; b += kThreads) warp_take(list, b + lane < n ? s.found[b + lane] : uint64_t(0), lane);
+        __syncthreads();
+    }
+    block_merge(list, s.lists, lane, warp);
+    if (warp == 0) {
+        out->keys[lane] = list;
+        if (lane == 0) {
+            double total = 0.0;
+            for (int w = 0; w < kWarps; ++w) total += s.sums[w];
+            out->top = best;
+            out->sum = total;
+        }
+    }
+    __syncthreads();
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
+    __shared__ Shared s;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank(), parts = (int)cl.num_blocks();
+    const int64_t r = blockIdx.x / parts;
+    const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
+    const int n = c.beams, keep = c.keep, slices = c.slices;
+    const float* scores = c.scores + r * n;
+    const uint8_t* done = c.done ? c.done + r * n : nullptr;
+    const int32_t* lengths = c.lengths ? c.lengths + r * n : nullptr;
+    const uint32_t vocab = (uint32_t)c.vocab, slice = ((vocab + slices - 1) / slices + 3) / 4 * 4;
+
+    if (parts > 1) cl.sync();  // the first block runs before another writes to it
+    Shared* s0 = cl.map_shared_rank(&s, 0);
+    if (rank == 0 && warp == kWarps - 1 && lane < n) {
+        double norm = 1.0;
+        if (c.penalty != 0.0f) {
+            const int len = (lengths ? lengths[lane] : 0) + !(done && done[lane]);
+            norm = pow((double)len, (double)c.penalty);
+        }
+        s.norm[lane] = norm;
+    }
+    for (int item = rank; item < n * slices; item += parts) {
+        const int k = item / slices;
+        const float sc = scores[k];
+        if ((done && done[k]) || !(fabsf(sc) < INFINITY)) continue;  // no need of its logits
+        const uint32_t first = min((uint64_t)(item % slices) * slice, (uint64_t)vocab), last = min(first + slice, vocab);
+        fold_row(static_cast<const T*>(c.logits) + r * c.batch_stride + k * c.beam_stride, first, last, keep, s, &s0->share[item]);
+    }
+    if (parts > 1) cl.sync();
+    else __syncthreads();
+    if (rank != 0) return;
+
+    // ---- the rows' logarithms
+    if (tid < n) {
+        float top = -INFINITY;
+        for (int i = 0; i < slices; ++i) top = fmaxf(top, s.share[tid * slices + i].top);
+        double sum = 0.0;
+        for (int i = 0; i < slices; ++i) {
+            const Share& h = s.share[tid * slices + i];
+            sum += h.top > -INFINITY ? h.sum * (slices > 1 ? expf(h.top - top) : 1.0f) : h.sum;
+        }
+        s.base[tid] = -(double)top - log(sum);
+    }
+    __syncthreads();
+    // ---- candidates of all rows
+    Pick list = {0, 0, 0.0f};
+    for (int item = warp; item < n * slices; item += kWarps) {
+        const int k = item / slices;
+        const float sc = scores[k];
+        Pick v = {0, 0, 0.0f};
+        if (fabsf(sc) < INFINITY) {
+            double total = 0.0;
+            bool any;
+            uint32_t token = 0;
+            if (done && done[k]) {
+                any = lane == 0 && item % slices == 0;
+                total = sc;
+                token = (uint32_t)max(c.end, 0);
+            } else {
+                const uint64_t key = s.share[item].keys[lane];
+                any = key != 0 && lane < keep;
+                token = 0xffffffffu - (uint32_t)key;
+                // (x - top) first: the difference of neighbours is exact
+                total = (double)sc + ((double)value_of((uint32_t)(key >> 32)) + s.base[k]);
+            }
+            const double q = total / s.norm[k];
+            if (any && q > -INFINITY && q < INFINITY) {
+                v.rank = ordered(q);
+                v.place = ~((uint64_t)k << 32 | token);
+                v.total = (float)total;
+            }
+        }
+        warp_take(list, v, lane);
+    }
+    block_merge(list, s.picks, lane, warp);
+    if (warp == 0 && lane < keep) {
+        const int64_t o = r * keep + lane;
+        int token = -1, parent = -1, length = 0;
+        bool ended = true;
+        float total = -INFINITY;
+        if (list.rank) {
+            const uint64_t place = ~list.place;
+            parent = (int)(place >> 32);
+            token = (int)(uint32_t)place;
+            total = list.total;
+            const bool was = done && done[parent];
+            if (was) token = c.end;
+            ended = was || (c.end >= 0 && token == c.end);
+            length = (lengths ? lengths[parent] : 0) + !was;
+        }
+        c.out_scores[o] = total;
+        c.out_tokens[o] = token;
+        c.out_parents[o] = parent;
+        if (c.out_done) c.out_done[o] = ended;
+        if (c.out_lengths) c.out_lengths[o] = length;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// reordering
+// ---------------------------------------------------------------------------
+
+// One column (of U) of all beams of a request and outer index at a time: a
+// thread reads what moves before it writes any of it, so beams may trade
+// places in place.
+template <class U, int MOST>
+__global__ void __launch_bounds__(kThreads) k_beam_reorder(const ReorderCall c) {
+    const int64_t units = c.inner / (int64_t)sizeof(U), chunks = (units + kThreads - 1) / kThreads;
+    const int64_t all = c.outer * c.batch * chunks;
+    for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
+        const int64_t row = div_fast(w, chunks), u = (w - row * chunks) * kThreads + threadIdx.x;
+        const int64_t o = div_fast(row, c.batch), r = row - o * c.batch;
+        if (u >= units) continue;
+        char* base = static_cast<char*>(c.state) + o * c.outer_stride + r * c.batch_stride + u * (int64_t)sizeof(U);
+        const int32_t* parents = c.parents + r * c.beams;
+        U v[MOST];
+        uint32_t moved = 0;
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+            if (k < c.beams) {
+                const int p = parents[k];
+                if (p != k && p >= 0 && p < c.beams) {
+                    moved |= 1u << k;
+                    v[k] = *reinterpret_cast<const U*>(base + p * c.beam_stride);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < MOST; ++k)
+            if (moved >> k & 1) *reinterpret_cast<U*>(base + k * c.beam_stride) = v[k];
+    }
+}
+
+template <class U>
+void launch_reorder(const ReorderCall& c, int sm_count, cudaStream_t stream) {
+    const int64_t chunks = (c.inner / (int64_t)sizeof(U) + kThreads - 1) / kThreads;
+    const unsigned grid = (unsigned)std::min<int64_t>(c.outer * c.batch * chunks, (int64_t)sm_count * 8);
+    if (c.beams <= 4) k_beam_reorder<U, 4><<<grid, kThreads, 0, stream>>>(c);
+    else if (c.beams <= 8) k_beam_reorder<U, 8><<<grid, kThreads, 0, stream>>>(c);
+    else if (c.beams <= 16) k_beam_reorder<U, 16><<<grid, kThreads, 0, stream>>>(c);
+    else k_beam_reorder<U, 32><<<grid, kThreads, 0, stream>>>(c);
+}
+
+}  // namespace bs
+
+ak_status run_beam_select(BeamCall c, cudaStream_t stream) {
+    using namespace bs;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return AK_ERR_CUDA;
+    // blocks of a request: as many as run at once over all requests, four an
+    // SM; whole rows each, or each row in slices of a round of loads at least
+    const int64_t room = std::max<int64_t>(1, std::min<int64_t>(kMaxParts, 4 * dev.sm_count / c.batch));
+    int parts = (int)std::min<int64_t>(room, c.beams);
+    c.slices = 1;
+    while ((c.slices + 1) * c.beams <= room && c.vocab / (c.slices + 1) >= kThreads * 4) ++c.slices;
+    if (c.slices > 1) parts = c.slices * c.beams;
+    auto* kernel = c.dtype == AK_F32 ? k_beam_select<float> : k_beam_select<bf16>;
+    static std::atomic<uint64_t> ready[2];
+    std::atomic<uint64_t>& set = ready[c.dtype == AK_F32];
+    if (!(set.load() >> dev.device & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e);
+        set.fetch_or(1ull << dev.device);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(c.batch * parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (log_on())
+        log_call("beam_select requests=%lld beams=%d vocab=%lld keep=%d: clusters of %d blocks, rows in %d slices",
+                 (long long)c.batch, c.beams, (long long)c.vocab, c.keep, parts, c.slices);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, c);
+    if (e != cudaSuccess) return cuda_fail(e);
+    count_launches(1);
+    return check_launch();
+}
+
+ak_status run_beam_reorder(const ReorderCall& c, cudaStream_t stream) {
+    using namespace bs;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return AK_ERR_CUDA;
+    const uint64_t bits = (uint64_t)reinterpret_cast<uintptr_t>(c.state) | (uint64_t)c.inner | (uint64_t)c.beam_stride |
+                          (uint64_t)c.batch_stride | (uint64_t)c.outer_stride;
+    if (bits % 16 == 0) launch_reorder<int4>(c, dev.sm_count, stream);
+    else if (bits % 4 == 0) launch_reorder<int32_t>(c, dev.sm_count, stream);
+    else if (bits % 2 == 0) launch_reorder<int16_t>(c, dev.sm_count, stream);
+    else launch_reorder<int8_t>(c, dev.sm_count, stream);
+    count_launches(1);
+    return check_launch();
+}
+
+}  // namespace ak
