@@ -24,10 +24,11 @@
 // the order of every sum is fixed, and there is neither a workspace nor a wait
 // on another cluster. The next tile's loads are in flight meanwhile.
 //
-// A is carried as its logarithm (in the decay form the sum of the gates, whose
-// error is relative to itself), and one above 1/2 is applied as A - 1: a factor
-// near one that is rounded itself is off by up to 3e-8, the same way each time
-// where gates are equal, for every token (or run) of a memory of thousands.
+// Of a run's or tile's A both A and A - 1 are held, and one above 1/2 is applied
+// as A - 1: a factor near one that is rounded itself is off by up to 3e-8, the
+// same way each time where gates are equal, for every token (or run) of a memory
+// of thousands. A - 1 comes from the sum of the gates (decay), or from the b_t
+// (gate), and its error is relative to itself.
 #include <algorithm>
 #include <atomic>
 #include <cooperative_groups.h>
@@ -108,40 +109,70 @@ __device__ __forceinline__ void store(T* p, const float (&v)[kVec], int left) {
     }
 }
 
-// a and b of a gate; both to their own relative precision.
-template <int FORM>
+// 2^x; an infinity gives 0 or an infinity, a NaN itself.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// a and b of a gate, both to their own relative precision: 2^-22 where the
+// results are bf16, a rounding or two where they are float32 (twice the
+// instructions, for twice the bytes). In the first, e stops at 2^126, where a
+// has long been nothing beside b.
+template <class T, int FORM>
 __device__ __forceinline__ void weights(float g, float& a, float& b) {
+    constexpr bool kFast = sizeof(T) == 2;
     if (FORM == AK_RECURRENCE_DECAY) {
-        a = expf(g);
+        a = kFast ? exp2_fast(g * kLog2e) : expf(g);
         b = 1.0f;
     } else {
-        const float e = expf(-fabsf(g)), r = __frcp_rn(1.0f + e);
-        a = g >= 0.0f ? r : e * r;
-        b = g >= 0.0f ? e * r : r;
+        if (kFast) {
+            const float e = exp2_fast(min_nan(g * -kLog2e, 126.0f));
+            a = rcp_fast(1.0f + e);
+            b = e * a;
+        } else {
+            const float e = expf(-fabsf(g)), r = __frcp_rn(1.0f + e);
+            a = g >= 0.0f ? r : e * r;
+            b = g >= 0.0f ? e * r : r;
+        }
     }
 }
 
-// A product of a's, by its logarithm.
+// A product of a's, and it less one.
 template <int FORM>
 struct Product {
-    float l = 0.0f;               // decay: the sum of the gates
-    float p = 1.0f, m = 0.0f;     // gate: the product, and the product less one
+    float p = FORM == AK_RECURRENCE_DECAY ? 0.0f : 1.0f, m = 0.0f;  // (decay: p is the sum of the gates until done)
     __device__ __forceinline__ void take(float g, float a, float b) {
         if (FORM == AK_RECURRENCE_DECAY) {
-            l += g;
+            p += g;
         } else {
             p *= a;
             m = fmaf(m, -b, m - b);  // (1 + m)(1 - b) - 1
         }
     }
-    __device__ __forceinline__ float log() const {
-        if (FORM == AK_RECURRENCE_DECAY) return l;
-        return p > 0.5f ? log1pf(m) : logf(p);
+    __device__ __forceinline__ void done() {
+        if (FORM == AK_RECURRENCE_DECAY) {
+            m = expm1f(p);
+            p = expf(p);
+        }
     }
 };
 
-// Whether the factor e^l is held less one, and a map's value at h.
-__device__ __forceinline__ bool is_near(float l) { return l > -0.6931f; }
+// A map h -> A h + off at h, of A and A - 1.
+__device__ __forceinline__ bool is_near(float p) { return p > 0.5f; }
 __device__ __forceinline__ float apply(float f, bool near, float off, bool reset, float h) {
     return reset ? off : fmaf(f, h, off) + (near ? h : 0.0f);
 }
@@ -165,6 +196,7 @@ struct Borders {
 // sequence for each token that has one.
 template <int R>
 struct Marks {
+    int any;  // of the tile, or a row of it lies outside every sequence
     uint32_t first[kTy], last[kTy];
     int seq_first[kTy * R], seq_last[kTy * R];
 };
@@ -175,8 +207,9 @@ struct Walk {
     int base, v;
     __device__ __forceinline__ void window(int lane) { v = base + lane <= b.n ? b.at(base + lane) : 0x7fffffff; }
     // Marks of tile [t0, t0 + kTy R); tiles come in increasing order.
-    __device__ __forceinline__ void mark(Marks<R>& k, int64_t t0, int lane) {
+    __device__ __forceinline__ void mark(Marks<R>& k, int64_t t0, int lane, int lo, int hi) {
         constexpr int kTile = kTy * R;
+        bool any = t0 < lo || t0 + kTile > hi;
         if (lane < kTy) k.first[lane] = k.last[lane] = 0;
         __syncwarp();
         while (true) {
@@ -184,10 +217,12 @@ struct Walk {
             if (lane < kWarp - 1 && base + lane < b.n && v < next) {
                 const int64_t f = v - t0, l = next - 1 - t0;
                 if (f >= 0 && f < kTile) {
+                    any = true;
                     k.seq_first[f] = base + lane;
                     atomicOr(&k.first[f / R], 1u << (f % R));
                 }
                 if (l >= 0 && l < kTile) {
+                    any = true;
                     k.seq_last[l] = base + lane;
                     atomicOr(&k.last[l / R], 1u << (l % R));
                 }
@@ -197,18 +232,25 @@ struct Walk {
             base += kWarp - 1;
             window(lane);
         }
+        any = __any_sync(0xffffffffu, any);
+        if (lane == 0) k.any = any;
         __syncwarp();
     }
 };
 
 template <int R>
 struct Shared {
-    float a[kTy][kCh], l[kTy][kCh], b[kTy][kCh];  // the runs' maps: factor (less one if near one), its logarithm, offset
+    float p[kTy][kCh], m[kTy][kCh], b[kTy][kCh];  // the runs' maps: factor, factor less one, offset
     float in[kTy][kCh];                           // the state before each run
     float2 peer[2][kMaxParts][kCh];               // the blocks' maps: factor (less one where `near`), offset
     uint32_t near[2][kMaxParts][kCh / kWarp];
     int reset[kTy], peer_reset[2][kMaxParts];     // whether a map forgets what was before
     Marks<R> marks[2];
+};
+
+template <bool B>
+struct Is {
+    static constexpr bool value = B;
 };
 
 template <class T, int FORM, int R, bool REV, bool WIDE>
@@ -217,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall
     constexpr bool kGate = FORM == AK_RECURRENCE_GATE;
     constexpr bool kRows = REV && !kGate;   // h_{t-1} is read for every token
     constexpr bool kAgain = REV && kGate;   // h_{t-1} is computed again from the one before the run
+    constexpr int RZ = REV ? R : 1, RB = kAgain ? R : 1;
     __shared__ Shared<R> s;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), parts = (int)cl.num_blocks();
@@ -231,14 +274,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall
     walk.b.tokens = (int)tokens;
     walk.b.n = (int)c.seqs;
     const int lo = walk.b.n ? walk.b.at(0) : 0, hi = walk.b.n ? walk.b.at(walk.b.n) : 0;
-    const int64_t steps = (tokens + (int64_t)kTile * parts - 1) / ((int64_t)kTile * parts);
+    const int steps = (int)((tokens + (int64_t)kTile * parts - 1) / ((int64_t)kTile * parts));
     const float* const first_state = REV ? c.dstate_out : c.state_in;
     float* const last_state = REV ? c.dstate_in : c.state_out;
-
-    const T* const xp = static_cast<const T*>(c.x.data) + ch;
-    const T* const gp = static_cast<const T*>(c.gate.data) + ch;
-    const T* const hp = static_cast<const T*>(c.h.data) + ch;
-    const T* const dp = static_cast<const T*>(c.dh.data) + ch;
 
     // sequences without tokens pass their state on
     if (last_state) {
@@ -253,166 +291,153 @@ __global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall
         }
     }
 
-    auto row_of = [&](int64_t v) { return REV ? tokens - 1 - v : v; };
+    // this thread's first row of an array, and the way to its next one
+    const int64_t t_first = (int64_t)rank * kTile, t_step = (int64_t)parts * kTile;
+    const int64_t row0 = REV ? tokens - 1 - (t_first + ty * R) : t_first + ty * R;
+    struct Rows {
+        T* p;
+        int64_t row, tile;
+    };
+    auto rows = [&](const ak_rows& r, int64_t shift) {
+        const int64_t st = REV ? -r.token_stride : r.token_stride;
+        return Rows{static_cast<T*>(r.data) + (row0 + shift) * r.token_stride + ch, st, st * t_step};
+    };
+    Rows gr = rows(c.gate, 0), ur = rows(REV ? c.dh : c.x, 0), zr = rows(kRows ? c.h : c.x, kRows ? -1 : 0);
+    Rows br = rows(c.h, -R);  // the row before the run's first token in time
+    Rows outr = rows(REV ? c.dx : c.out, 0), dgr = rows(c.dgate, 0);
+
     // raw inputs of one tile: the gate, what is scanned (x, or dh), and for
     // gradients h_{t-1} of each token, or x and the state before the run
-    Four<T> rg[R], ru[R], rz[REV ? R : 1], rb[1];
+    Four<T> rg[R], ru[R], rz[RZ], rb[1];
     auto fetch = [&](int64_t t0) {
         const int64_t v0 = t0 + ty * R;
+        if (t0 + kTile < tokens) {  // (the last row of all has none before it)
+            if (left > 0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t v = v0 + r, t = row_of(v);
-            rg[r] = ru[r] = Four<T>{};
-            if (REV) rz[r % (REV ? R : 1)] = Four<T>{};
-            if (v < tokens && left > 0) {
-                rg[r] = load<T, WIDE>(gp + t * c.gate.token_stride, left);
-                ru[r] = REV ? load<T, WIDE>(dp + t * c.dh.token_stride, left) : load<T, WIDE>(xp + t * c.x.token_stride, left);
-                if (kAgain) rz[r % (REV ? R : 1)] = load<T, WIDE>(xp + t * c.x.token_stride, left);
-                if (kRows && t > 0) rz[r % (REV ? R : 1)] = load<T, WIDE>(hp + (t - 1) * c.h.token_stride, left);
+                for (int r = 0; r < R; ++r) {
+                    rg[r] = load<T, WIDE>(gr.p + r * gr.row, left);
+                    ru[r] = load<T, WIDE>(ur.p + r * ur.row, left);
+                    if (REV) rz[r % RZ] = load<T, WIDE>(zr.p + r * zr.row, left);
+                }
+                if (kAgain) rb[0] = load<T, WIDE>(br.p, left);
             }
-        }
-        if (kAgain) {
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t v = v0 + r;
+                rg[r] = ru[r] = Four<T>{};
+                if (REV) rz[r % RZ] = Four<T>{};
+                if (v < tokens && left > 0) {
+                    rg[r] = load<T, WIDE>(gr.p + r * gr.row, left);
+                    ru[r] = load<T, WIDE>(ur.p + r * ur.row, left);
+                    if (REV && (kAgain || v + 1 < tokens)) rz[r % RZ] = load<T, WIDE>(zr.p + r * zr.row, left);
+                }
+            }
             rb[0] = Four<T>{};
-            const int64_t t = row_of(v0 + R - 1);
-            if (t > 0 && t < tokens && left > 0) rb[0] = load<T, WIDE>(hp + (t - 1) * c.h.token_stride, left);
+            if (kAgain && v0 + R < tokens && left > 0) rb[0] = load<T, WIDE>(br.p, left);
         }
+        gr.p += gr.tile, ur.p += ur.tile, zr.p += zr.tile, br.p += br.tile;
     };
 
     float carry = 0.0f;  // of channel c0 + tid, for tid < kCh
-    const int64_t t_first = (int64_t)rank * kTile, t_step = (int64_t)parts * kTile;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        rg[r] = ru[r] = Four<T>{};
+        if (REV) rz[r % RZ] = Four<T>{};
+    }
+    rb[0] = Four<T>{};
     fetch(t_first);
     constexpr int kMarker = kThreads / kWarp - 1;
     if (warp == kMarker) {
         walk.base = 0;
         walk.window(lane);
-        walk.mark(s.marks[0], t_first, lane);
+        walk.mark(s.marks[0], t_first, lane, lo, hi);
     }
     if (parts > 1) cl.sync();  // every block of the cluster runs before one writes to another
     else __syncthreads();
 
-    for (int64_t i = 0; i < steps; ++i) {
-        const int64_t t0 = i * t_step + t_first;
-        const Marks<R>& mk = s.marks[i & 1];
-        const uint32_t first = mk.first[ty], last = mk.last[ty];
-
-        // ---- fold of the run: B in `fold`, A in `prod`
-        float a[R][kVec], b[kGate && REV ? R : 1][kVec], u[R][kVec], z[REV ? R : 1][kVec], fold[kVec];
+    float a[R][kVec], b[RB][kVec], u[R][kVec], z[RZ][kVec];
+    // ---- the run's map; in a tile with marks, tokens that begin a sequence
+    // take its state and forget what was before
+    auto fold_run = [&](auto marked, const Marks<R>& mk) {
+        constexpr bool M = decltype(marked)::value;
+        const uint32_t first = M ? mk.first[ty] : 0, last = M ? mk.last[ty] : 0;
+        float fold[kVec] = {};
         Product<FORM> prod[kVec];
 #pragma unroll
-        for (int q = 0; q < kVec; ++q) fold[q] = 0.0f;
-#pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool begins = first >> r & 1;
+            const bool begins = M && (first >> r & 1);
             const float* from = begins && first_state ? first_state + walk.b.seq(mk.seq_first[ty * R + r]) * c.channels + ch : nullptr;
 #pragma unroll
             for (int q = 0; q < kVec; ++q) {
                 const float g = get(rg[r], q), in = get(ru[r], q);
                 float w;
-                weights<FORM>(g, a[r][q], w);
-                const float s0 = from && q < left ? from[q] : 0.0f;
+                weights<T, FORM>(g, a[r][q], w);
+                const float s0 = M && from && q < left ? from[q] : 0.0f;
                 if (REV) {
-                    if (kGate) b[r % (kGate && REV ? R : 1)][q] = w;
+                    if (kAgain) b[r % RB][q] = w;
                     u[r][q] = begins ? in + s0 : in;
                     fold[q] = a[r][q] * (begins ? u[r][q] : u[r][q] + fold[q]);
                 } else {
                     const float in_b = kGate ? w * in : in;
                     u[r][q] = begins ? fmaf(a[r][q], s0, in_b) : in_b;
-                    fold[q] = begins ? u[r][q] : fmaf(a[r][q], fold[q], u[r][q]);
+                    fold[q] = begins || r == 0 ? u[r][q] : fmaf(a[r][q], fold[q], u[r][q]);
                 }
                 prod[q].take(g, a[r][q], w);
             }
         }
-        // ---- h_{t-1} of each token (gradients)
-        if (REV) {
+        if (REV) {  // h_{t-1} of each token
             float hh[kVec];
 #pragma unroll
             for (int q = 0; q < kVec; ++q) hh[q] = kAgain ? get(rb[0], q) : 0.0f;
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) {  // forward in time
-                const bool begins = last >> r & 1;  // the sequence's first token
+                const bool begins = M && (last >> r & 1);  // the sequence's first token
                 const float* from = begins && c.state_in ? c.state_in + walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch : nullptr;
 #pragma unroll
                 for (int q = 0; q < kVec; ++q) {
-                    const float s0 = from && q < left ? from[q] : 0.0f;
+                    const float s0 = M && from && q < left ? from[q] : 0.0f;
                     if (kRows) {
-                        z[r % (REV ? R : 1)][q] = begins ? s0 : get(rz[r % (REV ? R : 1)], q);
+                        z[r % RZ][q] = begins ? s0 : get(rz[r % RZ], q);
                     } else {
-                        const float bq = b[r % (kGate && REV ? R : 1)][q], x = get(rz[r % (REV ? R : 1)], q);
+                        const float bq = b[r % RB][q], x = get(rz[r % RZ], q);
                         if (begins) hh[q] = s0;
-                        z[r % (REV ? R : 1)][q] = (hh[q] - x) * a[r][q] * bq;
+                        z[r % RZ][q] = (hh[q] - x) * (a[r][q] * bq);
                         hh[q] = fmaf(a[r][q], hh[q], bq * x);
                     }
                 }
             }
         }
-        if (i + 1 < steps) fetch(t0 + t_step);
-
-        // ---- the runs' maps meet
+        float p[kVec], m[kVec];
 #pragma unroll
         for (int q = 0; q < kVec; ++q) {
-            const float l = prod[q].log();
-            s.l[ty][lx * kVec + q] = l;
-            s.a[ty][lx * kVec + q] = is_near(l) ? expm1f(l) : expf(l);
-            s.b[ty][lx * kVec + q] = fold[q];
+            prod[q].done();
+            p[q] = prod[q].p, m[q] = prod[q].m;
         }
+        store_values(&s.p[ty][lx * kVec], p);
+        store_values(&s.m[ty][lx * kVec], m);
+        store_values(&s.b[ty][lx * kVec], fold);
         if (lx == 0) s.reset[ty] = first != 0;
-        __syncthreads();
-        if (warp == kMarker && i + 1 < steps) walk.mark(s.marks[(i + 1) & 1], t0 + t_step, lane);
-        float2 map = {};
-        uint32_t near = 0, run_near = 0, run_reset = 0;
-        if (tid < kCh) {
-            float l = 0.0f, off = 0.0f;
-#pragma unroll
-            for (int y = 0; y < kTy; ++y) {
-                const float ly = s.l[y][tid];
-                run_reset |= (uint32_t)s.reset[y] << y;
-                run_near |= (uint32_t)is_near(ly) << y;
-                off = apply(s.a[y][tid], is_near(ly), s.b[y][tid], run_reset >> y & 1, off);
-                l += ly;
-            }
-            near = __ballot_sync(0xffffffffu, is_near(l));
-            map = make_float2(is_near(l) ? expm1f(l) : expf(l), off);
-            for (int p = 0; p < parts && parts > 1; ++p) {
-                Shared<R>* o = cl.map_shared_rank(&s, p);
-                o->peer[i & 1][rank][tid] = map;
-                if (lane == 0) o->near[i & 1][rank][warp] = near;
-                if (tid == 0) o->peer_reset[i & 1][rank] = run_reset != 0;
-            }
-        }
-        if (parts > 1) cl.sync();
-        if (tid < kCh) {
-            auto of_peer = [&](int p, float h) {
-                const float2 m = s.peer[i & 1][p][tid];
-                return apply(m.x, s.near[i & 1][p][warp] >> lane & 1, m.y, s.peer_reset[i & 1][p], h);
-            };
-            float h = carry;
-            for (int p = 0; p < rank; ++p) h = of_peer(p, h);
-            carry = apply(map.x, near >> lane & 1, map.y, run_reset != 0, h);
-            for (int p = rank + 1; p < parts; ++p) carry = of_peer(p, carry);
-#pragma unroll
-            for (int y = 0; y < kTy; ++y) {
-                s.in[y][tid] = h;
-                h = apply(s.a[y][tid], run_near >> y & 1, s.b[y][tid], run_reset >> y & 1, h);
-            }
-        }
-        __syncthreads();
-
-        // ---- the run again, from its state
+    };
+    // ---- the run again, from its state
+    auto finish_run = [&](auto marked, const Marks<R>& mk, int64_t t0) {
+        constexpr bool M = decltype(marked)::value;
+        const uint32_t first = M ? mk.first[ty] : 0, last = M ? mk.last[ty] : 0;
         float h[kVec];
 #pragma unroll
         for (int q = 0; q < kVec; ++q) h[q] = s.in[ty][lx * kVec + q];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t v = t0 + ty * R + r, t = row_of(v);
-            const bool begins = first >> r & 1, inside = v >= lo && v < hi;
+            const int64_t v = t0 + ty * R + r;
+            const bool begins = M && (first >> r & 1), inside = !M || (v >= lo && v < hi);
             float o[kVec], og[kVec];
 #pragma unroll
             for (int q = 0; q < kVec; ++q) {
                 if (REV) {
                     const float g = begins ? u[r][q] : u[r][q] + h[q];
                     h[q] = a[r][q] * g;
-                    o[q] = kGate ? b[r % (kGate && REV ? R : 1)][q] * g : g;
-                    og[q] = kGate ? g * z[r % (REV ? R : 1)][q] : h[q] * z[r % (REV ? R : 1)][q];
+                    o[q] = kGate ? b[r % RB][q] * g : g;
+                    og[q] = (kGate ? g : h[q]) * z[r % RZ][q];
                     if (!inside) og[q] = 0.0f;
                 } else {
                     h[q] = begins ? u[r][q] : fmaf(a[r][q], h[q], u[r][q]);
@@ -420,21 +445,73 @@ __global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall
                 }
                 if (!inside) o[q] = 0.0f;
             }
-            if (v < tokens && left > 0) {
-                if (REV) {
-                    store<T, WIDE>(static_cast<T*>(c.dx.data) + ch + t * c.dx.token_stride, o, left);
-                    store<T, WIDE>(static_cast<T*>(c.dgate.data) + ch + t * c.dgate.token_stride, og, left);
-                } else {
-                    store<T, WIDE>(static_cast<T*>(c.out.data) + ch + t * c.out.token_stride, o, left);
-                }
+            if (left > 0 && (!M || v < tokens)) {
+                store<T, WIDE>(outr.p + r * outr.row, o, left);
+                if (REV) store<T, WIDE>(dgr.p + r * dgr.row, og, left);
             }
-            if ((last >> r & 1) && last_state) {
+            if (M && (last >> r & 1) && last_state) {
                 float* to = last_state + walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch;
 #pragma unroll
                 for (int q = 0; q < kVec; ++q)
                     if (q < left) to[q] = h[q];
             }
         }
+        outr.p += outr.tile, dgr.p += dgr.tile;
+    };
+
+    for (int i = 0; i < steps; ++i) {
+        const int64_t t0 = i * t_step + t_first;
+        const Marks<R>& mk = s.marks[i & 1];
+        const bool marked = mk.any;
+        if (marked) fold_run(Is<true>(), mk);
+        else fold_run(Is<false>(), mk);
+        if (i + 1 < steps) fetch(t0 + t_step);
+        __syncthreads();
+        if (warp == kMarker && i + 1 < steps) walk.mark(s.marks[(i + 1) & 1], t0 + t_step, lane, lo, hi);
+
+        // ---- the runs' maps meet
+        float2 map = {};
+        uint32_t near = 0;
+        int reset = 0;
+        if (tid < kCh) {
+            float p = 1.0f, m = 0.0f, off = 0.0f;
+#pragma unroll
+            for (int y = 0; y < kTy; ++y) {
+                const float py = s.p[y][tid], my = s.m[y][tid];
+                off = apply(is_near(py) ? my : py, is_near(py), s.b[y][tid], s.reset[y], off);
+                p *= py;
+                m = fmaf(m, my, m + my);
+                reset |= s.reset[y];
+            }
+            near = __ballot_sync(0xffffffffu, is_near(p));
+            map = make_float2(is_near(p) ? m : p, off);
+            for (int k = 0; k < parts && parts > 1; ++k) {
+                Shared<R>* o = cl.map_shared_rank(&s, k);
+                o->peer[i & 1][rank][tid] = map;
+                if (lane == 0) o->near[i & 1][rank][warp] = near;
+                if (tid == 0) o->peer_reset[i & 1][rank] = reset;
+            }
+        }
+        if (parts > 1) cl.sync();
+        if (tid < kCh) {
+            auto of_peer = [&](int k, float h) {
+                const float2 f = s.peer[i & 1][k][tid];
+                return apply(f.x, s.near[i & 1][k][warp] >> lane & 1, f.y, s.peer_reset[i & 1][k], h);
+            };
+            float h = carry;
+            for (int k = 0; k < rank; ++k) h = of_peer(k, h);
+            carry = apply(map.x, near >> lane & 1, map.y, reset != 0, h);
+            for (int k = rank + 1; k < parts; ++k) carry = of_peer(k, carry);
+#pragma unroll
+            for (int y = 0; y < kTy; ++y) {
+                const float py = s.p[y][tid];
+                s.in[y][tid] = h;
+                h = apply(is_near(py) ? s.m[y][tid] : py, is_near(py), s.b[y][tid], s.reset[y], h);
+            }
+        }
+        __syncthreads();
+        if (marked) finish_run(Is<true>(), mk, t0);
+        else finish_run(Is<false>(), mk, t0);
     }
 }
 
@@ -462,7 +539,7 @@ __global__ void __launch_bounds__(kThreads) k_step(const RecurrenceCall c, float
 #pragma unroll
         for (int q = 0; q < kVec; ++q) {
             float a, b;
-            weights<FORM>(get(g, q), a, b);
+            weights<float, FORM>(get(g, q), a, b);  // (states are float32)
             h[q] = fmaf(a, h[q], FORM == AK_RECURRENCE_GATE ? b * get(x, q) : get(x, q));
         }
         store<float, WIDE>(p, h, left);
