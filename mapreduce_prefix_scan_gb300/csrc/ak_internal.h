@@ -367,7 +367,13 @@ struct RecurrenceCall {
     float* state_out;
     const float* dstate_out;  // gradient of the final state, or null
     float* dstate_in;         // gradient of the initial state, or null
+    uint64_t epoch;           // left behind by a kernel that gave up waiting
+    int64_t wait_limit_ns;
+    int64_t skip_tile;        // the tile whose map is not sent (tests), or -1
+    bool wide_out;            // four values of every output row are one store; filled in by the launcher
 };
+// Whether the call of that epoch gave up waiting (the device has come to its end).
+ak_status recurrence_lost(uint64_t epoch, bool* lost);
 ak_status run_recurrence(const RecurrenceCall& c, cudaStream_t stream);
 ak_status run_recurrence_backward(const RecurrenceCall& c, cudaStream_t stream);
 ak_status run_recurrence_step(const RecurrenceCall& c, float* state, const int32_t* slots, int64_t nslots,

@@ -38,12 +38,27 @@ static bool good(const ak_recurrence* a, const ak_rows* x, bool output) {
     return !output || a->tokens == 1 || x->token_stride >= a->channels;
 }
 
-static RecurrenceCall call_of(const ak_recurrence* a) {
+// A shorter wait could run out where nothing is wrong.
+static constexpr int64_t kLeastWait = 100000000;
+
+static RecurrenceCall call_of(const ak_recurrence* a, const ak_opts& o) {
     RecurrenceCall c = {};
+    c.epoch = next_epoch();
+    c.wait_limit_ns = o.wait_limit_ns > kLeastWait ? o.wait_limit_ns : kLeastWait;
+    c.skip_tile = o.debug_skip_publish_tile;
     c.dtype = (ak_dtype)a->dtype;
     c.form = a->form;
     c.tokens = a->tokens, c.seqs = a->seqs, c.channels = a->channels;
     return c;
+}
+
+// With opts->check: waits for the call and reports a wait that ran out.
+static ak_status finish_recurrence(ak_status s, const RecurrenceCall& c, const ak_opts* opts, void* stream) {
+    s = finish(s, opts, stream);
+    if (s != AK_OK || !resolve_opts(opts).check) return s;
+    bool lost = false;
+    s = recurrence_lost(c.epoch, &lost);
+    return s == AK_OK && lost ? AK_ERR_TIMEOUT : s;
 }
 
 extern "C" ak_status ak_gated_recurrence(const ak_recurrence* a, const ak_rows* x, const ak_rows* gate,
@@ -55,10 +70,10 @@ extern "C" ak_status ak_gated_recurrence(const ak_recurrence* a, const ak_rows* 
     if (!word_ptr(offsets, a->seqs != 1) || !word_ptr(state_in, false) || !word_ptr(state_out, false))
         return AK_ERR_INVALID_ARG;
     if (a->tokens == 0 && (a->seqs == 0 || !state_out)) return AK_OK;
-    RecurrenceCall c = call_of(a);
+    RecurrenceCall c = call_of(a, resolve_opts(opts));
     c.x = *x, c.gate = *gate, c.out = *h;
     c.offsets = offsets, c.state_in = state_in, c.state_out = state_out;
-    return finish(run_recurrence(c, static_cast<cudaStream_t>(stream)), opts, stream);
+    return finish_recurrence(run_recurrence(c, static_cast<cudaStream_t>(stream)), c, opts, stream);
 }
 
 extern "C" ak_status ak_gated_recurrence_backward(const ak_recurrence* a, const ak_rows* dh, const ak_rows* x,
@@ -76,11 +91,11 @@ extern "C" ak_status ak_gated_recurrence_backward(const ak_recurrence* a, const 
         !word_ptr(dstate_in, false))
         return AK_ERR_INVALID_ARG;
     if (a->tokens == 0 && (a->seqs == 0 || !dstate_in)) return AK_OK;
-    RecurrenceCall c = call_of(a);
+    RecurrenceCall c = call_of(a, resolve_opts(opts));
     c.dh = *dh, c.gate = *gate, c.h = *h, c.dx = *dx, c.dgate = *dgate;
     if (reads_x) c.x = *x;
     c.offsets = offsets, c.state_in = state_in, c.dstate_out = dstate_out, c.dstate_in = dstate_in;
-    return finish(run_recurrence_backward(c, static_cast<cudaStream_t>(stream)), opts, stream);
+    return finish_recurrence(run_recurrence_backward(c, static_cast<cudaStream_t>(stream)), c, opts, stream);
 }
 
 extern "C" ak_status ak_gated_recurrence_step(const ak_recurrence* a, const ak_rows* x, const ak_rows* gate,
@@ -93,7 +108,7 @@ extern "C" ak_status ak_gated_recurrence_step(const ak_recurrence* a, const ak_r
     // a thread takes four channels of a request
     if ((a->channels + 3) / 4 > kMost * 256 / (a->tokens ? a->tokens : 1)) return AK_ERR_INVALID_ARG;
     if (a->tokens == 0) return AK_OK;
-    RecurrenceCall c = call_of(a);
+    RecurrenceCall c = call_of(a, resolve_opts(opts));
     c.x = *x, c.gate = *gate, c.out = *h;
     if (log_on())
         log_call("gated_recurrence_step requests=%lld channels=%lld: one launch", (long long)a->tokens, (long long)a->channels);

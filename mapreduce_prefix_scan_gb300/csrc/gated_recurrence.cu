@@ -13,16 +13,19 @@
 // time (virtual token v = tokens - 1 - t), with a reset where a sequence begins.
 //
 // A cluster of up to 16 blocks takes 64 channels and walks the whole packed
-// axis, a tile of kTy x R tokens for each block and step, whatever the
+// axis, a tile of 8 runs of R tokens for each block and step, whatever the
 // sequences' lengths: balance does not depend on them, each input is read once
-// and each output written once. In a tile a thread holds R consecutive tokens of 4
-// channels in registers and folds them to (A, B), h -> A h + B; 64 threads fold
-// the tile's 16 pairs, hand the block's pair to every block of the cluster
-// (distributed shared memory), and after the cluster's barrier fold the pairs
-// before them onto the state carried from the last step. So a token is a few
-// dozen roundings away from any earlier one, not one for each token between,
-// the order of every sum is fixed, and there is neither a workspace nor a wait
-// on another cluster. The next tile's loads are in flight meanwhile.
+// and each output written once. In a tile a thread folds R consecutive tokens of 2
+// channels, which it keeps in registers, to a map h -> A h + B; a thread for each
+// channel folds the tile's 8 maps, sends the block's map to every block of the
+// cluster, and when theirs have come folds the maps before its own onto the
+// state carried from the last step. So a token is a few dozen roundings away from
+// any earlier one, not one for each token between, the order of every sum is fixed,
+// and there is neither a workspace nor a wait on another cluster. The next two
+// tiles' copies to shared memory are under way meanwhile. Maps travel as
+// asynchronous stores that count on the receiver's barrier: a cluster-wide
+// barrier after plain stores took 1500 to 2500 cycles of a step's 5500, most of
+// them the fence before it.
 //
 // Of a run's or tile's A both A and A - 1 are held, and one above 1/2 is applied
 // as A - 1: a factor near one that is rounded itself is off by up to 3e-8, the
@@ -35,6 +38,7 @@
 
 #include "ak_common.cuh"
 #include "ak_internal.h"
+#include "ak_tma.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -42,69 +46,56 @@ namespace ak {
 namespace gr {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;                       // channels of a thread
-constexpr int kLx = 16;                       // threads along the channels
+constexpr int kVec = 2;                       // channels of a thread
+constexpr int kLx = kWarp;                    // threads along the channels
 constexpr int kCh = kVec * kLx;               // channels of a block
 constexpr int kTy = kThreads / kLx;           // runs of tokens of a tile
 constexpr int kMaxParts = 16;                 // blocks of a cluster
+constexpr int kAhead = 4;                     // maps read before the first of them is applied
+constexpr int kStages = 2;                    // tiles on their way
 
-// Four neighbouring values as they lie in memory.
-template <class T>
-struct alignas(4 * sizeof(T)) Four {
-    uint32_t w[sizeof(T)];
+// Neighbouring values as they lie in memory.
+template <class T, int N>
+struct alignas(N * sizeof(T)) Values {
+    uint32_t w[N * sizeof(T) / 4];
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
 };
 
-__device__ __forceinline__ float get(const Four<float>& f, int i) { return __uint_as_float(f.w[i]); }
-__device__ __forceinline__ float get(const Four<bf16>& f, int i) {
-    return __uint_as_float(i % 2 ? f.w[i / 2] & 0xffff0000u : f.w[i / 2] << 16);
+// 16 bytes (or the first `size` of them, zeros past them) into shared memory.
+__device__ __forceinline__ void copy16(void* to, const void* from, int size) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from), "r"(size)
+                 : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ Four<float> ld_four(const float* p) {
-    Four<float> f;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-        : "=r"(f.w[0]), "=r"(f.w[1]), "=r"(f.w[2]), "=r"(f.w[3]) : "l"(p));
-    return f;
-}
-__device__ __forceinline__ Four<bf16> ld_four(const bf16* p) {
-    Four<bf16> f;
-    asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(f.w[0]), "=r"(f.w[1]) : "l"(p));
-    return f;
-}
-
-// Values [0, left) of four at p, zeros past them.
-template <class T, bool WIDE>
-__device__ __forceinline__ Four<T> load(const T* p, int left) {
-    if constexpr (WIDE) {
-        return ld_four(p);
-    } else {
-        T v[kVec];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = i < left ? p[i] : T(0.0f);
-        Four<T> f;
-        memcpy(&f, v, sizeof f);
-        return f;
-    }
-}
-
-__device__ __forceinline__ void store_values(float* p, const float (&v)[kVec]) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store_values(bf16* p, const float (&v)[kVec]) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-    uint2 u;
-    memcpy(&u.x, &lo, 4);
-    memcpy(&u.y, &hi, 4);
-    *reinterpret_cast<uint2*>(p) = u;
-}
 __device__ __forceinline__ void set(float* p, float v) { *p = v; }
 __device__ __forceinline__ void set(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <class T, bool WIDE>
-__device__ __forceinline__ void store(T* p, const float (&v)[kVec], int left) {
-    if constexpr (WIDE) store_values(p, v);
-    else {
+// Values [0, left) of v; in one store where `whole`.
+template <class T, int N>
+__device__ __forceinline__ void store(T* p, const float (&v)[N], int left, bool whole) {
+    if (whole) {
+        Values<T, N> o;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
+        for (int i = 0; i < (int)(N * sizeof(T) / 4); ++i) {
+            if constexpr (sizeof(T) == 4) {
+                o.w[i] = __float_as_uint(v[i]);
+            } else {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                memcpy(&o.w[i], &two, 4);
+            }
+        }
+        *reinterpret_cast<Values<T, N>*>(p) = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
             if (i < left) set(p + i, v[i]);
     }
 }
@@ -171,11 +162,58 @@ struct Product {
     }
 };
 
-// A map h -> A h + off at h, of A and A - 1.
-__device__ __forceinline__ bool is_near(float p) { return p > 0.5f; }
-__device__ __forceinline__ float apply(float f, bool near, float off, bool reset, float h) {
-    return reset ? off : fmaf(f, h, off) + (near ? h : 0.0f);
+// h -> A h + off, or off alone (a value that is not finite must not pass a
+// reset, so it is no factor of 0). A above 1/2 is one and f, else f alone.
+struct Map {
+    float f, one, off;
+    uint32_t reset;
+    __device__ __forceinline__ float operator()(float h) const {
+        const float v = fmaf(one, h, fmaf(f, h, off));
+        return reset ? off : v;
+    }
+};
+// A product of such A's in the making: A and A - 1.
+struct Factor {
+    float p = 1.0f, m = 0.0f;
+    // this one, then the factor of `o`
+    __device__ __forceinline__ Factor then(const Map& o) const {
+        const float om = o.f + (o.one - 1.0f);
+        Factor r;
+        r.p = p * (o.f + o.one);
+        r.m = fmaf(m, om, m + om);
+        return r;
+    }
+    __device__ __forceinline__ Map map(float off, uint32_t reset) const {
+        const bool near = p > 0.5f;
+        return {near ? m : p, near ? 1.0f : 0.0f, off, reset};
+    }
+};
+// What a channel's maps are to the blocks of its cluster: asynchronous stores
+// whose bytes count on the receiver's barrier.
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
 }
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, const Map& m) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(__float_as_uint(m.f)), "r"(__float_as_uint(m.one)), "r"(__float_as_uint(m.off)), "r"(m.reset), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool try_received(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// The call whose wait ran out last (its epoch): for opts->check.
+__device__ uint64_t g_gave_up;
 
 // The sequences' borders along the virtual axis, boundary by boundary: one
 // warp's window of 32 of them, moved on as the walk passes it.
@@ -196,7 +234,6 @@ struct Borders {
 // sequence for each token that has one.
 template <int R>
 struct Marks {
-    int any;  // of the tile, or a row of it lies outside every sequence
     uint32_t first[kTy], last[kTy];
     int seq_first[kTy * R], seq_last[kTy * R];
 };
@@ -207,9 +244,8 @@ struct Walk {
     int base, v;
     __device__ __forceinline__ void window(int lane) { v = base + lane <= b.n ? b.at(base + lane) : 0x7fffffff; }
     // Marks of tile [t0, t0 + kTy R); tiles come in increasing order.
-    __device__ __forceinline__ void mark(Marks<R>& k, int64_t t0, int lane, int lo, int hi) {
+    __device__ __forceinline__ void mark(Marks<R>& k, int64_t t0, int lane) {
         constexpr int kTile = kTy * R;
-        bool any = t0 < lo || t0 + kTile > hi;
         if (lane < kTy) k.first[lane] = k.last[lane] = 0;
         __syncwarp();
         while (true) {
@@ -217,12 +253,10 @@ struct Walk {
             if (lane < kWarp - 1 && base + lane < b.n && v < next) {
                 const int64_t f = v - t0, l = next - 1 - t0;
                 if (f >= 0 && f < kTile) {
-                    any = true;
                     k.seq_first[f] = base + lane;
                     atomicOr(&k.first[f / R], 1u << (f % R));
                 }
                 if (l >= 0 && l < kTile) {
-                    any = true;
                     k.seq_last[l] = base + lane;
                     atomicOr(&k.last[l / R], 1u << (l % R));
                 }
@@ -232,35 +266,38 @@ struct Walk {
             base += kWarp - 1;
             window(lane);
         }
-        any = __any_sync(0xffffffffu, any);
-        if (lane == 0) k.any = any;
         __syncwarp();
     }
 };
 
-template <int R>
-struct Shared {
-    float p[kTy][kCh], m[kTy][kCh], b[kTy][kCh];  // the runs' maps: factor, factor less one, offset
-    float in[kTy][kCh];                           // the state before each run
-    float2 peer[2][kMaxParts][kCh];               // the blocks' maps: factor (less one where `near`), offset
-    uint32_t near[2][kMaxParts][kCh / kWarp];
-    int reset[kTy], peer_reset[2][kMaxParts];     // whether a map forgets what was before
+// Inputs of a tile: the gate, what is scanned (x, or dh), and for gradients
+// h_{t-1} of each token (decay), or x and the state before each run (gate).
+template <class T, int R, bool REV, bool AGAIN>
+struct Tile {
+    T g[kTy * R][kCh], u[kTy * R][kCh], z[REV ? kTy * R : 1][REV ? kCh : 8], before[AGAIN ? kTy : 1][AGAIN ? kCh : 8];
+};
+
+template <class T, int R, bool REV, bool AGAIN>
+struct alignas(16) Shared {
+    Tile<T, R, REV, AGAIN> tile[kStages];
+    float4 run[kTy][kCh];  // the runs' maps; channel 2 i + q at 32 q + i, so that neighbouring threads' lie side by side
+    float in[kTy][kCh];    // the state before each run, in that order
     Marks<R> marks[2];
+    uint64_t come[2];  // maps of the even and of the odd steps
+    int lost;
+    float4 peer[1];  // [2][parts][kCh]: the blocks' maps
 };
 
-template <bool B>
-struct Is {
-    static constexpr bool value = B;
-};
-
-template <class T, int FORM, int R, bool REV, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall c) {
+template <class T, int FORM, int R, bool REV, bool WIDE, int PER_SM>
+__global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const RecurrenceCall c) {
     constexpr int kTile = kTy * R;
     constexpr bool kGate = FORM == AK_RECURRENCE_GATE;
     constexpr bool kRows = REV && !kGate;   // h_{t-1} is read for every token
     constexpr bool kAgain = REV && kGate;   // h_{t-1} is computed again from the one before the run
     constexpr int RZ = REV ? R : 1, RB = kAgain ? R : 1;
-    __shared__ Shared<R> s;
+    extern __shared__ __align__(16) unsigned char smem[];
+    using S = Shared<T, R, REV, kAgain>;
+    S& s = *reinterpret_cast<S*>(smem);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), parts = (int)cl.num_blocks();
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
@@ -268,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall
     const int64_t c0 = (int64_t)(blockIdx.x / parts) * kCh;
     const int64_t ch = c0 + lx * kVec;
     const int left = (int)max((int64_t)0, min((int64_t)kVec, c.channels - ch));
+    const bool whole = c.wide_out && left == kVec;
     const int64_t tokens = c.tokens;
     Walk<R, REV> walk;
     walk.b.offsets = c.offsets;
@@ -277,7 +315,70 @@ __global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall
     const int steps = (int)((tokens + (int64_t)kTile * parts - 1) / ((int64_t)kTile * parts));
     const float* const first_state = REV ? c.dstate_out : c.state_in;
     float* const last_state = REV ? c.dstate_in : c.state_out;
+    const int64_t t_first = (int64_t)rank * kTile, t_step = (int64_t)parts * kTile;
+    auto row_of = [&](int64_t v) { return REV ? tokens - 1 - v : v; };
 
+    // `rows` rows of an array, `apart` virtual tokens apart from v0 on (row + shift in
+    // memory), those below `end` of them; the others are zeros
+    auto copy = [&](T* to, const ak_rows& from, int rows, int apart, int64_t v0, int shift, int64_t end) {
+        const T* base = static_cast<const T*>(from.data) + c0;
+        if constexpr (WIDE) {
+            constexpr int kPer = 16 / (int)sizeof(T), kRow = kCh / kPer;
+            const int col = tid % kRow * kPer;
+            const int bytes = (int)max((int64_t)0, min((int64_t)kPer, c.channels - c0 - col)) * (int)sizeof(T);
+            int64_t v = v0 + (int64_t)(tid / kRow) * apart;
+            const T* p = base + (row_of(v) + shift) * from.token_stride + col;
+            const int64_t step = (int64_t)(REV ? -1 : 1) * (kThreads / kRow) * apart * from.token_stride;
+#pragma unroll
+            for (int r = 0; r < rows; r += kThreads / kRow) {
+                const bool in = v < end && bytes > 0;
+                if (r + tid / kRow < rows) copy16(to + (r + tid / kRow) * kCh + col, in ? p : base, in ? bytes : 0);
+                v += (kThreads / kRow) * apart;
+                p += step;
+            }
+        } else {
+            const int col = tid % kCh;
+            const bool some = c0 + col < c.channels;
+            constexpr int kOnce = 8;
+            for (int r0 = tid / kCh; r0 < rows; r0 += kOnce * (kThreads / kCh)) {
+                T v[kOnce];
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) {
+                    const int r = r0 + i * (kThreads / kCh);
+                    const int64_t at = v0 + (int64_t)r * apart;
+                    v[i] = some && r < rows && at < end ? base[(row_of(at) + shift) * from.token_stride + col] : T(0.0f);
+                }
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) {
+                    const int r = r0 + i * (kThreads / kCh);
+                    if (r < rows) to[r * kCh + col] = v[i];
+                }
+            }
+        }
+    };
+    auto fetch = [&](int i) {
+        auto& t = s.tile[i % kStages];
+        const int64_t v0 = t_first + i * t_step;
+        if (i < steps) {
+            copy(&t.g[0][0], c.gate, kTile, 1, v0, 0, tokens);
+            copy(&t.u[0][0], REV ? c.dh : c.x, kTile, 1, v0, 0, tokens);
+            if constexpr (kAgain) {
+                copy(&t.z[0][0], c.x, kTile, 1, v0, 0, tokens);
+                // the row before the run's first token in time
+                copy(&t.before[0][0], c.h, kTy, R, v0 + R - 1, -1, tokens - 1);
+            }
+            if constexpr (kRows) copy(&t.z[0][0], c.h, kTile, 1, v0, -1, tokens - 1);
+        }
+        copy_commit();
+    };
+    constexpr int kMarker = kThreads / kWarp - 1;
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(i);
+    if (warp == kMarker) {
+        walk.base = 0;
+        walk.window(lane);
+        walk.mark(s.marks[0], t_first, lane);
+    }
     // sequences without tokens pass their state on
     if (last_state) {
         for (int j0 = (rank * (kThreads / kWarp) + warp) * kWarp; j0 < walk.b.n; j0 += parts * kThreads) {
@@ -290,243 +391,307 @@ __global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceCall
             }
         }
     }
-
-    // this thread's first row of an array, and the way to its next one
-    const int64_t t_first = (int64_t)rank * kTile, t_step = (int64_t)parts * kTile;
-    const int64_t row0 = REV ? tokens - 1 - (t_first + ty * R) : t_first + ty * R;
-    struct Rows {
-        T* p;
-        int64_t row, tile;
-    };
-    auto rows = [&](const ak_rows& r, int64_t shift) {
-        const int64_t st = REV ? -r.token_stride : r.token_stride;
-        return Rows{static_cast<T*>(r.data) + (row0 + shift) * r.token_stride + ch, st, st * t_step};
-    };
-    Rows gr = rows(c.gate, 0), ur = rows(REV ? c.dh : c.x, 0), zr = rows(kRows ? c.h : c.x, kRows ? -1 : 0);
-    Rows br = rows(c.h, -R);  // the row before the run's first token in time
-    Rows outr = rows(REV ? c.dx : c.out, 0), dgr = rows(c.dgate, 0);
-
-    // raw inputs of one tile: the gate, what is scanned (x, or dh), and for
-    // gradients h_{t-1} of each token, or x and the state before the run
-    Four<T> rg[R], ru[R], rz[RZ], rb[1];
-    auto fetch = [&](int64_t t0) {
-        const int64_t v0 = t0 + ty * R;
-        if (t0 + kTile < tokens) {  // (the last row of all has none before it)
-            if (left > 0) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    rg[r] = load<T, WIDE>(gr.p + r * gr.row, left);
-                    ru[r] = load<T, WIDE>(ur.p + r * ur.row, left);
-                    if (REV) rz[r % RZ] = load<T, WIDE>(zr.p + r * zr.row, left);
-                }
-                if (kAgain) rb[0] = load<T, WIDE>(br.p, left);
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int64_t v = v0 + r;
-                rg[r] = ru[r] = Four<T>{};
-                if (REV) rz[r % RZ] = Four<T>{};
-                if (v < tokens && left > 0) {
-                    rg[r] = load<T, WIDE>(gr.p + r * gr.row, left);
-                    ru[r] = load<T, WIDE>(ur.p + r * ur.row, left);
-                    if (REV && (kAgain || v + 1 < tokens)) rz[r % RZ] = load<T, WIDE>(zr.p + r * zr.row, left);
-                }
-            }
-            rb[0] = Four<T>{};
-            if (kAgain && v0 + R < tokens && left > 0) rb[0] = load<T, WIDE>(br.p, left);
+    if (tid == 0) {
+        s.lost = 0;
+        if (parts > 1) {
+            mbar_init(&s.come[0], 1);
+            mbar_init(&s.come[1], 1);
+            fence_barrier_init();
         }
-        gr.p += gr.tile, ur.p += ur.tile, zr.p += zr.tile, br.p += br.tile;
-    };
-
-    float carry = 0.0f;  // of channel c0 + tid, for tid < kCh
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        rg[r] = ru[r] = Four<T>{};
-        if (REV) rz[r % RZ] = Four<T>{};
     }
-    rb[0] = Four<T>{};
-    fetch(t_first);
-    constexpr int kMarker = kThreads / kWarp - 1;
-    if (warp == kMarker) {
-        walk.base = 0;
-        walk.window(lane);
-        walk.mark(s.marks[0], t_first, lane, lo, hi);
-    }
-    if (parts > 1) cl.sync();  // every block of the cluster runs before one writes to another
-    else __syncthreads();
+    if (parts > 1) cl.sync();  // every block of the cluster runs, with its barriers, before one sends to another
 
     float a[R][kVec], b[RB][kVec], u[R][kVec], z[RZ][kVec];
-    // ---- the run's map; in a tile with marks, tokens that begin a sequence
-    // take its state and forget what was before
-    auto fold_run = [&](auto marked, const Marks<R>& mk) {
-        constexpr bool M = decltype(marked)::value;
-        const uint32_t first = M ? mk.first[ty] : 0, last = M ? mk.last[ty] : 0;
-        float fold[kVec] = {};
+    // this thread's channels of a sequence's state
+    auto state_of = [&](const float* states, int64_t seq, float (&v)[kVec]) {
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) v[q] = states && q < left ? states[seq * c.channels + ch + q] : 0.0f;
+    };
+    // ---- the run's map. A token that begins a sequence takes its state, and its
+    // factor is 0: it forgets what was before, which is dropped as well, as it may
+    // not be finite. Such tokens are rare; only the chains, a few dozen
+    // instructions each, exist with and without them. (Larger paths of their own
+    // wait for their instructions, 200 cycles a token; a branch for every token
+    // keeps them from overlapping.)
+    auto fold_run = [&](const Marks<R>& mk, const Tile<T, R, REV, kAgain>& t) {
+        const uint32_t first = mk.first[ty];
+        [[maybe_unused]] const uint32_t last = mk.last[ty];
+        auto values = [&](const T* row) { return *reinterpret_cast<const Values<T, kVec>*>(row + lx * kVec); };
         Product<FORM> prod[kVec];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool begins = M && (first >> r & 1);
-            const float* from = begins && first_state ? first_state + walk.b.seq(mk.seq_first[ty * R + r]) * c.channels + ch : nullptr;
+            const Values<T, kVec> rg = values(t.g[ty * R + r]), ru = values(t.u[ty * R + r]);
+            [[maybe_unused]] Values<T, kVec> rz;
+            if constexpr (REV) rz = values(t.z[ty * R + r]);
 #pragma unroll
             for (int q = 0; q < kVec; ++q) {
-                const float g = get(rg[r], q), in = get(ru[r], q);
                 float w;
-                weights<T, FORM>(g, a[r][q], w);
-                const float s0 = M && from && q < left ? from[q] : 0.0f;
-                if (REV) {
-                    if (kAgain) b[r % RB][q] = w;
-                    u[r][q] = begins ? in + s0 : in;
-                    fold[q] = a[r][q] * (begins ? u[r][q] : u[r][q] + fold[q]);
-                } else {
-                    const float in_b = kGate ? w * in : in;
-                    u[r][q] = begins ? fmaf(a[r][q], s0, in_b) : in_b;
-                    fold[q] = begins || r == 0 ? u[r][q] : fmaf(a[r][q], fold[q], u[r][q]);
-                }
-                prod[q].take(g, a[r][q], w);
+                weights<T, FORM>(rg[q], a[r][q], w);
+                prod[q].take(rg[q], a[r][q], w);
+                u[r][q] = kGate && !REV ? w * ru[q] : ru[q];
+                if constexpr (kAgain) b[r][q] = w;
+                if constexpr (REV) z[r][q] = rz[q];
             }
         }
-        if (REV) {  // h_{t-1} of each token
-            float hh[kVec];
+        if constexpr (REV) {  // h_{t-1} of each token, forward in time
+            float hh[kVec] = {};
+            if constexpr (kAgain) {
+                const Values<T, kVec> rb = values(t.before[ty]);
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) hh[q] = kAgain ? get(rb[0], q) : 0.0f;
-#pragma unroll
-            for (int r = R - 1; r >= 0; --r) {  // forward in time
-                const bool begins = M && (last >> r & 1);  // the sequence's first token
-                const float* from = begins && c.state_in ? c.state_in + walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch : nullptr;
+                for (int q = 0; q < kVec; ++q) hh[q] = rb[q];
+            }
+            auto again = [&](int r) {
 #pragma unroll
                 for (int q = 0; q < kVec; ++q) {
-                    const float s0 = M && from && q < left ? from[q] : 0.0f;
-                    if (kRows) {
-                        z[r % RZ][q] = begins ? s0 : get(rz[r % RZ], q);
-                    } else {
-                        const float bq = b[r % RB][q], x = get(rz[r % RZ], q);
-                        if (begins) hh[q] = s0;
-                        z[r % RZ][q] = (hh[q] - x) * (a[r][q] * bq);
-                        hh[q] = fmaf(a[r][q], hh[q], bq * x);
-                    }
+                    const float bx = b[r % RB][q] * z[r][q];
+                    z[r][q] = (hh[q] - z[r][q]) * (a[r][q] * b[r % RB][q]);
+                    hh[q] = fmaf(a[r][q], hh[q], bx);
                 }
+            };
+            if (last) {
+#pragma unroll
+                for (int r = R - 1; r >= 0; --r) {
+                    if (last & 1u << r) {  // the sequence's first token
+                        float s0[kVec];
+                        state_of(c.state_in, walk.b.seq(mk.seq_last[ty * R + r]), s0);
+#pragma unroll
+                        for (int q = 0; q < kVec; ++q) {
+                            hh[q] = s0[q];
+                            if (kRows) z[r][q] = s0[q];
+                        }
+                    }
+                    if constexpr (kAgain) again(r);
+                }
+            } else if constexpr (kAgain) {
+#pragma unroll
+                for (int r = R - 1; r >= 0; --r) again(r);
             }
         }
-        float p[kVec], m[kVec];
+        float fold[kVec] = {};
+        auto add = [&](int r) {
+#pragma unroll
+            for (int q = 0; q < kVec; ++q)
+                fold[q] = REV ? a[r][q] * (u[r][q] + fold[q]) : fmaf(a[r][q], fold[q], u[r][q]);
+        };
+        if (first) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (first & 1u << r) {
+                    float s0[kVec];
+                    state_of(first_state, walk.b.seq(mk.seq_first[ty * R + r]), s0);
+#pragma unroll
+                    for (int q = 0; q < kVec; ++q) {
+                        fold[q] = 0.0f;
+                        if (REV) {
+                            u[r][q] += s0[q];
+                        } else {
+                            if (first_state) u[r][q] = fmaf(a[r][q], s0[q], u[r][q]);
+                            a[r][q] = 0.0f;
+                        }
+                    }
+                }
+                add(r);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) add(r);
+        }
 #pragma unroll
         for (int q = 0; q < kVec; ++q) {
             prod[q].done();
-            p[q] = prod[q].p, m[q] = prod[q].m;
+            const Map m = Factor{prod[q].p, prod[q].m}.map(fold[q], first != 0);
+            s.run[ty][q * kLx + lx] = make_float4(m.f, m.one, m.off, __uint_as_float(m.reset));
         }
-        store_values(&s.p[ty][lx * kVec], p);
-        store_values(&s.m[ty][lx * kVec], m);
-        store_values(&s.b[ty][lx * kVec], fold);
-        if (lx == 0) s.reset[ty] = first != 0;
     };
-    // ---- the run again, from its state
-    auto finish_run = [&](auto marked, const Marks<R>& mk, int64_t t0) {
-        constexpr bool M = decltype(marked)::value;
-        const uint32_t first = M ? mk.first[ty] : 0, last = M ? mk.last[ty] : 0;
+    // ---- the run again, from its state: u becomes h_t, or G_t
+    T* const out = static_cast<T*>(REV ? c.dx.data : c.out.data) + ch;
+    T* const out_g = static_cast<T*>(c.dgate.data) + ch;
+    const int64_t out_stride = REV ? c.dx.token_stride : c.out.token_stride;
+    auto finish_run = [&](const Marks<R>& mk, int64_t t0) {
+        const uint32_t first = mk.first[ty], last = mk.last[ty];
+        const int64_t v0 = t0 + ty * R;
         float h[kVec];
 #pragma unroll
-        for (int q = 0; q < kVec; ++q) h[q] = s.in[ty][lx * kVec + q];
+        for (int q = 0; q < kVec; ++q) h[q] = s.in[ty][q * kLx + lx];
+        auto move = [&](int r) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t v = t0 + ty * R + r;
-            const bool begins = M && (first >> r & 1), inside = !M || (v >= lo && v < hi);
+            for (int q = 0; q < kVec; ++q) {
+                u[r][q] = REV ? u[r][q] + h[q] : fmaf(a[r][q], h[q], u[r][q]);
+                h[q] = REV ? a[r][q] * u[r][q] : u[r][q];
+            }
+        };
+        if (first) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int q = 0; q < kVec; ++q) h[q] = first & 1u << r ? 0.0f : h[q];
+                move(r);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) move(r);
+        }
+        if (last && last_state) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (last & 1u << r) {
+                    float* to = last_state + walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch;
+#pragma unroll
+                    for (int q = 0; q < kVec; ++q)
+                        if (q < left) to[q] = REV ? a[r][q] * u[r][q] : u[r][q];
+                }
+            }
+        }
+        T *po = out + row_of(v0) * out_stride, *pg = out_g + row_of(v0) * c.dgate.token_stride;
+        const int64_t next = REV ? -out_stride : out_stride, next_g = REV ? -c.dgate.token_stride : c.dgate.token_stride;
+        auto put = [&](int r, bool wide) {
             float o[kVec], og[kVec];
 #pragma unroll
             for (int q = 0; q < kVec; ++q) {
-                if (REV) {
-                    const float g = begins ? u[r][q] : u[r][q] + h[q];
-                    h[q] = a[r][q] * g;
-                    o[q] = kGate ? b[r % RB][q] * g : g;
-                    og[q] = (kGate ? g : h[q]) * z[r % RZ][q];
-                    if (!inside) og[q] = 0.0f;
-                } else {
-                    h[q] = begins ? u[r][q] : fmaf(a[r][q], h[q], u[r][q]);
-                    o[q] = h[q];
-                }
-                if (!inside) o[q] = 0.0f;
+                o[q] = REV && kGate ? b[r % RB][q] * u[r][q] : u[r][q];
+                og[q] = REV ? (kGate ? u[r][q] : a[r][q] * u[r][q]) * z[r % RZ][q] : 0.0f;
             }
-            if (left > 0 && (!M || v < tokens)) {
-                store<T, WIDE>(outr.p + r * outr.row, o, left);
-                if (REV) store<T, WIDE>(dgr.p + r * dgr.row, og, left);
-            }
-            if (M && (last >> r & 1) && last_state) {
-                float* to = last_state + walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch;
+            store(po, o, left, wide);
+            if (REV) store(pg, og, left, wide);
+            po += next, pg += next_g;
+        };
+        if (whole && v0 + R <= tokens) {
 #pragma unroll
-                for (int q = 0; q < kVec; ++q)
-                    if (q < left) to[q] = h[q];
+            for (int r = 0; r < R; ++r) put(r, true);
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (v0 + r < tokens) put(r, false);
+        }
+        if (t0 < lo || t0 + kTile > hi) {  // rows outside every sequence
+            const float zero[kVec] = {};
+#pragma unroll 1
+            for (int64_t v = v0; v < min(v0 + R, tokens); ++v) {
+                if (v >= lo && v < hi) continue;
+                store(out + row_of(v) * out_stride, zero, left, whole);
+                if (REV) store(out_g + row_of(v) * c.dgate.token_stride, zero, left, whole);
             }
         }
-        outr.p += outr.tile, dgr.p += dgr.tile;
     };
 
+    float carry = 0.0f;  // of channel c0 + tid, for tid < kCh
     for (int i = 0; i < steps; ++i) {
         const int64_t t0 = i * t_step + t_first;
         const Marks<R>& mk = s.marks[i & 1];
-        const bool marked = mk.any;
-        if (marked) fold_run(Is<true>(), mk);
-        else fold_run(Is<false>(), mk);
-        if (i + 1 < steps) fetch(t0 + t_step);
+        copy_wait<kStages - 1>();
         __syncthreads();
-        if (warp == kMarker && i + 1 < steps) walk.mark(s.marks[(i + 1) & 1], t0 + t_step, lane, lo, hi);
+        if (s.lost) break;
+        fold_run(mk, s.tile[i % kStages]);
+        __syncthreads();
 
         // ---- the runs' maps meet
-        float2 map = {};
-        uint32_t near = 0;
-        int reset = 0;
+        auto map_of = [](const float4& f) { return Map{f.x, f.y, f.z, __float_as_uint(f.w)}; };
+        Map tile = {};
         if (tid < kCh) {
-            float p = 1.0f, m = 0.0f, off = 0.0f;
+            Factor fac;
+            float off = 0.0f;
+            uint32_t reset = 0;
 #pragma unroll
-            for (int y = 0; y < kTy; ++y) {
-                const float py = s.p[y][tid], my = s.m[y][tid];
-                off = apply(is_near(py) ? my : py, is_near(py), s.b[y][tid], s.reset[y], off);
-                p *= py;
-                m = fmaf(m, my, m + my);
-                reset |= s.reset[y];
+            for (int y0 = 0; y0 < kTy; y0 += kAhead) {
+                float4 f[kAhead];
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) f[y] = s.run[y0 + y][tid];
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) {
+                    const Map m = map_of(f[y]);
+                    fac = fac.then(m);
+                    off = m(off);
+                    reset |= m.reset;
+                }
             }
-            near = __ballot_sync(0xffffffffu, is_near(p));
-            map = make_float2(is_near(p) ? m : p, off);
-            for (int k = 0; k < parts && parts > 1; ++k) {
-                Shared<R>* o = cl.map_shared_rank(&s, k);
-                o->peer[i & 1][rank][tid] = map;
-                if (lane == 0) o->near[i & 1][rank][warp] = near;
-                if (tid == 0) o->peer_reset[i & 1][rank] = reset;
+            tile = fac.map(off, reset);
+            if (parts > 1) {
+                if (tid == 0) mbar_arrive_expect_tx(&s.come[i & 1], (uint32_t)(parts * kCh * sizeof(float4)));
+                const uint32_t to = smem_addr(s.peer + ((i & 1) * parts + rank) * kCh + tid), bar = smem_addr(&s.come[i & 1]);
+#pragma unroll 4
+                for (int k = 0; k < parts && (int64_t)i * parts + rank != c.skip_tile; ++k) send(in_block(to, k), in_block(bar, k), tile);
             }
         }
-        if (parts > 1) cl.sync();
+        fetch(i + kStages);
+        if (warp == kMarker && i + 1 < steps) walk.mark(s.marks[(i + 1) & 1], t0 + t_step, lane);
         if (tid < kCh) {
-            auto of_peer = [&](int k, float h) {
-                const float2 f = s.peer[i & 1][k][tid];
-                return apply(f.x, s.near[i & 1][k][warp] >> lane & 1, f.y, s.peer_reset[i & 1][k], h);
-            };
             float h = carry;
-            for (int k = 0; k < rank; ++k) h = of_peer(k, h);
-            carry = apply(map.x, near >> lane & 1, map.y, reset != 0, h);
-            for (int k = rank + 1; k < parts; ++k) carry = of_peer(k, carry);
+            if (parts > 1) {
+                const uint32_t parity = i >> 1 & 1;
+                if (!try_received(&s.come[i & 1], parity)) {
+                    const uint64_t deadline = globaltimer_ns() + c.wait_limit_ns;
+                    while (!try_received(&s.come[i & 1], parity)) {
+                        if (globaltimer_ns() > deadline) {
+                            s.lost = 1;
+                            g_gave_up = c.epoch;
+                            break;
+                        }
+                    }
+                }
+                const float4* peer = s.peer + (i & 1) * parts * kCh + tid;
+                float at = carry;
+                for (int k0 = 0; k0 < parts; k0 += kAhead) {
+                    float4 f[kAhead];
 #pragma unroll
-            for (int y = 0; y < kTy; ++y) {
-                const float py = s.p[y][tid];
-                s.in[y][tid] = h;
-                h = apply(is_near(py) ? s.m[y][tid] : py, is_near(py), s.b[y][tid], s.reset[y], h);
+                    for (int k = 0; k < kAhead; ++k) f[k] = peer[min(k0 + k, parts - 1) * kCh];
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) {
+                        if (k0 + k == rank) h = at;
+                        if (k0 + k < parts) at = map_of(f[k])(at);
+                    }
+                }
+                carry = at;
+            } else {
+                carry = tile(carry);
+            }
+#pragma unroll
+            for (int y0 = 0; y0 < kTy; y0 += kAhead) {
+                float4 f[kAhead];
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) f[y] = s.run[y0 + y][tid];
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) {
+                    s.in[y0 + y][tid] = h;
+                    h = map_of(f[y])(h);
+                }
             }
         }
         __syncthreads();
-        if (marked) finish_run(Is<true>(), mk, t0);
-        else finish_run(Is<false>(), mk, t0);
+        finish_run(mk, t0);
+    }
+    copy_wait<0>();
+    if (parts > 1) cl.sync();  // nothing is on its way to a block that has left
+}
+
+constexpr int kStepVec = 4;  // channels of a thread of the step
+
+// Neighbouring values of a row, zeros from the left-th on.
+template <class T, bool WIDE>
+__device__ __forceinline__ Values<T, kStepVec> load(const T* p, int left) {
+    if constexpr (WIDE) {
+        return *reinterpret_cast<const Values<T, kStepVec>*>(p);
+    } else {
+        T v[kStepVec];
+#pragma unroll
+        for (int i = 0; i < kStepVec; ++i) v[i] = i < left ? p[i] : T(0.0f);
+        Values<T, kStepVec> f;
+        memcpy(&f, v, sizeof f);
+        return f;
     }
 }
 
 // One token of each request, on its state of a pool.
 template <class T, int FORM, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_step(const RecurrenceCall c, float* state, const int32_t* slots, int64_t nslots) {
-    const int64_t per = (c.channels + kVec - 1) / kVec;
+    const int64_t per = (c.channels + kStepVec - 1) / kStepVec;
     const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (at >= per * c.tokens) return;
-    const int64_t t = div_fast(at, per), ch = (at - t * per) * kVec;
-    const int left = (int)min((int64_t)kVec, c.channels - ch);
-    const Four<T> g = load<T, WIDE>(static_cast<const T*>(c.gate.data) + t * c.gate.token_stride + ch, left);
-    const Four<T> x = load<T, WIDE>(static_cast<const T*>(c.x.data) + t * c.x.token_stride + ch, left);
+    const int64_t t = div_fast(at, per), ch = (at - t * per) * kStepVec;
+    const int left = (int)min((int64_t)kStepVec, c.channels - ch);
+    const Values<T, kStepVec> g = load<T, WIDE>(static_cast<const T*>(c.gate.data) + t * c.gate.token_stride + ch, left);
+    const Values<T, kStepVec> x = load<T, WIDE>(static_cast<const T*>(c.x.data) + t * c.x.token_stride + ch, left);
     const int64_t slot = slots ? slots[t] : t;
-    float h[kVec] = {};
+    float h[kStepVec] = {};
     if (slot >= 0 && slot < nslots) {
         float* p = state + slot * c.channels + ch;
         if (WIDE) {
@@ -534,51 +699,67 @@ __global__ void __launch_bounds__(kThreads) k_step(const RecurrenceCall c, float
             h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
         } else {
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) h[q] = q < left ? p[q] : 0.0f;
+            for (int q = 0; q < kStepVec; ++q) h[q] = q < left ? p[q] : 0.0f;
         }
 #pragma unroll
-        for (int q = 0; q < kVec; ++q) {
+        for (int q = 0; q < kStepVec; ++q) {
             float a, b;
-            weights<float, FORM>(get(g, q), a, b);  // (states are float32)
-            h[q] = fmaf(a, h[q], FORM == AK_RECURRENCE_GATE ? b * get(x, q) : get(x, q));
+            weights<float, FORM>(g[q], a, b);  // (states are float32)
+            h[q] = fmaf(a, h[q], FORM == AK_RECURRENCE_GATE ? b * x[q] : x[q]);
         }
-        store<float, WIDE>(p, h, left);
+        store(p, h, left, WIDE);
     }
-    store<T, WIDE>(static_cast<T*>(c.out.data) + t * c.out.token_stride + ch, h, left);
+    store(static_cast<T*>(c.out.data) + t * c.out.token_stride + ch, h, left, WIDE);
 }
 
-// Whether four neighbouring channels are one aligned load in every row.
+// Whether every row of an array begins at a multiple of `bytes`.
 template <class T>
-bool wide(const RecurrenceCall& c, const ak_rows& r) {
-    return r.data == nullptr || (aligned(r.data, 4 * sizeof(T)) && r.token_stride % 4 == 0);
+bool rows_at(const ak_rows& r, size_t bytes) {
+    return r.data == nullptr || (aligned(r.data, bytes) && r.token_stride * sizeof(T) % bytes == 0);
 }
 
-template <class T, int FORM, int R, bool REV, bool WIDE>
+template <class T, int FORM, int R, bool REV, bool WIDE, int PER_SM>
 ak_status launch(const RecurrenceCall& c, cudaStream_t stream) {
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
-    auto* kernel = k_recurrence<T, FORM, R, REV, WIDE>;
-    static std::atomic<uint64_t> ready{0};
-    if (!(ready.load() >> dev.device & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return cuda_fail(e);
-        ready.fetch_or(1ull << dev.device);
-    }
-    // blocks of a cluster: as many as run at once over all channels, two an SM,
-    // and no more than there are tiles
-    const int64_t groups = std::max<int64_t>(1, (c.channels + kCh - 1) / kCh);
-    const int64_t tiles = std::max<int64_t>(1, (c.tokens + kTy * R - 1) / (kTy * R));
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({(int64_t)kMaxParts, tiles, 2 * dev.sm_count / groups}));
+    auto* kernel = k_recurrence<T, FORM, R, REV, WIDE, PER_SM>;
+    using S = Shared<T, R, REV, REV && FORM == AK_RECURRENCE_GATE>;
+    auto smem_of = [](int64_t parts) { return sizeof(S) + 2 * (size_t)parts * kCh * sizeof(float4); };
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(groups * parts));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)parts;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    // clusters of each size that the device holds at once; asked for once
+    static std::atomic<uint64_t> ready{0};
+    static std::atomic<int> room[64][kMaxParts + 1];
+    if (!(ready.load() >> dev.device & 1)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxParts));
+        for (int p = 1; p <= kMaxParts && e == cudaSuccess; ++p) {
+            int n = 0;
+            cfg.gridDim = dim3((unsigned)p);
+            cfg.dynamicSmemBytes = smem_of(p);
+            attr[0].val.clusterDim.x = (unsigned)p;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            room[dev.device & 63][p] = n;
+        }
+        if (e != cudaSuccess) return cuda_fail(e);
+        ready.fetch_or(1ull << dev.device);
+    }
+    // blocks of a cluster: the most with which the clusters of all channels run
+    // at once, and no more than there are tiles
+    const int64_t groups = std::max<int64_t>(1, (c.channels + kCh - 1) / kCh);
+    const int64_t tiles = std::max<int64_t>(1, (c.tokens + kTy * R - 1) / (kTy * R));
+    int64_t parts = std::min<int64_t>(kMaxParts, tiles);
+    while (parts > 1 && room[dev.device & 63][parts] < groups) --parts;
+    cfg.gridDim = dim3((unsigned)(groups * parts));
+    cfg.dynamicSmemBytes = smem_of(parts);
+    attr[0].val.clusterDim.x = (unsigned)parts;
     if (log_on())
         log_call("gated_recurrence%s tokens=%lld seqs=%lld channels=%lld: %lld clusters of %lld blocks", REV ? "_backward" : "",
                  (long long)c.tokens, (long long)c.seqs, (long long)c.channels, (long long)groups, (long long)parts);
@@ -588,25 +769,27 @@ ak_status launch(const RecurrenceCall& c, cudaStream_t stream) {
     return check_launch();
 }
 
-// Tokens of a run: as many bytes in flight for either type.
+// Tokens of a run, and blocks of an SM.
 template <class T, bool REV>
-constexpr int run_of() { return REV || sizeof(T) == 4 ? 4 : 8; }
+constexpr int run_of() { return (sizeof(T) == 2 ? 16 : 8) / (REV ? 2 : 1); }
 
 template <class T, bool REV>
-ak_status by_form(const RecurrenceCall& c, cudaStream_t stream) {
+ak_status by_form(RecurrenceCall c, cudaStream_t stream) {
     constexpr int R = run_of<T, REV>();
-    const bool w = c.channels % 4 == 0 && wide<T>(c, c.x) && wide<T>(c, c.gate) && wide<T>(c, c.h) && wide<T>(c, c.dh) &&
-                   wide<T>(c, c.out) && wide<T>(c, c.dx) && wide<T>(c, c.dgate);
+    const bool w = rows_at<T>(c.x, 16) && rows_at<T>(c.gate, 16) && rows_at<T>(c.h, 16) && rows_at<T>(c.dh, 16);
+    constexpr size_t kOut = kVec * sizeof(T);
+    c.wide_out = rows_at<T>(c.out, kOut) && rows_at<T>(c.dx, kOut) && rows_at<T>(c.dgate, kOut);
     if (c.form == AK_RECURRENCE_DECAY)
-        return w ? launch<T, AK_RECURRENCE_DECAY, R, REV, true>(c, stream) : launch<T, AK_RECURRENCE_DECAY, R, REV, false>(c, stream);
-    return w ? launch<T, AK_RECURRENCE_GATE, R, REV, true>(c, stream) : launch<T, AK_RECURRENCE_GATE, R, REV, false>(c, stream);
+        return w ? launch<T, AK_RECURRENCE_DECAY, R, REV, true, 2>(c, stream) : launch<T, AK_RECURRENCE_DECAY, R, REV, false, 2>(c, stream);
+    return w ? launch<T, AK_RECURRENCE_GATE, R, REV, true, 2>(c, stream) : launch<T, AK_RECURRENCE_GATE, R, REV, false, 2>(c, stream);
 }
 
 template <class T, int FORM>
 ak_status step(const RecurrenceCall& c, float* state, const int32_t* slots, int64_t nslots, cudaStream_t stream) {
-    const int64_t per = (c.channels + kVec - 1) / kVec;
+    const int64_t per = (c.channels + kStepVec - 1) / kStepVec;
     const unsigned grid = (unsigned)((per * c.tokens + kThreads - 1) / kThreads);
-    const bool w = c.channels % 4 == 0 && aligned(state, 16) && wide<T>(c, c.x) && wide<T>(c, c.gate) && wide<T>(c, c.out);
+    constexpr size_t kFour = 4 * sizeof(T);
+    const bool w = c.channels % 4 == 0 && aligned(state, 16) && rows_at<T>(c.x, kFour) && rows_at<T>(c.gate, kFour) && rows_at<T>(c.out, kFour);
     if (w) k_step<T, FORM, true><<<grid, kThreads, 0, stream>>>(c, state, slots, nslots);
     else k_step<T, FORM, false><<<grid, kThreads, 0, stream>>>(c, state, slots, nslots);
     count_launches(1);
@@ -614,6 +797,14 @@ ak_status step(const RecurrenceCall& c, float* state, const int32_t* slots, int6
 }
 
 }  // namespace gr
+
+ak_status recurrence_lost(uint64_t epoch, bool* lost) {
+    uint64_t word = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(&word, gr::g_gave_up, sizeof word);
+    if (e != cudaSuccess) return cuda_fail(e);
+    *lost = word == epoch;
+    return AK_OK;
+}
 
 ak_status run_recurrence(const RecurrenceCall& c, cudaStream_t stream) {
     return c.dtype == AK_F32 ? gr::by_form<float, false>(c, stream) : gr::by_form<bf16, false>(c, stream);
