@@ -370,7 +370,6 @@ struct RecurrenceCall {
     uint64_t epoch;           // left behind by a kernel that gave up waiting
     int64_t wait_limit_ns;
     int64_t skip_tile;        // the tile whose map is not sent (tests), or -1
-    bool wide_out;            // four values of every output row are one store; filled in by the launcher
 };
 // Whether the call of that epoch gave up waiting (the device has come to its end).
 ak_status recurrence_lost(uint64_t epoch, bool* lost);

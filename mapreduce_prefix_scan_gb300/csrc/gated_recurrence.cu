@@ -12,11 +12,11 @@
 // Both are affine scans along the packed token axis, the second in reversed
 // time (virtual token v = tokens - 1 - t), with a reset where a sequence begins.
 //
-// A cluster of up to 16 blocks takes 64 channels and walks the whole packed
+// A cluster of up to 16 blocks takes 32 channels and walks the whole packed
 // axis, a tile of 8 runs of R tokens for each block and step, whatever the
 // sequences' lengths: balance does not depend on them, each input is read once
-// and each output written once. In a tile a thread folds R consecutive tokens of 2
-// channels, which it keeps in registers, to a map h -> A h + B; a thread for each
+// and each output written once. In a tile a thread folds R consecutive tokens of a
+// channel, which it keeps in registers, to a map h -> A h + B; a thread for each
 // channel folds the tile's 8 maps, sends the block's map to every block of the
 // cluster, and when theirs have come folds the maps before its own onto the
 // state carried from the last step. So a token is a few dozen roundings away from
@@ -31,7 +31,8 @@
 // as A - 1: a factor near one that is rounded itself is off by up to 3e-8, the
 // same way each time where gates are equal, for every token (or run) of a memory
 // of thousands. A - 1 comes from the sum of the gates (decay), or from the b_t
-// (gate), and its error is relative to itself.
+// (gate), and its error is relative to itself. In float32 calls the tokens of a
+// run whose factors are all above 1/2 are applied so as well.
 #include <algorithm>
 #include <atomic>
 #include <cooperative_groups.h>
@@ -46,23 +47,12 @@ namespace ak {
 namespace gr {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 2;                       // channels of a thread
-constexpr int kLx = kWarp;                    // threads along the channels
-constexpr int kCh = kVec * kLx;               // channels of a block
-constexpr int kTy = kThreads / kLx;           // runs of tokens of a tile
+constexpr int kPerSm = 2;                     // blocks of an SM
+constexpr int kCh = kWarp;                    // channels of a cluster, one a thread of a warp
+constexpr int kTy = kThreads / kCh;           // runs of tokens of a tile
 constexpr int kMaxParts = 16;                 // blocks of a cluster
 constexpr int kAhead = 4;                     // maps read before the first of them is applied
 constexpr int kStages = 2;                    // tiles on their way
-
-// Neighbouring values as they lie in memory.
-template <class T, int N>
-struct alignas(N * sizeof(T)) Values {
-    uint32_t w[N * sizeof(T) / 4];
-    __device__ __forceinline__ float operator[](int i) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        else return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    }
-};
 
 // 16 bytes (or the first `size` of them, zeros past them) into shared memory.
 __device__ __forceinline__ void copy16(void* to, const void* from, int size) {
@@ -71,12 +61,28 @@ __device__ __forceinline__ void copy16(void* to, const void* from, int size) {
                  "l"(from), "r"(size)
                  : "memory");
 }
+__device__ __forceinline__ void copy4(void* to, const void* from, int size) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from), "r"(size)
+                 : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(bf16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void set(float* p, float v) { *p = v; }
 __device__ __forceinline__ void set(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Neighbouring values as they lie in memory.
+template <class T, int N>
+struct alignas(N * sizeof(T)) Values {
+    T v[N];
+    __device__ __forceinline__ float operator[](int i) const {
+        return as_float(v[i]);
+    }
+};
 
 // Values [0, left) of v; in one store where `whole`.
 template <class T, int N>
@@ -84,14 +90,7 @@ __device__ __forceinline__ void store(T* p, const float (&v)[N], int left, bool 
     if (whole) {
         Values<T, N> o;
 #pragma unroll
-        for (int i = 0; i < (int)(N * sizeof(T) / 4); ++i) {
-            if constexpr (sizeof(T) == 4) {
-                o.w[i] = __float_as_uint(v[i]);
-            } else {
-                const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                memcpy(&o.w[i], &two, 4);
-            }
-        }
+        for (int i = 0; i < N; ++i) set(&o.v[i], v[i]);
         *reinterpret_cast<Values<T, N>*>(p) = o;
     } else {
 #pragma unroll
@@ -119,15 +118,13 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// a and b of a gate, both to their own relative precision: 2^-22 where the
-// results are bf16, a rounding or two where they are float32 (twice the
-// instructions, for twice the bytes). In the first, e stops at 2^126, where a
-// has long been nothing beside b.
+// a and b of a gate, both to their own relative precision, 2^-21. Where results are
+// bf16 e stops at 2^126: a has long been nothing beside b there.
 template <class T, int FORM>
 __device__ __forceinline__ void weights(float g, float& a, float& b) {
     constexpr bool kFast = sizeof(T) == 2;
     if (FORM == AK_RECURRENCE_DECAY) {
-        a = kFast ? exp2_fast(g * kLog2e) : expf(g);
+        a = exp2_fast(g * kLog2e);
         b = 1.0f;
     } else {
         if (kFast) {
@@ -135,11 +132,26 @@ __device__ __forceinline__ void weights(float g, float& a, float& b) {
             a = rcp_fast(1.0f + e);
             b = e * a;
         } else {
-            const float e = expf(-fabsf(g)), r = __frcp_rn(1.0f + e);
+            const float e = exp2_fast(fabsf(g) * -kLog2e), r = rcp_fast(1.0f + e);
             a = g >= 0.0f ? r : e * r;
             b = g >= 0.0f ? e * r : r;
         }
     }
+}
+
+// e^l - 1, by its series where that is used as such (l within log 2 of 0: the
+// terms left out are below 2^-23 of it); e^l is e.
+__device__ __forceinline__ float less_one(float l, float e) {
+    float m = 1.0f / 362880;
+    m = fmaf(m, l, 1.0f / 40320);
+    m = fmaf(m, l, 1.0f / 5040);
+    m = fmaf(m, l, 1.0f / 720);
+    m = fmaf(m, l, 1.0f / 120);
+    m = fmaf(m, l, 1.0f / 24);
+    m = fmaf(m, l, 1.0f / 6);
+    m = fmaf(m, l, 0.5f);
+    m = fmaf(m * l, l, l);
+    return fabsf(l) < 0.6932f ? m : e - 1.0f;
 }
 
 // A product of a's, and it less one.
@@ -156,8 +168,9 @@ struct Product {
     }
     __device__ __forceinline__ void done() {
         if (FORM == AK_RECURRENCE_DECAY) {
-            m = expm1f(p);
-            p = expf(p);
+            const float l = p;
+            p = exp2_fast(l * kLog2e);
+            m = less_one(l, p);
         }
     }
 };
@@ -272,40 +285,43 @@ struct Walk {
 
 // Inputs of a tile: the gate, what is scanned (x, or dh), and for gradients
 // h_{t-1} of each token (decay), or x and the state before each run (gate).
-template <class T, int R, bool REV, bool AGAIN>
+// Rows that do not begin at multiples of 16 bytes are copied by 4-byte words; of
+// bf16 ones that may be from the value before a row on, one word more.
+template <class T, int R, bool REV, bool AGAIN, bool WIDE>
 struct Tile {
-    T g[kTy * R][kCh], u[kTy * R][kCh], z[REV ? kTy * R : 1][REV ? kCh : 8], before[AGAIN ? kTy : 1][AGAIN ? kCh : 8];
+    static constexpr int kPitch = WIDE || sizeof(T) == 4 ? kCh : kCh + 2;
+    T g[kTy * R * kPitch], u[kTy * R * kPitch], z[REV ? kTy * R * kPitch : 8], before[AGAIN ? kTy * kPitch : 8];
 };
 
-template <class T, int R, bool REV, bool AGAIN>
+template <class T, int R, bool REV, bool AGAIN, bool WIDE>
 struct alignas(16) Shared {
-    Tile<T, R, REV, AGAIN> tile[kStages];
-    float4 run[kTy][kCh];  // the runs' maps; channel 2 i + q at 32 q + i, so that neighbouring threads' lie side by side
-    float in[kTy][kCh];    // the state before each run, in that order
+    Tile<T, R, REV, AGAIN, WIDE> tile[kStages];
+    float4 run[kTy][kCh];  // the runs' maps
+    float in[kTy][kCh];    // the state before each run
     Marks<R> marks[2];
     uint64_t come[2];  // maps of the even and of the odd steps
     int lost;
     float4 peer[1];  // [2][parts][kCh]: the blocks' maps
 };
 
-template <class T, int FORM, int R, bool REV, bool WIDE, int PER_SM>
-__global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const RecurrenceCall c) {
+template <class T, int FORM, int R, bool REV, bool WIDE>
+__global__ void __launch_bounds__(kThreads, kPerSm) k_recurrence(const RecurrenceCall c) {
     constexpr int kTile = kTy * R;
     constexpr bool kGate = FORM == AK_RECURRENCE_GATE;
     constexpr bool kRows = REV && !kGate;   // h_{t-1} is read for every token
     constexpr bool kAgain = REV && kGate;   // h_{t-1} is computed again from the one before the run
     constexpr int RZ = REV ? R : 1, RB = kAgain ? R : 1;
     extern __shared__ __align__(16) unsigned char smem[];
-    using S = Shared<T, R, REV, kAgain>;
+    using S = Shared<T, R, REV, kAgain, WIDE>;
+    using In = Tile<T, R, REV, kAgain, WIDE>;
+    constexpr int kPitch = In::kPitch;
     S& s = *reinterpret_cast<S*>(smem);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), parts = (int)cl.num_blocks();
-    const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
-    const int lx = tid % kLx, ty = tid / kLx;
+    const int tid = threadIdx.x, lane = tid % kWarp, ty = tid / kWarp;
     const int64_t c0 = (int64_t)(blockIdx.x / parts) * kCh;
-    const int64_t ch = c0 + lx * kVec;
-    const int left = (int)max((int64_t)0, min((int64_t)kVec, c.channels - ch));
-    const bool whole = c.wide_out && left == kVec;
+    const int64_t ch = c0 + lane;
+    const bool some = ch < c.channels;
     const int64_t tokens = c.tokens;
     Walk<R, REV> walk;
     walk.b.offsets = c.offsets;
@@ -322,37 +338,38 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const Recurrenc
     // memory), those below `end` of them; the others are zeros
     auto copy = [&](T* to, const ak_rows& from, int rows, int apart, int64_t v0, int shift, int64_t end) {
         const T* base = static_cast<const T*>(from.data) + c0;
+        const int64_t way = (REV ? -1 : 1) * from.token_stride;
         if constexpr (WIDE) {
             constexpr int kPer = 16 / (int)sizeof(T), kRow = kCh / kPer;
             const int col = tid % kRow * kPer;
             const int bytes = (int)max((int64_t)0, min((int64_t)kPer, c.channels - c0 - col)) * (int)sizeof(T);
             int64_t v = v0 + (int64_t)(tid / kRow) * apart;
             const T* p = base + (row_of(v) + shift) * from.token_stride + col;
-            const int64_t step = (int64_t)(REV ? -1 : 1) * (kThreads / kRow) * apart * from.token_stride;
 #pragma unroll
             for (int r = 0; r < rows; r += kThreads / kRow) {
                 const bool in = v < end && bytes > 0;
-                if (r + tid / kRow < rows) copy16(to + (r + tid / kRow) * kCh + col, in ? p : base, in ? bytes : 0);
+                if (r + tid / kRow < rows) copy16(to + (r + tid / kRow) * kPitch + col, in ? p : base, in ? bytes : 0);
                 v += (kThreads / kRow) * apart;
-                p += step;
+                p += way * ((kThreads / kRow) * apart);
             }
         } else {
-            const int col = tid % kCh;
-            const bool some = c0 + col < c.channels;
-            constexpr int kOnce = 8;
-            for (int r0 = tid / kCh; r0 < rows; r0 += kOnce * (kThreads / kCh)) {
-                T v[kOnce];
-#pragma unroll
-                for (int i = 0; i < kOnce; ++i) {
-                    const int r = r0 + i * (kThreads / kCh);
-                    const int64_t at = v0 + (int64_t)r * apart;
-                    v[i] = some && r < rows && at < end ? base[(row_of(at) + shift) * from.token_stride + col] : T(0.0f);
+            // a row a warp, a 4-byte word a lane; a bf16 row that begins inside a word
+            // is taken from the word's other value on (which is of the same
+            // allocation: those begin at words), and ends with half a word
+            const int64_t n = min((int64_t)kCh, c.channels - c0);
+            const char* none = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(from.data) & ~(uintptr_t)3);
+            int64_t v = v0 + (int64_t)ty * apart;
+            const T* p = base + (row_of(v) + shift) * from.token_stride;
+            for (int r = ty; r < rows; r += kTy) {
+                const char* row = reinterpret_cast<const char*>(p);
+                const int64_t odd = reinterpret_cast<uintptr_t>(row) & 3;
+                const int64_t bytes = v < end ? n * (int64_t)sizeof(T) + odd : 0;
+                for (int w = lane; w < kPitch * (int)sizeof(T) / 4; w += kWarp) {
+                    const int size = (int)max((int64_t)0, min((int64_t)4, bytes - 4 * w));
+                    copy4(reinterpret_cast<char*>(to + r * kPitch) + 4 * w, size ? row - odd + 4 * w : none, size);
                 }
-#pragma unroll
-                for (int i = 0; i < kOnce; ++i) {
-                    const int r = r0 + i * (kThreads / kCh);
-                    if (r < rows) to[r * kCh + col] = v[i];
-                }
+                v += kTy * apart;
+                p += way * (kTy * apart);
             }
         }
     };
@@ -360,34 +377,43 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const Recurrenc
         auto& t = s.tile[i % kStages];
         const int64_t v0 = t_first + i * t_step;
         if (i < steps) {
-            copy(&t.g[0][0], c.gate, kTile, 1, v0, 0, tokens);
-            copy(&t.u[0][0], REV ? c.dh : c.x, kTile, 1, v0, 0, tokens);
+            copy(t.g, c.gate, kTile, 1, v0, 0, tokens);
+            copy(t.u, REV ? c.dh : c.x, kTile, 1, v0, 0, tokens);
             if constexpr (kAgain) {
-                copy(&t.z[0][0], c.x, kTile, 1, v0, 0, tokens);
+                copy(t.z, c.x, kTile, 1, v0, 0, tokens);
                 // the row before the run's first token in time
-                copy(&t.before[0][0], c.h, kTy, R, v0 + R - 1, -1, tokens - 1);
+                copy(t.before, c.h, kTy, R, v0 + R - 1, -1, tokens - 1);
             }
-            if constexpr (kRows) copy(&t.z[0][0], c.h, kTile, 1, v0, -1, tokens - 1);
+            if constexpr (kRows) copy(t.z, c.h, kTile, 1, v0, -1, tokens - 1);
         }
         copy_commit();
     };
-    constexpr int kMarker = kThreads / kWarp - 1;
+    // value of this thread's channel in row r of a copied array whose row 0 is virtual token v0
+    auto value = [&](const T* rows, const ak_rows& from, int r, int apart, int64_t v0, int shift) {
+        int at = lane;
+        if constexpr (!WIDE && sizeof(T) == 2) {
+            const uint32_t first = (uint32_t)(reinterpret_cast<uintptr_t>(from.data) >> 1) + (uint32_t)c0;
+            const uint32_t row = (uint32_t)row_of(v0) + (uint32_t)shift + (uint32_t)((REV ? -1 : 1) * r * apart);
+            at += (first + row * (uint32_t)from.token_stride) & 1;
+        }
+        return as_float(rows[r * kPitch + at]);
+    };
+    constexpr int kMarker = kTy - 1;
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(i);
-    if (warp == kMarker) {
+    if (ty == kMarker) {
         walk.base = 0;
         walk.window(lane);
         walk.mark(s.marks[0], t_first, lane);
     }
     // sequences without tokens pass their state on
     if (last_state) {
-        for (int j0 = (rank * (kThreads / kWarp) + warp) * kWarp; j0 < walk.b.n; j0 += parts * kThreads) {
+        for (int j0 = (rank * kTy + ty) * kWarp; j0 < walk.b.n; j0 += parts * kThreads) {
             const int j = j0 + lane;
             unsigned empty = __ballot_sync(0xffffffffu, j < walk.b.n && walk.b.at(j) >= walk.b.at(j + 1));
             for (; empty; empty &= empty - 1) {
-                const int64_t row = walk.b.seq(j0 + __ffs(empty) - 1) * c.channels;
-                for (int64_t i = c0 + lane; i < min(c0 + kCh, c.channels); i += kWarp)
-                    last_state[row + i] = first_state ? first_state[row + i] : 0.0f;
+                const int64_t at = walk.b.seq(j0 + __ffs(empty) - 1) * c.channels + ch;
+                if (some) last_state[at] = first_state ? first_state[at] : 0.0f;
             }
         }
     }
@@ -401,93 +427,86 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const Recurrenc
     }
     if (parts > 1) cl.sync();  // every block of the cluster runs, with its barriers, before one sends to another
 
-    float a[R][kVec], b[RB][kVec], u[R][kVec], z[RZ][kVec];
-    // this thread's channels of a sequence's state
-    auto state_of = [&](const float* states, int64_t seq, float (&v)[kVec]) {
-#pragma unroll
-        for (int q = 0; q < kVec; ++q) v[q] = states && q < left ? states[seq * c.channels + ch + q] : 0.0f;
-    };
+    // a token's factor is a + one: in runs of float32 calls whose factors are all
+    // near one, a is held less one
+    constexpr bool kNear = sizeof(T) == 4;
+    float a[R] = {}, b[RB] = {}, u[R] = {}, z[RZ] = {}, one = 0.0f;
+    auto times = [&](int r, float h) { return kNear ? fmaf(a[r], h, one * h) : a[r] * h; };
+    auto step = [&](int r, float h) { return kNear ? fmaf(one, h, fmaf(a[r], h, u[r])) : fmaf(a[r], h, u[r]); };
+    auto state_of = [&](const float* states, int64_t seq) { return states && some ? states[seq * c.channels + ch] : 0.0f; };
     // ---- the run's map. A token that begins a sequence takes its state, and its
     // factor is 0: it forgets what was before, which is dropped as well, as it may
     // not be finite. Such tokens are rare; only the chains, a few dozen
     // instructions each, exist with and without them. (Larger paths of their own
     // wait for their instructions, 200 cycles a token; a branch for every token
     // keeps them from overlapping.)
-    auto fold_run = [&](const Marks<R>& mk, const Tile<T, R, REV, kAgain>& t) {
+    auto fold_run = [&](const Marks<R>& mk, const In& t, int64_t t0) {
         const uint32_t first = mk.first[ty];
         [[maybe_unused]] const uint32_t last = mk.last[ty];
-        auto values = [&](const T* row) { return *reinterpret_cast<const Values<T, kVec>*>(row + lx * kVec); };
-        Product<FORM> prod[kVec];
+        const int64_t v0 = t0 + ty * R;
+        const int at = ty * R * kPitch;
+        Product<FORM> prod;
+        [[maybe_unused]] float m[kNear ? R : 1], least = 1.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const Values<T, kVec> rg = values(t.g[ty * R + r]), ru = values(t.u[ty * R + r]);
-            [[maybe_unused]] Values<T, kVec> rz;
-            if constexpr (REV) rz = values(t.z[ty * R + r]);
-#pragma unroll
-            for (int q = 0; q < kVec; ++q) {
-                float w;
-                weights<T, FORM>(rg[q], a[r][q], w);
-                prod[q].take(rg[q], a[r][q], w);
-                u[r][q] = kGate && !REV ? w * ru[q] : ru[q];
-                if constexpr (kAgain) b[r][q] = w;
-                if constexpr (REV) z[r][q] = rz[q];
+            const float g = value(t.g + at, c.gate, r, 1, v0, 0), in = value(t.u + at, REV ? c.dh : c.x, r, 1, v0, 0);
+            float w;
+            weights<T, FORM>(g, a[r], w);
+            prod.take(g, a[r], w);
+            u[r] = kGate && !REV ? w * in : in;
+            if constexpr (kAgain) {
+                b[r] = w;
+                z[r] = value(t.z + at, c.x, r, 1, v0, 0);
+            }
+            if constexpr (kRows) z[r] = value(t.z + at, c.h, r, 1, v0, -1);
+            if constexpr (kNear) {
+                m[r] = kGate ? -w : less_one(g, a[r]);
+                least = fminf(least, a[r]);
             }
         }
+        if constexpr (kNear) {
+            const bool near = least > 0.5f;
+            one = near ? 1.0f : 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) a[r] = near ? m[r] : a[r];
+        }
         if constexpr (REV) {  // h_{t-1} of each token, forward in time
-            float hh[kVec] = {};
-            if constexpr (kAgain) {
-                const Values<T, kVec> rb = values(t.before[ty]);
-#pragma unroll
-                for (int q = 0; q < kVec; ++q) hh[q] = rb[q];
-            }
+            float hh = 0.0f;
+            if constexpr (kAgain) hh = value(t.before, c.h, ty, R, t0 + R - 1, -1);
             auto again = [&](int r) {
-#pragma unroll
-                for (int q = 0; q < kVec; ++q) {
-                    const float bx = b[r % RB][q] * z[r][q];
-                    z[r][q] = (hh[q] - z[r][q]) * (a[r][q] * b[r % RB][q]);
-                    hh[q] = fmaf(a[r][q], hh[q], bx);
+                if constexpr (kAgain) {
+                    const float bx = b[r] * z[r], h = hh;
+                    hh = kNear ? fmaf(one, h, fmaf(a[r], h, bx)) : fmaf(a[r], h, bx);
+                    z[r] = (h - z[r]) * ((a[r] + one) * b[r]);
                 }
             };
             if (last) {
 #pragma unroll
                 for (int r = R - 1; r >= 0; --r) {
                     if (last & 1u << r) {  // the sequence's first token
-                        float s0[kVec];
-                        state_of(c.state_in, walk.b.seq(mk.seq_last[ty * R + r]), s0);
-#pragma unroll
-                        for (int q = 0; q < kVec; ++q) {
-                            hh[q] = s0[q];
-                            if (kRows) z[r][q] = s0[q];
-                        }
+                        hh = state_of(c.state_in, walk.b.seq(mk.seq_last[ty * R + r]));
+                        if (kRows) z[r] = hh;
                     }
-                    if constexpr (kAgain) again(r);
+                    again(r);
                 }
             } else if constexpr (kAgain) {
 #pragma unroll
                 for (int r = R - 1; r >= 0; --r) again(r);
             }
         }
-        float fold[kVec] = {};
-        auto add = [&](int r) {
-#pragma unroll
-            for (int q = 0; q < kVec; ++q)
-                fold[q] = REV ? a[r][q] * (u[r][q] + fold[q]) : fmaf(a[r][q], fold[q], u[r][q]);
-        };
+        float fold = 0.0f;
+        auto add = [&](int r) { fold = REV ? times(r, u[r] + fold) : step(r, fold); };
         if (first) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (first & 1u << r) {
-                    float s0[kVec];
-                    state_of(first_state, walk.b.seq(mk.seq_first[ty * R + r]), s0);
-#pragma unroll
-                    for (int q = 0; q < kVec; ++q) {
-                        fold[q] = 0.0f;
-                        if (REV) {
-                            u[r][q] += s0[q];
-                        } else {
-                            if (first_state) u[r][q] = fmaf(a[r][q], s0[q], u[r][q]);
-                            a[r][q] = 0.0f;
-                        }
+                    const float s0 = state_of(first_state, walk.b.seq(mk.seq_first[ty * R + r]));
+                    fold = 0.0f;
+                    if (REV) {
+                        u[r] += s0;
+                    } else {
+                        if (first_state) u[r] = step(r, s0);
+                        a[r] = 0.0f;
                     }
                 }
                 add(r);
@@ -496,12 +515,9 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const Recurrenc
 #pragma unroll
             for (int r = 0; r < R; ++r) add(r);
         }
-#pragma unroll
-        for (int q = 0; q < kVec; ++q) {
-            prod[q].done();
-            const Map m = Factor{prod[q].p, prod[q].m}.map(fold[q], first != 0);
-            s.run[ty][q * kLx + lx] = make_float4(m.f, m.one, m.off, __uint_as_float(m.reset));
-        }
+        prod.done();
+        const Map all = Factor{prod.p, prod.m}.map(fold, first != 0);
+        s.run[ty][lane] = make_float4(all.f, all.one, all.off, __uint_as_float(all.reset));
     };
     // ---- the run again, from its state: u becomes h_t, or G_t
     T* const out = static_cast<T*>(REV ? c.dx.data : c.out.data) + ch;
@@ -510,21 +526,15 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const Recurrenc
     auto finish_run = [&](const Marks<R>& mk, int64_t t0) {
         const uint32_t first = mk.first[ty], last = mk.last[ty];
         const int64_t v0 = t0 + ty * R;
-        float h[kVec];
-#pragma unroll
-        for (int q = 0; q < kVec; ++q) h[q] = s.in[ty][q * kLx + lx];
+        float h = s.in[ty][lane];
         auto move = [&](int r) {
-#pragma unroll
-            for (int q = 0; q < kVec; ++q) {
-                u[r][q] = REV ? u[r][q] + h[q] : fmaf(a[r][q], h[q], u[r][q]);
-                h[q] = REV ? a[r][q] * u[r][q] : u[r][q];
-            }
+            u[r] = REV ? u[r] + h : step(r, h);
+            h = REV ? times(r, u[r]) : u[r];
         };
         if (first) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-#pragma unroll
-                for (int q = 0; q < kVec; ++q) h[q] = first & 1u << r ? 0.0f : h[q];
+                h = first & 1u << r ? 0.0f : h;
                 move(r);
             }
         } else {
@@ -534,60 +544,52 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const Recurrenc
         if (last && last_state) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (last & 1u << r) {
-                    float* to = last_state + walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch;
-#pragma unroll
-                    for (int q = 0; q < kVec; ++q)
-                        if (q < left) to[q] = REV ? a[r][q] * u[r][q] : u[r][q];
-                }
+                if ((last & 1u << r) && some)
+                    last_state[walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch] = REV ? times(r, u[r]) : u[r];
             }
         }
         T *po = out + row_of(v0) * out_stride, *pg = out_g + row_of(v0) * c.dgate.token_stride;
         const int64_t next = REV ? -out_stride : out_stride, next_g = REV ? -c.dgate.token_stride : c.dgate.token_stride;
-        auto put = [&](int r, bool wide) {
-            float o[kVec], og[kVec];
-#pragma unroll
-            for (int q = 0; q < kVec; ++q) {
-                o[q] = REV && kGate ? b[r % RB][q] * u[r][q] : u[r][q];
-                og[q] = REV ? (kGate ? u[r][q] : a[r][q] * u[r][q]) * z[r % RZ][q] : 0.0f;
-            }
-            store(po, o, left, wide);
-            if (REV) store(pg, og, left, wide);
+        auto put = [&](int r) {
+            if constexpr (kAgain) set(po, b[r] * u[r]);
+            else set(po, u[r]);
+            if constexpr (REV) set(pg, (kGate ? u[r] : times(r, u[r])) * z[r]);
             po += next, pg += next_g;
         };
-        if (whole && v0 + R <= tokens) {
+        if (v0 + R <= tokens) {
+            if (some) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) put(r, true);
-        } else {
+                for (int r = 0; r < R; ++r) put(r);
+            }
+        } else if (some) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (v0 + r < tokens) put(r, false);
+                if (v0 + r < tokens) put(r);
         }
         if (t0 < lo || t0 + kTile > hi) {  // rows outside every sequence
-            const float zero[kVec] = {};
 #pragma unroll 1
             for (int64_t v = v0; v < min(v0 + R, tokens); ++v) {
-                if (v >= lo && v < hi) continue;
-                store(out + row_of(v) * out_stride, zero, left, whole);
-                if (REV) store(out_g + row_of(v) * c.dgate.token_stride, zero, left, whole);
+                if ((v >= lo && v < hi) || !some) continue;
+                set(out + row_of(v) * out_stride, 0.0f);
+                if (REV) set(out_g + row_of(v) * c.dgate.token_stride, 0.0f);
             }
         }
     };
 
-    float carry = 0.0f;  // of channel c0 + tid, for tid < kCh
+    float carry = 0.0f;  // of this thread's channel (warp 0)
     for (int i = 0; i < steps; ++i) {
         const int64_t t0 = i * t_step + t_first;
         const Marks<R>& mk = s.marks[i & 1];
         copy_wait<kStages - 1>();
         __syncthreads();
         if (s.lost) break;
-        fold_run(mk, s.tile[i % kStages]);
+        fold_run(mk, s.tile[i % kStages], t0);
         __syncthreads();
 
         // ---- the runs' maps meet
         auto map_of = [](const float4& f) { return Map{f.x, f.y, f.z, __float_as_uint(f.w)}; };
         Map tile = {};
-        if (tid < kCh) {
+        if (ty == 0) {
             Factor fac;
             float off = 0.0f;
             uint32_t reset = 0;
@@ -613,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_recurrence(const Recurrenc
             }
         }
         fetch(i + kStages);
-        if (warp == kMarker && i + 1 < steps) walk.mark(s.marks[(i + 1) & 1], t0 + t_step, lane);
-        if (tid < kCh) {
+        if (ty == kMarker && i + 1 < steps) walk.mark(s.marks[(i + 1) & 1], t0 + t_step, lane);
+        if (ty == 0) {
             float h = carry;
             if (parts > 1) {
                 const uint32_t parity = i >> 1 & 1;
@@ -705,7 +707,9 @@ __global__ void __launch_bounds__(kThreads) k_step(const RecurrenceCall c, float
         for (int q = 0; q < kStepVec; ++q) {
             float a, b;
             weights<float, FORM>(g[q], a, b);  // (states are float32)
-            h[q] = fmaf(a, h[q], FORM == AK_RECURRENCE_GATE ? b * x[q] : x[q]);
+            const bool near = a > 0.5f;
+            const float less = FORM == AK_RECURRENCE_GATE ? -b : less_one(g[q], a), in = FORM == AK_RECURRENCE_GATE ? b * x[q] : x[q];
+            h[q] = fmaf(near ? less : a, h[q], in) + (near ? h[q] : 0.0f);
         }
         store(p, h, left, WIDE);
     }
@@ -718,12 +722,12 @@ bool rows_at(const ak_rows& r, size_t bytes) {
     return r.data == nullptr || (aligned(r.data, bytes) && r.token_stride * sizeof(T) % bytes == 0);
 }
 
-template <class T, int FORM, int R, bool REV, bool WIDE, int PER_SM>
+template <class T, int FORM, int R, bool REV, bool WIDE>
 ak_status launch(const RecurrenceCall& c, cudaStream_t stream) {
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
-    auto* kernel = k_recurrence<T, FORM, R, REV, WIDE, PER_SM>;
-    using S = Shared<T, R, REV, REV && FORM == AK_RECURRENCE_GATE>;
+    auto* kernel = k_recurrence<T, FORM, R, REV, WIDE>;
+    using S = Shared<T, R, REV, REV && FORM == AK_RECURRENCE_GATE, WIDE>;
     auto smem_of = [](int64_t parts) { return sizeof(S) + 2 * (size_t)parts * kCh * sizeof(float4); };
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -769,19 +773,24 @@ ak_status launch(const RecurrenceCall& c, cudaStream_t stream) {
     return check_launch();
 }
 
-// Tokens of a run, and blocks of an SM.
-template <class T, bool REV>
-constexpr int run_of() { return (sizeof(T) == 2 ? 16 : 8) / (REV ? 2 : 1); }
+template <class T, int FORM, bool REV>
+ak_status by_length(const RecurrenceCall& c, cudaStream_t stream) {
+    DeviceInfo dev;
+    if (!current_device(&dev)) return AK_ERR_CUDA;
+    const bool w = rows_at<T>(c.x, 16) && rows_at<T>(c.gate, 16) && rows_at<T>(c.h, 16) && rows_at<T>(c.dh, 16);
+    // tokens of a run: what the registers hold; fewer where the tiles would leave
+    // SMs without a block
+    constexpr int R = (sizeof(T) == 2 ? 32 : 16) / (REV ? 2 : 1), kShort = 8;
+    const int64_t groups = (c.channels + kCh - 1) / kCh;
+    if (R > kShort && groups * ((c.tokens + kTy * R - 1) / (kTy * R)) < dev.sm_count)
+        return w ? launch<T, FORM, kShort, REV, true>(c, stream) : launch<T, FORM, kShort, REV, false>(c, stream);
+    return w ? launch<T, FORM, R, REV, true>(c, stream) : launch<T, FORM, R, REV, false>(c, stream);
+}
 
 template <class T, bool REV>
-ak_status by_form(RecurrenceCall c, cudaStream_t stream) {
-    constexpr int R = run_of<T, REV>();
-    const bool w = rows_at<T>(c.x, 16) && rows_at<T>(c.gate, 16) && rows_at<T>(c.h, 16) && rows_at<T>(c.dh, 16);
-    constexpr size_t kOut = kVec * sizeof(T);
-    c.wide_out = rows_at<T>(c.out, kOut) && rows_at<T>(c.dx, kOut) && rows_at<T>(c.dgate, kOut);
-    if (c.form == AK_RECURRENCE_DECAY)
-        return w ? launch<T, AK_RECURRENCE_DECAY, R, REV, true, 2>(c, stream) : launch<T, AK_RECURRENCE_DECAY, R, REV, false, 2>(c, stream);
-    return w ? launch<T, AK_RECURRENCE_GATE, R, REV, true, 2>(c, stream) : launch<T, AK_RECURRENCE_GATE, R, REV, false, 2>(c, stream);
+ak_status by_form(const RecurrenceCall& c, cudaStream_t stream) {
+    return c.form == AK_RECURRENCE_DECAY ? by_length<T, AK_RECURRENCE_DECAY, REV>(c, stream)
+                                         : by_length<T, AK_RECURRENCE_GATE, REV>(c, stream);
 }
 
 template <class T, int FORM>
