@@ -619,7 +619,7 @@ ak_status ak_gated_recurrence_step(const ak_recurrence* shape, const ak_rows* x,
  *   length lengths[k]; its logits are not read
  * and the request's best `keep` of all its beams' candidates, by
  * total / length^penalty, are its next beams, in decreasing order (ties: the
- * lowest beam, then token).
+ * lowest beam, then the larger logit, then the lowest token).
  *
  *   logits     device, element (r, k, v) at r*batch_stride + k*beam_stride + v;
  *              AK_F32 or AK_BF16

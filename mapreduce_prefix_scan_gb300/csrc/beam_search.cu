@@ -12,10 +12,10 @@
 // over a row gives its sum and its best `keep` logits, and the request's
 // answer is among them. A cluster of blocks takes a request, a block a row
 // or a slice of one at a time:
-//  - pass: each thread folds its columns (groups of four, kThreads groups
-//    apart) to a maximum, its column and a sum of exponentials; no list is
-//    kept beside it, so an element costs a conversion, a maximum, a
-//    difference, an exponential and two sums;
+//  - pass: each thread folds its columns (16 bytes of them, then those kThreads
+//    times as far on, four such groups in flight) to a maximum, its column and a
+//    sum of exponentials; no list is kept beside it, so an element costs a
+//    conversion, a maximum, an exponential and three halves of packed pairs;
 //  - the `keep`-th best of the threads' maxima is a bound below which nothing
 //    can be chosen, and only the (at most `keep`) threads whose maximum
 //    reaches it hold candidates: their columns are read once more, from L2;
@@ -26,7 +26,8 @@
 //
 // Decisions lie next to one another: logits differ by little, and so do the
 // beams' sums. Sums of exponentials are float32 with a running compensation,
-// the logarithm, the totals and the ranks are 64-bit.
+// the logarithm, the totals and the ranks are 64-bit (a few for each row: the
+// device adds 64-bit numbers 64 times slower than 32-bit ones).
 #include <algorithm>
 #include <atomic>
 #include <cooperative_groups.h>
@@ -43,8 +44,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kMaxBeams = 32;     // of a request, before and after: a list is a warp
 constexpr int kMaxParts = 16;     // blocks of a cluster
-constexpr int kUnroll = 4;        // groups of four in flight
-constexpr int kBatch = kThreads * 4;  // elements of a candidates' batch
+constexpr int kAhead = 4;         // groups of 16 bytes that a thread has in flight
+constexpr int kFound = kThreads * 4;  // candidates held at a time
 
 // Orders floats as unsigned integers; -0 and 0 are one value.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -64,24 +65,21 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t col) {
     return x > -INFINITY ? (uint64_t)ordered(x) << 32 | (0xffffffffu - col) : 0;
 }
 
-// What the merge of the rows sorts: the rank, then the lowest beam and token.
+// What the merge of the rows sorts: the rank, then the lowest beam and its own order.
 struct Pick {
     uint64_t rank;   // 0: none
-    uint64_t place;  // ~(beam << 32 | token)
-    float total;
-    __device__ __forceinline__ bool over(const Pick& o) const {
-        return rank > o.rank || (rank == o.rank && place > o.place);
-    }
+    uint32_t place;  // ~(beam * 32 + place in its list)
 };
 
 __device__ __forceinline__ bool over(uint64_t a, uint64_t b) { return a > b; }
-__device__ __forceinline__ bool over(const Pick& a, const Pick& b) { return a.over(b); }
+__device__ __forceinline__ bool over(const Pick& a, const Pick& b) {
+    return a.rank > b.rank || (a.rank == b.rank && a.place > b.place);
+}
 __device__ __forceinline__ uint64_t from_lane(uint64_t v, int mask) { return __shfl_xor_sync(0xffffffffu, v, mask); }
 __device__ __forceinline__ Pick from_lane(const Pick& v, int mask) {
     Pick o;
     o.rank = __shfl_xor_sync(0xffffffffu, v.rank, mask);
     o.place = __shfl_xor_sync(0xffffffffu, v.place, mask);
-    o.total = __shfl_xor_sync(0xffffffffu, v.total, mask);
     return o;
 }
 
@@ -128,62 +126,77 @@ __device__ __forceinline__ void block_merge(K& list, K (*s_lists)[kWarp], int la
     }
 }
 
+// 16 bytes of a row.
 template <class T>
-struct alignas(4 * sizeof(T)) Group {
-    uint32_t w[sizeof(T)];
-};
-__device__ __forceinline__ float get(const Group<float>& f, int i) { return __uint_as_float(f.w[i]); }
-__device__ __forceinline__ float get(const Group<bf16>& f, int i) {
-    return __uint_as_float(i % 2 ? f.w[i / 2] & 0xffff0000u : f.w[i / 2] << 16);
-}
-__device__ __forceinline__ Group<float> ld_group(const float* p) {
-    Group<float> f;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-        : "=r"(f.w[0]), "=r"(f.w[1]), "=r"(f.w[2]), "=r"(f.w[3]) : "l"(p));
-    return f;
-}
-__device__ __forceinline__ Group<bf16> ld_group(const bf16* p) {
-    Group<bf16> f;
-    asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(f.w[0]), "=r"(f.w[1]) : "l"(p));
-    return f;
-}
-__device__ __forceinline__ float as_float(float v) { return v; }
-__device__ __forceinline__ float as_float(bf16 v) { return __bfloat162float(v); }
-
-// Columns [col, col + 4) of a row of `vocab`, -infinity past its end. The
-// columns of a group are the same whatever the row's alignment: equal rows
-// give equal sums.
-template <class T>
-__device__ __forceinline__ void load_group(float (&x)[4], const T* row, uint32_t col, uint32_t end, bool wide) {
-    if (wide && col + 4 <= end) {
-        const Group<T> g = ld_group(row + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = get(g, i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = col + i < end ? as_float(row[col + i]) : -INFINITY;
+struct alignas(16) Group {
+    static constexpr int kSize = 16 / (int)sizeof(T);
+    uint32_t w[4];
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
+};
+
+// Columns [col, col + kSize) of a row, -infinity from column `end` on. The columns of
+// a group are the same whatever the row's alignment: equal rows give equal sums.
+template <class T>
+__device__ __forceinline__ Group<T> load_group(const T* row, uint64_t col, uint32_t end, bool wide) {
+    constexpr int G = Group<T>::kSize;
+    Group<T> g;
+    if (wide && col + G <= end) {
+        asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+            : "=r"(g.w[0]), "=r"(g.w[1]), "=r"(g.w[2]), "=r"(g.w[3]) : "l"(row + col));
+        return g;
+    }
+    T v[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) v[i] = col + i < end ? row[col + i] : T(-INFINITY);
+    memcpy(&g, v, sizeof g);
+    return g;
+}
+
+// Two float32 sums or products at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float low(uint64_t p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float high(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // A row's (or slice's) share of the answer, in the first block's shared memory.
 struct Share {
     float top;         // the largest logit, or -infinity
-    double sum;        // of exp(x - top)
+    float sum, lost;   // of exp(x - top)
     uint64_t keys[kMaxBeams];
 };
 
 struct Shared {
     uint64_t lists[kWarps][kWarp];
     Pick picks[kWarps][kWarp];
-    uint64_t found[kBatch];
+    uint64_t found[kFound];
     int nfound, nchosen;
     int chosen[kMaxBeams];
     uint64_t bound;
-    float tops[kWarps];
-    double sums[kWarps];
+    float tops[kWarps], sums[kWarps], losts[kWarps];
     double norm[kMaxBeams];   // length^penalty of a beam's candidates
+    double base[kMaxBeams];   // minus the largest logit, minus log sum exp over it
     Share share[kMaxBeams];   // of the rows' slices (first block)
-    double base[kMaxBeams];   // s_k - log sum exp, less the largest logit
+    float totals[kMaxBeams][kWarp];
+    uint32_t tokens[kMaxBeams][kWarp];
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -197,55 +210,55 @@ __device__ __forceinline__ void add(float& sum, float& lost, float x) {
 
 // Folds columns [first, last) of a row and writes its share.
 template <class T>
-__device__ void fold_row(const T* row, uint32_t first, uint32_t last, int keep, Shared& s, Share* out) {
+__device__ void fold_row(const T* row, uint32_t first, uint32_t last, int keep, Shared& s, Share* out, bool& waited) {
+    constexpr int G = Group<T>::kSize;
+    constexpr uint64_t kStep = (uint64_t)kThreads * G;
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
-    const bool wide = (reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) == 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
     float top = -INFINITY, ref = 0.0f, sum = 0.0f, lost = 0.0f;
     uint32_t at = 0;
-    for (uint64_t c0 = first + tid * 4u; c0 < last; c0 += (uint64_t)kThreads * 4 * kUnroll) {
-        float x[kUnroll][4];
+    Group<T> next[kAhead];
+    uint64_t c0 = first + (uint64_t)tid * G;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint64_t col = c0 + (uint64_t)u * kThreads * 4;
-            if (col < last) load_group(x[u], row, (uint32_t)col, last, wide);
-            else x[u][0] = x[u][1] = x[u][2] = x[u][3] = -INFINITY;
+    for (int u = 0; u < kAhead; ++u) next[u] = load_group(row, c0 + u * kStep, last, wide);
+    for (; c0 < last; c0 += kAhead * kStep) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const uint64_t col = c0 + u * kStep;
+            float x[G];
+#pragma unroll
+            for (int i = 0; i < G; ++i) x[i] = next[u][i];
+            next[u] = load_group(row, col + kAhead * kStep, last, wide);
+            float m = x[0];
+#pragma unroll
+            for (int i = 1; i < G; ++i) m = fmaxf(m, x[i]);
+            if (m > top) {
+                const float f = exp2f((ref - m) * kLog2e);
+                if (top > -INFINITY) sum *= f, lost *= f;
+                top = ref = m;
+                uint32_t i = 0;
+#pragma unroll
+                for (int j = G - 1; j >= 0; --j)
+                    if (x[j] == m) i = j;
+                at = (uint32_t)col + i;
+            }
+            const uint64_t less = pair(-ref, -ref), scale = pair(kLog2e, kLog2e);
+            uint64_t e = 0;
+#pragma unroll
+            for (int i = 0; i < G; i += 2) {
+                const uint64_t y = mul2(add2(pair(x[i], x[i + 1]), less), scale);
+                const uint64_t z = pair(exp2_fast(low(y)), exp2_fast(high(y)));
+                e = i == 0 ? z : add2(e, z);
+            }
+            add(sum, lost, low(e) + high(e));
         }
-        float m = x[0][0];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m = fmaxf(m, x[u][i]);
-        if (m > top) {
-            const float f = exp2f((ref - m) * kLog2e);
-            if (top > -INFINITY) sum *= f, lost *= f;
-            top = ref = m;
-            bool found = false;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (!found && x[u][i] == m) {
-                        found = true;
-                        at = (uint32_t)c0 + u * kThreads * 4 + i;
-                    }
-        }
-        float e = 0.0f;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"((x[u][i] - ref) * kLog2e));
-            e += (y[0] + y[1]) + (y[2] + y[3]);
-        }
-        add(sum, lost, e);
     }
-    // ---- the block's maximum and sum
+    // ---- the block's maximum and sum; the threads' best, and the bound
     float best = top;
 #pragma unroll
     for (int d = kWarp / 2; d > 0; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
     if (lane == 0) s.tops[warp] = best;
     if (tid == 0) s.nchosen = 0;
-    // ---- the threads' best, and the bound
     const uint64_t mine = key_of(top, at);
     uint64_t list = mine;
     warp_sort(list, lane);
@@ -253,11 +266,16 @@ __device__ void fold_row(const T* row, uint32_t first, uint32_t last, int keep, 
     best = s.tops[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) best = fmaxf(best, s.tops[w]);
-    // a NaN among the logits is in `sum` alone
-    double sm = top > -INFINITY ? ((double)sum + lost) * expf(top - best) : (double)sum;
+    // (a NaN among the logits is in `sum` alone)
+    const float f = top > -INFINITY ? exp2f((top - best) * kLog2e) : 1.0f;
+    sum *= f, lost *= f;
 #pragma unroll
-    for (int d = kWarp / 2; d > 0; d >>= 1) sm += __shfl_xor_sync(0xffffffffu, sm, d);
-    if (lane == 0) s.sums[warp] = sm;
+    for (int d = kWarp / 2; d > 0; d >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, sum, d), ol = __shfl_xor_sync(0xffffffffu, lost, d);
+        lost += ol;
+        add(sum, lost, o);
+    }
+    if (lane == 0) s.sums[warp] = sum, s.losts[warp] = lost;
     block_merge(list, s.lists, lane, warp);
     if (warp == 0) {
         const uint64_t b = __shfl_sync(0xffffffffu, list, keep - 1);
@@ -268,39 +286,62 @@ __device__ void fold_row(const T* row, uint32_t first, uint32_t last, int keep, 
     // (fewer than `keep` threads with a candidate: each of them is looked through)
     if (mine && mine >= bound) s.chosen[atomicAdd(&s.nchosen, 1)] = tid;
     __syncthreads();
-    // ---- the chosen threads' columns again, a batch of groups at a time
+    // ---- the chosen threads' columns again, 16 of them a thread at a time; where
+    // more are candidates than there is room for, a group
+    constexpr int kSome = 16 / G;
     const int chosen = s.nchosen;
-    const uint32_t groups = (last - first + 3) / 4, per = (groups + kThreads - 1) / kThreads;  // of a thread, at most
+    const uint32_t groups = (last - first + G - 1) / G, per = (groups + kThreads - 1) / kThreads;  // of a thread, at most
+    const uint32_t all = per * (uint32_t)chosen;
+    bool spread = false;  // more than warp 0 holds a list
     list = 0;
-    for (uint32_t g0 = 0; g0 < per * (uint32_t)chosen; g0 += kThreads) {
-        if (tid == 0) s.nfound = 0;
-        __syncthreads();
-        const uint32_t g = g0 + tid;
-        if (g < per * (uint32_t)chosen) {
-            const uint64_t col = first + ((uint64_t)(g % per) * kThreads + s.chosen[g / per]) * 4;
-            if (col < last) {
-                float x[4];
-                load_group(x, row, (uint32_t)col, last, wide);
+    for (uint32_t g0 = 0; g0 < all; g0 += kSome * kThreads) {
+        Group<T> x[kSome];
+        uint64_t col[kSome];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint64_t k = key_of(x[i], (uint32_t)col + i);
-                    if (k && k >= bound) s.found[atomicAdd(&s.nfound, 1)] = k;
+        for (int j = 0; j < kSome; ++j) {
+            const uint32_t g = g0 + j * kThreads + tid;
+            col[j] = g < all ? first + ((uint64_t)(g % per) * kThreads + s.chosen[g / per]) * G : last;
+            x[j] = load_group(row, col[j], last, wide);
+        }
+        for (int only = -1; only < kSome; ++only) {
+            if (tid == 0) s.nfound = 0;
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kSome; ++j) {
+                if (only >= 0 && only != j) continue;
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    const uint64_t k = key_of(x[j][i], (uint32_t)col[j] + i);
+                    if (k && k >= bound) {
+                        const int to = atomicAdd(&s.nfound, 1);
+                        if (to < kFound) s.found[to] = k;
+                    }
                 }
             }
+            __syncthreads();
+            const int n = s.nfound;
+            if (n <= kFound) {
+                spread |= n > kWarp;
+                for (int b = warp * kWarp; b < n; b += kThreads) warp_take(list, b + lane < n ? s.found[b + lane] : uint64_t(0), lane);
+            }
+            __syncthreads();
+            if (only < 0 && n <= kFound) break;
         }
-        __syncthreads();
-        const int n = s.nfound;
-        for (int b = warp * kWarp; b < n; b += kThreads) warp_take(list, b + lane < n ? s.found[b + lane] : uint64_t(0), lane);
-        __syncthreads();
     }
-    block_merge(list, s.lists, lane, warp);
+    if (spread) block_merge(list, s.lists, lane, warp);
+    if (!waited) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the first block runs
+    waited = true;
     if (warp == 0) {
         out->keys[lane] = list;
         if (lane == 0) {
-            double total = 0.0;
-            for (int w = 0; w < kWarps; ++w) total += s.sums[w];
+            sum = s.sums[0], lost = s.losts[0];
+            for (int w = 1; w < kWarps; ++w) {
+                lost += s.losts[w];
+                add(sum, lost, s.sums[w]);
+            }
             out->top = best;
-            out->sum = total;
+            out->sum = sum;
+            out->lost = lost;
         }
     }
     __syncthreads();
@@ -317,25 +358,27 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
     const float* scores = c.scores + r * n;
     const uint8_t* done = c.done ? c.done + r * n : nullptr;
     const int32_t* lengths = c.lengths ? c.lengths + r * n : nullptr;
-    const uint32_t vocab = (uint32_t)c.vocab, slice = ((vocab + slices - 1) / slices + 3) / 4 * 4;
+    const uint32_t vocab = (uint32_t)c.vocab, slice = ((vocab + slices - 1) / slices + 7) / 8 * 8;
 
-    if (parts > 1) cl.sync();  // the first block runs before another writes to it
+    if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     Shared* s0 = cl.map_shared_rank(&s, 0);
     if (rank == 0 && warp == kWarps - 1 && lane < n) {
         double norm = 1.0;
         if (c.penalty != 0.0f) {
             const int len = (lengths ? lengths[lane] : 0) + !(done && done[lane]);
-            norm = pow((double)len, (double)c.penalty);
+            norm = c.penalty == 1.0f ? (double)len : pow((double)len, (double)c.penalty);
         }
         s.norm[lane] = norm;
     }
+    bool waited = parts == 1;
     for (int item = rank; item < n * slices; item += parts) {
         const int k = item / slices;
         const float sc = scores[k];
         if ((done && done[k]) || !(fabsf(sc) < INFINITY)) continue;  // no need of its logits
         const uint32_t first = min((uint64_t)(item % slices) * slice, (uint64_t)vocab), last = min(first + slice, vocab);
-        fold_row(static_cast<const T*>(c.logits) + r * c.batch_stride + k * c.beam_stride, first, last, keep, s, &s0->share[item]);
+        fold_row(static_cast<const T*>(c.logits) + r * c.batch_stride + k * c.beam_stride, first, last, keep, s, &s0->share[item], waited);
     }
+    if (!waited) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (parts > 1) cl.sync();
     else __syncthreads();
     if (rank != 0) return;
@@ -347,40 +390,36 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
         double sum = 0.0;
         for (int i = 0; i < slices; ++i) {
             const Share& h = s.share[tid * slices + i];
-            sum += h.top > -INFINITY ? h.sum * (slices > 1 ? expf(h.top - top) : 1.0f) : h.sum;
+            const float f = slices > 1 && h.top > -INFINITY ? exp2f((h.top - top) * kLog2e) : 1.0f;
+            sum += (double)(h.sum * f) + (double)(h.lost * f);
         }
         s.base[tid] = -(double)top - log(sum);
     }
     __syncthreads();
-    // ---- candidates of all rows
-    Pick list = {0, 0, 0.0f};
-    for (int item = warp; item < n * slices; item += kWarps) {
-        const int k = item / slices;
+    // ---- candidates of all rows, each a list in its own order
+    Pick list = {0, 0};
+    for (int k = warp; k < n; k += kWarps) {
         const float sc = scores[k];
-        Pick v = {0, 0, 0.0f};
+        const bool was = done && done[k];
+        Pick v = {0, ~(uint32_t)(k * kWarp + lane)};
         if (fabsf(sc) < INFINITY) {
-            double total = 0.0;
-            bool any;
+            double total = sc;
+            bool any = lane == 0;
             uint32_t token = 0;
-            if (done && done[k]) {
-                any = lane == 0 && item % slices == 0;
-                total = sc;
-                token = (uint32_t)max(c.end, 0);
-            } else {
-                const uint64_t key = s.share[item].keys[lane];
+            if (!was) {
+                uint64_t key = s.share[k * slices].keys[lane];
+                for (int i = 1; i < slices; ++i) warp_merge(key, s.share[k * slices + i].keys[kWarp - 1 - lane], lane);
                 any = key != 0 && lane < keep;
                 token = 0xffffffffu - (uint32_t)key;
                 // (x - top) first: the difference of neighbours is exact
-                total = (double)sc + ((double)value_of((uint32_t)(key >> 32)) + s.base[k]);
+                total += (double)value_of((uint32_t)(key >> 32)) + s.base[k];
             }
-            const double q = total / s.norm[k];
-            if (any && q > -INFINITY && q < INFINITY) {
-                v.rank = ordered(q);
-                v.place = ~((uint64_t)k << 32 | token);
-                v.total = (float)total;
-            }
+            const double q = c.penalty == 0.0f ? total : total / s.norm[k];
+            if (any && q > -INFINITY && q < INFINITY) v.rank = ordered(q);
+            s.totals[k][lane] = (float)total;
+            s.tokens[k][lane] = token;
         }
-        warp_take(list, v, lane);
+        warp_merge(list, from_lane(v, kWarp - 1), lane);
     }
     block_merge(list, s.picks, lane, warp);
     if (warp == 0 && lane < keep) {
@@ -389,10 +428,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
         bool ended = true;
         float total = -INFINITY;
         if (list.rank) {
-            const uint64_t place = ~list.place;
-            parent = (int)(place >> 32);
-            token = (int)(uint32_t)place;
-            total = list.total;
+            const uint32_t place = ~list.place;
+            parent = (int)(place / kWarp);
+            token = (int)s.tokens[parent][place % kWarp];
+            total = s.totals[parent][place % kWarp];
             const bool was = done && done[parent];
             if (was) token = c.end;
             ended = was || (c.end >= 0 && token == c.end);
