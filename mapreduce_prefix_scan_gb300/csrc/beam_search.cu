@@ -18,7 +18,9 @@
 //    conversion, a maximum, an exponential and three halves of packed pairs;
 //  - the `keep`-th best of the threads' maxima is a bound below which nothing
 //    can be chosen, and only the (at most `keep`) threads whose maximum
-//    reaches it hold candidates: their columns are read once more, from L2;
+//    reaches it hold candidates: their columns are read once more, from L2 (with
+//    the least of the warps' maxima for a bound, found sooner, 20 threads hold
+//    candidates for 8 beams, and 64 x 8 rows of 128000 take 58 us, not 44);
 //  - lists of 32 lie in the lanes of a warp and are merged as bitonic
 //    sequences; the cluster's first block merges the rows.
 // Keys order by (logit, lowest column), so the answer does not depend on the
@@ -114,11 +116,11 @@ __device__ __forceinline__ void warp_take(K& list, K v, int lane) {
     warp_merge(list, from_lane(v, kWarp - 1), lane);
 }
 
-// Warp 0's list becomes the best 32 of all warps' lists. Ends in sync.
+// Warp 0's list becomes the best 32 of the first `warps` warps' lists (a power of
+// two). Ends in sync.
 template <class K>
-__device__ __forceinline__ void block_merge(K& list, K (*s_lists)[kWarp], int lane, int warp) {
-#pragma unroll
-    for (int half = kWarps / 2; half > 0; half >>= 1) {
+__device__ __forceinline__ void block_merge(K& list, K (*s_lists)[kWarp], int lane, int warp, int warps = kWarps) {
+    for (int half = warps / 2; half > 0; half >>= 1) {
         if (warp >= half && warp < 2 * half) s_lists[warp][lane] = list;
         __syncthreads();
         if (warp < half) warp_merge(list, s_lists[warp + half][kWarp - 1 - lane], lane);
@@ -192,7 +194,9 @@ struct Shared {
     int chosen[kMaxBeams];
     uint64_t bound;
     float tops[kWarps], sums[kWarps], losts[kWarps];
-    double norm[kMaxBeams];   // length^penalty of a beam's candidates
+    double per[kMaxBeams];    // 1 / length^penalty of a beam's candidates
+    float score[kMaxBeams];
+    bool was[kMaxBeams];
     double base[kMaxBeams];   // minus the largest logit, minus log sum exp over it
     Share share[kMaxBeams];   // of the rows' slices (first block)
     float totals[kMaxBeams][kWarp];
@@ -363,12 +367,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
     if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     Shared* s0 = cl.map_shared_rank(&s, 0);
     if (rank == 0 && warp == kWarps - 1 && lane < n) {
-        double norm = 1.0;
-        if (c.penalty != 0.0f) {
-            const int len = (lengths ? lengths[lane] : 0) + !(done && done[lane]);
-            norm = c.penalty == 1.0f ? (double)len : pow((double)len, (double)c.penalty);
-        }
-        s.norm[lane] = norm;
+        const bool was = done && done[lane];
+        const int len = (lengths ? lengths[lane] : 0) + !was;
+        s.score[lane] = scores[lane];
+        s.was[lane] = was;
+        s.per[lane] = c.penalty == 0.0f ? 1.0 : 1.0 / (c.penalty == 1.0f ? (double)len : pow((double)len, (double)c.penalty));
     }
     bool waited = parts == 1;
     for (int item = rank; item < n * slices; item += parts) {
@@ -385,22 +388,22 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
 
     // ---- the rows' logarithms
     if (tid < n) {
-        float top = -INFINITY;
-        for (int i = 0; i < slices; ++i) top = fmaxf(top, s.share[tid * slices + i].top);
-        double sum = 0.0;
+        const Share* h = s.share + tid * slices;
+        float top = -INFINITY, sum = 0.0f, lost = 0.0f;
+        for (int i = 0; i < slices; ++i) top = fmaxf(top, h[i].top);
         for (int i = 0; i < slices; ++i) {
-            const Share& h = s.share[tid * slices + i];
-            const float f = slices > 1 && h.top > -INFINITY ? exp2f((h.top - top) * kLog2e) : 1.0f;
-            sum += (double)(h.sum * f) + (double)(h.lost * f);
+            const float f = slices > 1 && h[i].top > -INFINITY ? exp2f((h[i].top - top) * kLog2e) : 1.0f;
+            lost += h[i].lost * f;
+            add(sum, lost, h[i].sum * f);
         }
-        s.base[tid] = -(double)top - log(sum);
+        s.base[tid] = -(double)top - log((double)sum + lost);
     }
     __syncthreads();
     // ---- candidates of all rows, each a list in its own order
     Pick list = {0, 0};
     for (int k = warp; k < n; k += kWarps) {
-        const float sc = scores[k];
-        const bool was = done && done[k];
+        const float sc = s.score[k];
+        const bool was = s.was[k];
         Pick v = {0, ~(uint32_t)(k * kWarp + lane)};
         if (fabsf(sc) < INFINITY) {
             double total = sc;
@@ -414,14 +417,16 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
                 // (x - top) first: the difference of neighbours is exact
                 total += (double)value_of((uint32_t)(key >> 32)) + s.base[k];
             }
-            const double q = c.penalty == 0.0f ? total : total / s.norm[k];
+            const double q = total * s.per[k];
             if (any && q > -INFINITY && q < INFINITY) v.rank = ordered(q);
             s.totals[k][lane] = (float)total;
             s.tokens[k][lane] = token;
         }
         warp_merge(list, from_lane(v, kWarp - 1), lane);
     }
-    block_merge(list, s.picks, lane, warp);
+    int warps = 1;
+    while (warps < kWarps && warps < n) warps *= 2;
+    block_merge(list, s.picks, lane, warp, warps);
     if (warp == 0 && lane < keep) {
         const int64_t o = r * keep + lane;
         int token = -1, parent = -1, length = 0;
@@ -432,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
             parent = (int)(place / kWarp);
             token = (int)s.tokens[parent][place % kWarp];
             total = s.totals[parent][place % kWarp];
-            const bool was = done && done[parent];
+            const bool was = s.was[parent];
             if (was) token = c.end;
             ended = was || (c.end >= 0 && token == c.end);
             length = (lengths ? lengths[parent] : 0) + !was;
