@@ -68,9 +68,13 @@ def ak_beam_select(logits: torch.Tensor, scores: torch.Tensor, *, done: torch.Te
     if kind is None or on < 0 or not _s._dense_rows(logits):
         raise ValueError("logits: a float32 or bfloat16 CUDA tensor with contiguous rows is needed")
     m = k if keep is None else int(keep)
-    given = out if out is not None else (None,) * 5
-    step = BeamStep(*(_given(t, (n, m), d, f, on, dev, stream) for t, d, f in zip(
-        given, (torch.float32, torch.int32, torch.int32, torch.bool, torch.int32), BeamStep._fields)))
+    if out is None:  # (allocations are half of a small call's time, views of a larger one more)
+        e, shape, i32 = _s._empty, (n, m), torch.int32
+        step = BeamStep(e(shape, torch.float32, dev, stream), e(shape, i32, dev, stream), e(shape, i32, dev, stream),
+                        e(shape, torch.bool, dev, stream), e(shape, i32, dev, stream))
+    else:
+        step = BeamStep(*(_given(t, (n, m), d, f, on, dev, stream) for t, d, f in zip(
+            out, (torch.float32, torch.int32, torch.int32, torch.bool, torch.int32), BeamStep._fields)))
     ls = logits.stride()
     _s._check(_abi.load().ak_beam_select(
         logits.data_ptr(), ls[0], ls[1], kind, n, k, vocab, m, _shaped(scores, (n, k), torch.float32, "scores", on),
@@ -152,7 +156,10 @@ def ak_blocks_count(block_table: torch.Tensor, lens: torch.Tensor, *, block_size
     first ceil(len / block_size) entries of each request's row of ``block_table``."""
     on = block_table.get_device()
     a = _table(block_table, lens, on)
-    refs = _given(out, (blocks,), torch.int32, "out", on, block_table.device, stream)
+    if out is None:
+        refs = _s._empty(blocks, torch.int32, block_table.device, stream)
+    else:
+        refs = _given(out, (blocks,), torch.int32, "out", on, None, None)
     _s._check(_abi.load().ak_blocks_count(*a, block_size, blocks, refs.data_ptr(), _s._opts(opts),
                                           _s._stream_of(stream, block_table)), "ak_blocks_count")
     return refs
@@ -170,10 +177,14 @@ def ak_blocks_fork(block_table: torch.Tensor, lens: torch.Tensor, parents: torch
     a = _table(block_table, lens, on)
     n, nfree = parents.numel(), free_blocks.numel()
     p, fb = _s._flat(parents, torch.int32, n, "parents", on), _s._flat(free_blocks, torch.int32, nfree, "free_blocks", on)
-    given = out if out is not None else (None,) * 5
     width = block_table.shape[1]
-    f = BlockFork(*(_given(t, s, torch.int32, name, on, dev, stream) for t, s, name in zip(
-        given, ((n, width), (n,), (blocks,), (n, 2), (1,)), BlockFork._fields)))
+    if out is None:
+        e, i32 = _s._empty, torch.int32
+        f = BlockFork(e((n, width), i32, dev, stream), e(n, i32, dev, stream), e(blocks, i32, dev, stream), e((n, 2), i32, dev, stream),
+                      e(1, i32, dev, stream))
+    else:
+        f = BlockFork(*(_given(t, s, torch.int32, name, on, dev, stream) for t, s, name in zip(
+            out, ((n, width), (n,), (blocks,), (n, 2), (1,)), BlockFork._fields)))
     b = ctypes.c_size_t()
     L = _abi.load()
     _s._check(L.ak_blocks_fork_workspace_size(n, blocks, None, b), "ak_blocks_fork_workspace_size")
@@ -190,8 +201,9 @@ def ak_blocks_free(refs: torch.Tensor, *, out: torch.Tensor | None = None, count
     order, then -1 ([blocks] int32), and how many they are ([1] int32)."""
     on, n = refs.get_device(), refs.numel()
     p = _s._flat(refs, torch.int32, n, "refs", on)
-    free = _given(out, (n,), torch.int32, "out", on, refs.device, stream)
-    counts = _given(counts, (1,), torch.int32, "counts", on, refs.device, stream)
+    dev = refs.device
+    free = _s._empty(n, torch.int32, dev, stream) if out is None else _given(out, (n,), torch.int32, "out", on, dev, stream)
+    counts = _s._empty(1, torch.int32, dev, stream) if counts is None else _given(counts, (1,), torch.int32, "counts", on, dev, stream)
     _s._check(_abi.load().ak_blocks_free(p, n, free.data_ptr(), counts.data_ptr(), _s._opts(opts), _s._stream_of(stream, refs)),
               "ak_blocks_free")
     return free, counts

@@ -100,7 +100,8 @@ def ak_gated_recurrence(x: torch.Tensor, gate: torch.Tensor, *, form: str = "dec
         out = _s._empty(x.shape, x.dtype, x.device, stream)
     if state_out is None and final_state:
         state_out = _s._empty(ss, torch.float32, x.device, stream)
-    rx, rg, ro = (_rows(t, x.shape, x.dtype, n, on) for t, n in ((x, "x"), (gate, "gate"), (out, "out")))
+    shape, dt = x.shape, x.dtype
+    rx, rg, ro = _rows(x, shape, dt, "x", on), _rows(gate, shape, dt, "gate", on), _rows(out, shape, dt, "out", on)
     _s._check(_abi.load().ak_gated_recurrence(a, rx, rg, off, _state(state, ss, "state", on), ro,
                                               _state(state_out, ss, "state_out", on), _s._opts(opts),
                                               _s._stream_of(stream, x)), "ak_gated_recurrence")
@@ -121,8 +122,9 @@ def ak_gated_recurrence_backward(dh: torch.Tensor, x: torch.Tensor, gate: torch.
     dgate = _s._empty(x.shape, x.dtype, x.device, stream) if dgate is None else dgate
     if dstate is None and state is not None:
         dstate = _s._empty(ss, torch.float32, x.device, stream)
-    rd, rx, rg, rh, rdx, rdg = (_rows(t, x.shape, x.dtype, n, on) for t, n in (
-        (dh, "dh"), (x, "x"), (gate, "gate"), (h, "h"), (dx, "dx"), (dgate, "dgate")))
+    shape, dt = x.shape, x.dtype
+    rd, rx, rg = _rows(dh, shape, dt, "dh", on), _rows(x, shape, dt, "x", on), _rows(gate, shape, dt, "gate", on)
+    rh, rdx, rdg = _rows(h, shape, dt, "h", on), _rows(dx, shape, dt, "dx", on), _rows(dgate, shape, dt, "dgate", on)
     _s._check(_abi.load().ak_gated_recurrence_backward(
         a, rd, rx, rg, rh, off, _state(state, ss, "state", on), _state(dstate_out, ss, "dstate_out", on), rdx, rdg,
         _state(dstate, ss, "dstate", on), _s._opts(opts), _s._stream_of(stream, x)), "ak_gated_recurrence_backward")
@@ -143,7 +145,8 @@ def ak_gated_recurrence_step(x: torch.Tensor, gate: torch.Tensor, state: torch.T
     a, (_, c), _, on = _geometry(x, None, form)
     if out is None:
         out = _s._empty(x.shape, x.dtype, x.device, stream)
-    rx, rg, ro = (_rows(t, x.shape, x.dtype, n, on) for t, n in ((x, "x"), (gate, "gate"), (out, "out")))
+    shape, dt = x.shape, x.dtype
+    rx, rg, ro = _rows(x, shape, dt, "x", on), _rows(gate, shape, dt, "gate", on), _rows(out, shape, dt, "out", on)
     pool = state.shape[0]
     sp = _state(state, (pool, c), "state", on)
     at = None if slots is None else _s._flat(slots, torch.int32, x.shape[0], "slots", on)

@@ -348,3 +348,52 @@ def test_rows_past_two_to_the_31():
     h, _ = ak.ak_gated_recurrence(x, gate, out=out)
     want, _ = ak.ak_gated_recurrence(x.contiguous(), gate)
     assert torch.equal(h, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_checked_call_ends_well(dtype):
+    c = _case([700, 1, 900], 64, dtype, "gate")
+    call = lambda o: ak.ak_gated_recurrence(c["x"], c["gate"], form="gate", offsets=c["offsets"], state=c["s0"], final_state=True, opts=o)  # noqa: E731
+    h, sf = call(None)
+    for limit in (0, 1):  # 1 ns: a wait lasts 0.1 s at least
+        a, b = call(dict(check=True, wait_limit_ns=limit))
+        assert torch.equal(a, h) and torch.equal(b, sf)
+    back = lambda o: ak.ak_gated_recurrence_backward(c["dh"], c["x"], c["gate"], h, form="gate", offsets=c["offsets"], opts=o)  # noqa: E731
+    assert all(torch.equal(a, b) for a, b in zip(back(None)[:2], back(dict(check=True))[:2]))
+    s = c["s0"].clone()
+    ak.ak_gated_recurrence_step(c["x"][:3], c["gate"][:3], s, opts=dict(check=True))
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """A tile whose map is not sent: the blocks of its cluster give up after 0.1 s, and the next call is sound."""
+    c = _case([1500, 1300], 64, torch.float32, "decay")
+    call = lambda **o: ak.ak_gated_recurrence(c["x"], c["gate"], offsets=c["offsets"], state=c["s0"], final_state=True, opts=dict(check=True, **o))  # noqa: E731
+    want = call()
+    for tile in (0, 7):
+        with pytest.raises(ak.AkError) as e:
+            call(debug_skip_publish_tile=tile, wait_limit_ns=1)
+        assert e.value.status == 6
+        got = call()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_on_a_given_stream():
+    c = _case([300, 200], 96, torch.bfloat16, "decay")
+    want = ak.ak_gated_recurrence(c["x"], c["gate"], offsets=c["offsets"], state=c["s0"], final_state=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = ak.ak_gated_recurrence(c["x"], c["gate"], offsets=c["offsets"], state=c["s0"], final_state=True, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_equal_gates_in_bf16_calls():
+    """States of bf16 calls at one gate: a run's 32 factors are exact to 2^-22 each (4 units of 2^-24, and one of
+    rounding), and half of that of all that runs add: (32 + 16) * 5 * 2^-24 = 1.4e-5 if every one pushed as far as it may."""
+    t, ch = 20000, 64
+    x = (torch.randn(t, ch, device="cuda") + 0.5).bfloat16()
+    for form, gate in (("decay", -1e-3), ("gate", 7.0)):
+        g = torch.full((t, ch), gate, device="cuda").bfloat16()
+        _, sf = ak.ak_gated_recurrence(x, g, form=form, final_state=True)
+        _, wsf, _ = ref.recurrence(_np(x), _np(g), [0, t], None, form)
+        assert np.linalg.norm(_np(sf) - wsf) <= 1.4e-5 * np.linalg.norm(wsf)
