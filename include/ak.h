@@ -563,6 +563,8 @@ ak_status ak_linear_attention_step(const ak_linattn* shape, const ak_heads* q, c
  *              all tokens (seqs = 1). Values are clamped to [0, tokens].
  *              Output rows of tokens outside every sequence are set to 0.
  *   state_in   device, seqs rows of channels float, or NULL
+ *   h          may be x itself (the same memory and stride): the call then works
+ *              in place (the gate form's gradients need x as it was)
  *   state_out  device, the states after each sequence's last token, or NULL;
  *              may be state_in. A sequence without tokens hands its state on.
  * The order of summation is fixed by the shape: equal calls give equal bits.

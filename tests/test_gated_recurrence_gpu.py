@@ -397,3 +397,15 @@ def test_equal_gates_in_bf16_calls():
         _, sf = ak.ak_gated_recurrence(x, g, form=form, final_state=True)
         _, wsf, _ = ref.recurrence(_np(x), _np(g), [0, t], None, form)
         assert np.linalg.norm(_np(sf) - wsf) <= 1.4e-5 * np.linalg.norm(wsf)
+
+
+@pytest.mark.parametrize("form", ["decay", "gate"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("channels", [77, 320])
+def test_in_place(channels, dtype, form):
+    """Outputs in x's own memory."""
+    c = _case([900, 0, 1, 1300], channels, dtype, form)
+    want, ws = ak.ak_gated_recurrence(c["x"], c["gate"], form=form, offsets=c["offsets"], state=c["s0"], final_state=True)
+    x = c["x"].clone()
+    h, sf = ak.ak_gated_recurrence(x, c["gate"], form=form, offsets=c["offsets"], state=c["s0"], final_state=True, out=x)
+    assert h is x and torch.equal(h, want) and torch.equal(sf, ws)
