@@ -434,7 +434,9 @@ def _run_own(s):
     op = s["op"]
     if op in ("recur", "train"):
         same = dict(form=s["form"], offsets=s["offsets"], state=s["s0"])
-        h, sf = ak.ak_gated_recurrence(s["x"], s["gate"], final_state=s["final"], **same)
+        # the plain form's scan is in x's own memory where x needs no conversion and no factor, and so is the call
+        place = s["x"] if s["dtype"] == "f32" and s["form"] == "decay" else None
+        h, sf = ak.ak_gated_recurrence(s["x"], s["gate"], out=place, final_state=s["final"], **same)
         if op == "recur":
             return {"h": h, "state": sf}
         dx, dgate, d0 = ak.ak_gated_recurrence_backward(s["dh"], s["x"], s["gate"], h, dstate_out=s["ds"], **same)
