@@ -647,6 +647,8 @@ ak_status ak_gated_recurrence_step(const ak_recurrence* shape, const ak_rows* x,
  *   out_scores, out_tokens, out_parents  device, batch * keep: total, token
  *              and the beam it extends
  *   out_done, out_lengths  device, likewise, or NULL
+ * With keep = beams, out_scores, out_done and out_lengths may be scores, done and
+ * lengths themselves.
  * Sums of exponentials are float32 with compensation; logarithms, totals and
  * their comparison are 64-bit, out_scores rounded from them. A
  * logit of -infinity, and what has no finite rank, is no candidate; a row
@@ -661,7 +663,7 @@ ak_status ak_gated_recurrence_step(const ak_recurrence* shape, const ak_rows* x,
  * ------------------------------------------------------------------------- */
 ak_status ak_beam_select(const void* logits, int64_t batch_stride, int64_t beam_stride, ak_dtype dtype, int64_t batch,
                          int32_t beams, int64_t vocab, int32_t keep, const float* scores, const uint8_t* done,
-                         const int32_t* lengths, int32_t end_token, float penalty, float* out_scores,
+                         const int32_t* lengths, int32_t end_token, double penalty, float* out_scores,
                          int32_t* out_tokens, int32_t* out_parents, uint8_t* out_done, int32_t* out_lengths,
                          const ak_opts* opts, void* stream);
 ak_status ak_beam_reorder(void* state, int64_t outer, int64_t outer_stride, int64_t batch, int64_t batch_stride,

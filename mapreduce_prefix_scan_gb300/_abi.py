@@ -117,8 +117,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.ak_gated_recurrence.argtypes = [PR, PA, PA, P, P, PA, P, PO, P]
     L.ak_gated_recurrence_backward.argtypes = [PR, PA, PA, PA, PA, P, P, P, PA, PA, P, PO, P]
     L.ak_gated_recurrence_step.argtypes = [PR, PA, PA, P, P, I64, PA, PO, P]
-    F32 = ctypes.c_float
-    L.ak_beam_select.argtypes = [P, I64, I64, I32, I64, I32, I64, I32, P, P, P, I32, F32, P, P, P, P, P, PO, P]
+    L.ak_beam_select.argtypes = [P, I64, I64, I32, I64, I32, I64, I32, P, P, P, I32, ctypes.c_double, P, P, P, P, P, PO, P]
     L.ak_beam_reorder.argtypes = [P, I64, I64, I64, I64, I32, I64, I64, P, PO, P]
     L.ak_blocks_count.argtypes = [P, I64, I32, P, I64, I32, I64, P, PO, P]
     L.ak_blocks_fork_workspace_size.argtypes = [I64, I64, PO, PSZ]

@@ -4,6 +4,7 @@
 // launchers (reduce.cu, reduce_dims.cu, scan.cu).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cstring>
@@ -354,6 +355,35 @@ ak_status run_linattn_backward(const LinattnCall& c, void* ws, cudaStream_t stre
 ak_status run_linattn_step(const LinattnCall& c, float* state, const int32_t* slots, int64_t nslots,
                            cudaStream_t stream);
 
+// The largest cluster (16 blocks, or 8 where the context cannot hold one of 16) of a
+// kernel on a device; larger ones than 8 are allowed for on the first call.
+struct ClusterLimit {
+    std::atomic<int> most[64];
+    ak_status get(const void* kernel, int threads, int device, int* out) {
+        std::atomic<int>& m = most[device & 63];
+        if (m == 0) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            int n = 0;
+            if (e == cudaSuccess) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(16);
+                cfg.blockDim = dim3((unsigned)threads);
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = 16;
+                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            }
+            if (e != cudaSuccess) return cuda_fail(e);
+            m = n > 0 ? 16 : 8;
+        }
+        *out = m;
+        return AK_OK;
+    }
+};
+
 // gated_recurrence.cu
 struct RecurrenceCall {
     ak_dtype dtype;
@@ -385,7 +415,7 @@ struct BeamCall {
     ak_dtype dtype;
     int64_t batch, vocab;
     int32_t beams, keep, end;
-    float penalty;
+    double penalty;
     const float* scores;
     const uint8_t* done;
     const int32_t* lengths;

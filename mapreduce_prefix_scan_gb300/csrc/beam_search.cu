@@ -31,7 +31,6 @@
 // the logarithm, the totals and the ranks are 64-bit (a few for each row: the
 // device adds 64-bit numbers 64 times slower than 32-bit ones).
 #include <algorithm>
-#include <atomic>
 #include <cooperative_groups.h>
 
 #include "ak_common.cuh"
@@ -45,7 +44,6 @@ namespace bs {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kMaxBeams = 32;     // of a request, before and after: a list is a warp
-constexpr int kMaxParts = 16;     // blocks of a cluster
 constexpr int kAhead = 4;         // groups of 16 bytes that a thread has in flight
 constexpr int kFound = kThreads * 4;  // candidates held at a time
 
@@ -194,8 +192,9 @@ struct Shared {
     int chosen[kMaxBeams];
     uint64_t bound;
     float tops[kWarps], sums[kWarps], losts[kWarps];
-    double per[kMaxBeams];    // 1 / length^penalty of a beam's candidates
-    float score[kMaxBeams];
+    double norm[kMaxBeams];   // length^penalty of a beam's candidates
+    float score[kMaxBeams];   // (outputs may lie where these came from)
+    int length[kMaxBeams];
     bool was[kMaxBeams];
     double base[kMaxBeams];   // minus the largest logit, minus log sum exp over it
     Share share[kMaxBeams];   // of the rows' slices (first block)
@@ -371,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
         const int len = (lengths ? lengths[lane] : 0) + !was;
         s.score[lane] = scores[lane];
         s.was[lane] = was;
-        s.per[lane] = c.penalty == 0.0f ? 1.0 : 1.0 / (c.penalty == 1.0f ? (double)len : pow((double)len, (double)c.penalty));
+        s.length[lane] = len;
+        s.norm[lane] = c.penalty == 1.0 || c.penalty == 0.0 ? (double)len : pow((double)len, c.penalty);
     }
     bool waited = parts == 1;
     for (int item = rank; item < n * slices; item += parts) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
                 // (x - top) first: the difference of neighbours is exact
                 total += (double)value_of((uint32_t)(key >> 32)) + s.base[k];
             }
-            const double q = total * s.per[k];
+            const double q = c.penalty == 0.0 ? total : total / s.norm[k];
             if (any && q > -INFINITY && q < INFINITY) v.rank = ordered(q);
             s.totals[k][lane] = (float)total;
             s.tokens[k][lane] = token;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
             const bool was = s.was[parent];
             if (was) token = c.end;
             ended = was || (c.end >= 0 && token == c.end);
-            length = (lengths ? lengths[parent] : 0) + !was;
+            length = s.length[parent];
         }
         c.out_scores[o] = total;
         c.out_tokens[o] = token;
@@ -501,21 +501,18 @@ ak_status run_beam_select(BeamCall c, cudaStream_t stream) {
     using namespace bs;
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
+    auto* kernel = c.dtype == AK_F32 ? k_beam_select<float> : k_beam_select<bf16>;
+    static ClusterLimit limits[2];
+    int most = 0;
+    const ak_status st = limits[c.dtype == AK_F32].get(reinterpret_cast<const void*>(kernel), kThreads, dev.device, &most);
+    if (st != AK_OK) return st;
     // blocks of a request: as many as run at once over all requests, four an
     // SM; whole rows each, or each row in slices of a round of loads at least
-    const int64_t room = std::max<int64_t>(1, std::min<int64_t>(kMaxParts, 4 * dev.sm_count / c.batch));
+    const int64_t room = std::max<int64_t>(1, std::min<int64_t>(most, 4 * dev.sm_count / c.batch));
     int parts = (int)std::min<int64_t>(room, c.beams);
     c.slices = 1;
     while ((c.slices + 1) * c.beams <= room && c.vocab / (c.slices + 1) >= kThreads * 4) ++c.slices;
     if (c.slices > 1) parts = c.slices * c.beams;
-    auto* kernel = c.dtype == AK_F32 ? k_beam_select<float> : k_beam_select<bf16>;
-    static std::atomic<uint64_t> ready[2];
-    std::atomic<uint64_t>& set = ready[c.dtype == AK_F32];
-    if (!(set.load() >> dev.device & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return cuda_fail(e);
-        set.fetch_or(1ull << dev.device);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(c.batch * parts));
     cfg.blockDim = dim3(kThreads);

@@ -19,7 +19,6 @@
 // device could save. Histogram and ownership use integer atomics, whose order
 // does not show. Only the copies touch the pool's bytes; they take the whole device.
 #include <algorithm>
-#include <atomic>
 #include <cooperative_groups.h>
 
 #include "ak_common.cuh"
@@ -352,23 +351,21 @@ void launch_copy(const BlocksCopyCall& c, int sm_count, cudaStream_t stream) {
 }
 
 // One cluster of as many blocks as the work keeps busy.
-ak_status launch(void (*kernel)(BlocksCall), std::atomic<uint64_t>& ready, const BlocksCall& c, int64_t work, cudaStream_t stream) {
+ak_status launch(void (*kernel)(BlocksCall), ClusterLimit& limit, const BlocksCall& c, int64_t work, cudaStream_t stream) {
     DeviceInfo dev;
     if (!current_device(&dev)) return AK_ERR_CUDA;
-    if (!(ready.load() >> dev.device & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return cuda_fail(e);
-        ready.fetch_or(1ull << dev.device);
-    }
-    unsigned size = 1;
-    while (size < 16 && work > (int64_t)size * kThreads) size *= 2;
+    int most = 0;
+    const ak_status s = limit.get(reinterpret_cast<const void*>(kernel), kThreads, dev.device, &most);
+    if (s != AK_OK) return s;
+    int size = 1;
+    while (size < most && work > (int64_t)size * kThreads) size *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(size);
+    cfg.gridDim = dim3((unsigned)size);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.x = (unsigned)size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -386,22 +383,22 @@ size_t blocks_fork_workspace(int64_t rows, int64_t blocks) {
 size_t blocks_compact_workspace(int64_t blocks) { return kWsHeader + align_up((size_t)(2 * (blocks / 2) + blocks) * 4, 256); }
 
 ak_status run_blocks_count(const BlocksCall& c, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready{0};
-    return bk::launch(bk::k_blocks_count, ready, c, std::max(c.rows * c.width, c.blocks), stream);
+    static ClusterLimit limit;
+    return bk::launch(bk::k_blocks_count, limit, c, std::max(c.rows * c.width, c.blocks), stream);
 }
 ak_status run_blocks_fork(BlocksCall c, void* ws, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready{0};
+    static ClusterLimit limit;
     c.work = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kWsHeader);
-    return bk::launch(bk::k_blocks_fork, ready, c, std::max(c.rows * c.width, c.blocks), stream);
+    return bk::launch(bk::k_blocks_fork, limit, c, std::max(c.rows * c.width, c.blocks), stream);
 }
 ak_status run_blocks_free(const BlocksCall& c, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready{0};
-    return bk::launch(bk::k_blocks_free, ready, c, c.blocks, stream);
+    static ClusterLimit limit;
+    return bk::launch(bk::k_blocks_free, limit, c, c.blocks, stream);
 }
 ak_status run_blocks_compact(BlocksCall c, void* ws, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready{0};
+    static ClusterLimit limit;
     c.work = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kWsHeader);
-    return bk::launch(bk::k_blocks_compact, ready, c, std::max(c.rows * c.width, c.blocks), stream);
+    return bk::launch(bk::k_blocks_compact, limit, c, std::max(c.rows * c.width, c.blocks), stream);
 }
 ak_status run_blocks_copy(const BlocksCopyCall& c, cudaStream_t stream) {
     DeviceInfo dev;

@@ -22,7 +22,7 @@ static bool word_ptr(const void* p, bool needed) { return p ? aligned(p, 4) : !n
 // ===========================================================================
 
 static ak_status check_shape(const ak_recurrence* a) {
-    if (!a || a->tokens < 0 || a->seqs < 0 || a->channels < 1 || a->tokens > kMost || a->seqs > kMost ||
+    if (!a || a->tokens < 0 || a->seqs < 0 || a->channels < 1 || a->tokens > kMost || a->seqs > kMostRows ||
         a->channels > kMostRows)
         return AK_ERR_INVALID_ARG;
     if (a->form != AK_RECURRENCE_DECAY && a->form != AK_RECURRENCE_GATE) return AK_ERR_INVALID_ARG;
@@ -121,7 +121,7 @@ extern "C" ak_status ak_gated_recurrence_step(const ak_recurrence* a, const ak_r
 
 extern "C" ak_status ak_beam_select(const void* logits, int64_t batch_stride, int64_t beam_stride, ak_dtype dtype,
                                     int64_t batch, int32_t beams, int64_t vocab, int32_t keep, const float* scores,
-                                    const uint8_t* done, const int32_t* lengths, int32_t end_token, float penalty,
+                                    const uint8_t* done, const int32_t* lengths, int32_t end_token, double penalty,
                                     float* out_scores, int32_t* out_tokens, int32_t* out_parents, uint8_t* out_done,
                                     int32_t* out_lengths, const ak_opts* opts, void* stream) {
     if (dtype < AK_F32 || dtype > AK_U8 || batch < 0 || batch > kMost / 16 || beams < 1 || beams > 32 || keep < 1 ||
@@ -218,7 +218,8 @@ extern "C" ak_status ak_blocks_fork(const int32_t* table, int64_t stride, int32_
         return AK_ERR_INVALID_ARG;
     if (!word_ptr(counts, true) || !word_ptr(refs, nblocks > 0) || !word_ptr(free_blocks, nfree > 0)) return AK_ERR_INVALID_ARG;
     if (nnew > 0 && (!word_ptr(parents, true) || !word_ptr(out_lens, true) || !word_ptr(pairs, true) ||
-                     (width > 0 && (!word_ptr(out_table, true) || out_table == table || (nnew > 1 && out_stride < width)))))
+                     (width > 0 && (!word_ptr(out_table, true) || out_table == table || (nnew > 1 && out_stride < width))) ||
+                     (nreq > 0 && out_lens == lens)))
         return AK_ERR_INVALID_ARG;
     if (!good_workspace(ws, ws_bytes, blocks_fork_workspace(nnew, nblocks))) return AK_ERR_WORKSPACE;
     BlocksCall c = table_call(table, stride, width, lens, nreq, block_size, nblocks);

@@ -59,7 +59,8 @@ def ak_beam_select(logits: torch.Tensor, scores: torch.Tensor, *, done: torch.Te
     [requests, beams] the best ``keep`` (default: as many as there are beams)
     continuations by total over length**``length_penalty``, ties by the lowest beam, then
     token. Beams that are ``done`` (bool) go on as they are, by ``end_token``. ``lengths``
-    (int32) are the beams' tokens so far. ``out`` reuses an earlier step's tensors. It has no gradient."""
+    (int32) are the beams' tokens so far. ``out`` reuses an earlier step's tensors, which may be this
+    step's inputs. It has no gradient."""
     if logits.dim() != 3:
         raise ValueError("logits are [requests, beams, vocab]")
     n, k, vocab = logits.shape

@@ -20,9 +20,10 @@ def _check(logits, scores, done=None, lengths=None, end=-1, penalty=0.0, keep=No
     got = r.scores.double().cpu().numpy()
     fine = np.isfinite(s)
     assert (fine == np.isfinite(got)).all() and (got[~fine] == -np.inf).all()
+    got, s = got[fine], s[fine]
     # the stored float32's half step; exponentials off by 2^-21 in all (2 ulp of ex2 and its rounded argument, below 8 where
     # a term still weighs) give a logarithm off by as much
-    assert (np.abs(got - s)[fine] <= 2.0**-24 * np.abs(s[fine]) + 2.0**-20).all()
+    assert (np.abs(got - s) <= 2.0**-24 * np.abs(s) + 2.0**-20).all()
     return r
 
 
@@ -111,8 +112,7 @@ def test_banned_tokens_and_lost_rows():
     # the type's lowest value is a value
     logits = torch.full((1, 2, 40), torch.finfo(torch.float32).min, device="cuda")
     logits[0, 1, 20] = 0.0
-    r = _check(logits, torch.zeros(1, 2, device="cuda"))
-    assert r.parents.tolist() == [[1, 0]] or r.parents.tolist() == [[0, 0]] or r.parents.tolist() == [[1, 0]]
+    _check(logits, torch.zeros(1, 2, device="cuda"))
     # large logits: their differences count
     logits = torch.full((1, 3, 50), 3e38, device="cuda")
     logits[0, :, 7] = 3.1e38
@@ -127,6 +127,28 @@ def test_views():
     a = _check(logits, scores)
     b = ak.ak_beam_select(logits.contiguous(), scores, out=a)
     assert b.tokens.data_ptr() == a.tokens.data_ptr()
+
+
+def test_a_step_in_its_own_tensors():
+    """An earlier step's tensors are inputs and outputs at once."""
+    n, k, v = 40, 5, 700
+    logits, scores = _random(n, k, v, torch.float32, 3)
+    a = ak.ak_beam_select(logits, scores, end_token=7, length_penalty=0.7)
+    for seed in range(3):
+        logits = _random(n, k, v, torch.float32, 50 + seed)[0]
+        logits[:, :, 7] += 6
+        want = ak.ak_beam_select(logits, a.scores, done=a.done, lengths=a.lengths, end_token=7, length_penalty=0.7)
+        b = ak.ak_beam_select(logits, a.scores, done=a.done, lengths=a.lengths, end_token=7, length_penalty=0.7, out=a)
+        assert b.scores.data_ptr() == a.scores.data_ptr() and all(torch.equal(x, y) for x, y in zip(b, want))
+    assert a.done.any() and not a.done.all()
+
+
+def test_ranks_that_tie_after_the_division():
+    """-49 over 49 tokens and -50 over 50 are one rank: the lowest beam. Reciprocals would tell them apart."""
+    m = torch.tensor([[50, 49, 7]], dtype=torch.int32, device="cuda")
+    r = ak.ak_beam_select(torch.zeros(1, 3, 9, device="cuda"), -m.float(), done=torch.ones(1, 3, dtype=torch.bool, device="cuda"),
+                          lengths=m, end_token=1, length_penalty=1.0)
+    assert r.parents.tolist() == [[0, 1, 2]] and r.lengths.tolist() == m.tolist() and r.tokens.tolist() == [[1, 1, 1]]
 
 
 def test_captured_and_replayed():

@@ -113,7 +113,7 @@ def test_block_refusals(L):
         return L.ak_blocks_fork(*dict(good_f, **kw).values(), None, None)
 
     refuse(fork, bad_table + (dict(p=None), dict(nn=-1), dict(nn=1 << 40), dict(f=None), dict(nf=-1), dict(b=-1), dict(nb=-1), dict(ot=None),
-                              dict(ot=0x1000), dict(os=7), dict(ol=None), dict(r=None), dict(pr=None), dict(c=None), dict(c=0x7001)))
+                              dict(ot=0x1000), dict(os=7), dict(ol=None), dict(ol=0x2000), dict(r=None), dict(pr=None), dict(c=None), dict(c=0x7001)))
     assert fork(ws=None) == WS and fork(wb=64) == WS and fork(ws=0x8004) == WS
     assert L.ak_blocks_free(None, 5, 0x1000, 0x2000, None, None) == INV
     assert L.ak_blocks_free(0x1000, -1, 0x1000, 0x2000, None, None) == INV
