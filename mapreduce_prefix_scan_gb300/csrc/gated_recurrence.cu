@@ -436,10 +436,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_recurrence(const Recurrenc
     auto state_of = [&](const float* states, int64_t seq) { return states && some ? states[seq * c.channels + ch] : 0.0f; };
     // ---- the run's map. A token that begins a sequence takes its state, and its
     // factor is 0: it forgets what was before, which is dropped as well, as it may
-    // not be finite. Such tokens are rare; only the chains, a few dozen
-    // instructions each, exist with and without them. (Larger paths of their own
-    // wait for their instructions, 200 cycles a token; a branch for every token
-    // keeps them from overlapping.)
+    // not be finite. Such tokens are rare, but some tile of a step often has one, and
+    // code for them that is unrolled over the run evicts the rest from the
+    // instruction cache (2000 cycles a step). So they are taken one at a time in
+    // rolled loops, and only the chains, two or three instructions a token, exist
+    // with and without them. (A branch for every token would keep tokens from
+    // overlapping.)
     auto fold_run = [&](const Marks<R>& mk, const In& t, int64_t t0) {
         const uint32_t first = mk.first[ty];
         [[maybe_unused]] const uint32_t last = mk.last[ty];
@@ -480,35 +482,45 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_recurrence(const Recurrenc
                     z[r] = (h - z[r]) * ((a[r] + one) * b[r]);
                 }
             };
-            if (last) {
+            if (kRows) {
+#pragma unroll 1
+                for (uint32_t m = last; m; m &= m - 1) {  // the sequences' first tokens
+                    const int at = __ffs(m) - 1;
+                    const float s0 = state_of(c.state_in, walk.b.seq(mk.seq_last[ty * R + at]));
+#pragma unroll
+                    for (int r = 0; r < R; ++r) z[r] = r == at ? s0 : z[r];
+                }
+            } else if (last) {
 #pragma unroll
                 for (int r = R - 1; r >= 0; --r) {
-                    if (last & 1u << r) {  // the sequence's first token
-                        hh = state_of(c.state_in, walk.b.seq(mk.seq_last[ty * R + r]));
-                        if (kRows) z[r] = hh;
-                    }
+                    if (last & 1u << r) hh = state_of(c.state_in, walk.b.seq(mk.seq_last[ty * R + r]));
                     again(r);
                 }
-            } else if constexpr (kAgain) {
+            } else {
 #pragma unroll
                 for (int r = R - 1; r >= 0; --r) again(r);
             }
         }
         float fold = 0.0f;
         auto add = [&](int r) { fold = REV ? times(r, u[r] + fold) : step(r, fold); };
+#pragma unroll 1
+        for (uint32_t m = first; m; m &= m - 1) {
+            const int at = __ffs(m) - 1;
+            const float s0 = state_of(first_state, walk.b.seq(mk.seq_first[ty * R + at]));
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (REV) {
+                    u[r] = r == at ? u[r] + s0 : u[r];
+                } else {
+                    u[r] = r == at && first_state ? step(r, s0) : u[r];
+                    a[r] = r == at ? 0.0f - one : a[r];
+                }
+            }
+        }
         if (first) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (first & 1u << r) {
-                    const float s0 = state_of(first_state, walk.b.seq(mk.seq_first[ty * R + r]));
-                    fold = 0.0f;
-                    if (REV) {
-                        u[r] += s0;
-                    } else {
-                        if (first_state) u[r] = step(r, s0);
-                        a[r] = 0.0f;
-                    }
-                }
+                fold = first & 1u << r ? 0.0f : fold;
                 add(r);
             }
         } else {
@@ -541,11 +553,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_recurrence(const Recurrenc
 #pragma unroll
             for (int r = 0; r < R; ++r) move(r);
         }
-        if (last && last_state) {
+        if (last_state && some) {
+#pragma unroll 1
+            for (uint32_t m = last; m; m &= m - 1) {
+                const int at = __ffs(m) - 1;
+                float v = 0.0f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if ((last & 1u << r) && some)
-                    last_state[walk.b.seq(mk.seq_last[ty * R + r]) * c.channels + ch] = REV ? times(r, u[r]) : u[r];
+                for (int r = 0; r < R; ++r) v = r == at ? (REV ? times(r, u[r]) : u[r]) : v;
+                last_state[walk.b.seq(mk.seq_last[ty * R + at]) * c.channels + ch] = v;
             }
         }
         T *po = out + row_of(v0) * out_stride, *pg = out_g + row_of(v0) * c.dgate.token_stride;
