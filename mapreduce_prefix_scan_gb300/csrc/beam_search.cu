@@ -30,6 +30,14 @@
 // beams' sums. Sums of exponentials are float32 with a running compensation,
 // the logarithm, the totals and the ranks are 64-bit (a few for each row: the
 // device adds 64-bit numbers 64 times slower than 32-bit ones).
+//
+// Bound by HBM and the exponentials while rows are folded (0.78 of the copy
+// bandwidth with four rows an SM) and by a chain of latencies after them (about 10 us:
+// the block's sort, the candidates' loads, the cluster's exchange, the logarithms,
+// the ranks, the merge). Back to back: 64 x 8 rows of 128000 bf16 44 to 46 us, 32 x 8
+// float32 35 us (0.55), 4 rows of 32003 float32 11.4 us. Blocks of 128 threads: 52, 53
+// and 13 us; rows in twice as many slices: 58, 35 and 12.
+// The reordering of 8 x 64 x 8 states of 2048 float32 takes 6.9 us.
 #include <algorithm>
 #include <cooperative_groups.h>
 
