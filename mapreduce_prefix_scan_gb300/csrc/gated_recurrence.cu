@@ -39,8 +39,8 @@
 // not by its loads. Back to back: 16384 x 4096 bf16 95 us (0.63 of the copy
 // bandwidth), gradients of 8192 x 4096 bf16 93 us (0.53), 8192 x 4096 float32 77 to
 // 79 us (0.76), 32771 x 640 float32 65 us (0.57) and its gradients 102 us, 331 x 1000
-// in 64 sequences 6.6 us. Rows at odd addresses, 16384 x 1001: 86 us bf16, 103 float32
-// (32768 x 1024 bf16, aligned: 54). Steps: 256 x 4096 bf16 3.5 us (0.62), one request 2.2 us.
+// in 64 sequences 6.6 us. Rows at odd addresses, 16384 x 1001: 38 us bf16, 63 float32
+// (by 4-byte words 86 and 103). Steps: 256 x 4096 bf16 3.5 us (0.62), one request 2.2 us.
 // Tried: 64 channels a cluster, two a thread (32771 x 640 float32: 96 us, and 60 so;
 // 32768 x 2048 bf16 102 and 94; but 16384 x 4096 bf16 90 and 95); half the tile and
 // three blocks an SM (115, and 105 at the time); tiles in registers, loaded one step
@@ -70,11 +70,6 @@ constexpr int kStages = 2;                    // tiles on their way
 __device__ __forceinline__ void copy16(void* to, const void* from, int size) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
                      static_cast<uint32_t>(__cvta_generic_to_shared(to))),
-                 "l"(from), "r"(size)
-                 : "memory");
-}
-__device__ __forceinline__ void copy4(void* to, const void* from, int size) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))),
                  "l"(from), "r"(size)
                  : "memory");
 }
@@ -297,11 +292,11 @@ struct Walk {
 
 // Inputs of a tile: the gate, what is scanned (x, or dh), and for gradients
 // h_{t-1} of each token (decay), or x and the state before each run (gate).
-// Rows that do not begin at multiples of 16 bytes are copied by 4-byte words; of
-// bf16 ones that may be from the value before a row on, one word more.
+// Of rows that do not begin at multiples of 16 bytes the pieces of 16 that they lie
+// in are copied, so a row begins up to 14 bytes into its place.
 template <class T, int R, bool REV, bool AGAIN, bool WIDE>
 struct Tile {
-    static constexpr int kPitch = WIDE || sizeof(T) == 4 ? kCh : kCh + 2;
+    static constexpr int kPitch = WIDE ? kCh : kCh + 16 / (int)sizeof(T);
     T g[kTy * R * kPitch], u[kTy * R * kPitch], z[REV ? kTy * R * kPitch : 8], before[AGAIN ? kTy * kPitch : 8];
 };
 
@@ -365,23 +360,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_recurrence(const Recurrenc
                 p += way * ((kThreads / kRow) * apart);
             }
         } else {
-            // a row a warp, a 4-byte word a lane; a bf16 row that begins inside a word
-            // is taken from the word's other value on (which is of the same
-            // allocation: those begin at words), and ends with half a word
-            const int64_t n = min((int64_t)kCh, c.channels - c0);
-            const char* none = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(from.data) & ~(uintptr_t)3);
-            int64_t v = v0 + (int64_t)ty * apart;
+            // the aligned pieces of 16 bytes that the row lies in, from the first one's
+            // beginning (which is of the same allocation: those begin at such pieces)
+            constexpr int kPer = 16 / (int)sizeof(T), kRow = 2 * kCh / kPer, kUsed = kCh / kPer + 1;
+            const int piece = tid % kRow;
+            const int64_t n = min((int64_t)kCh, c.channels - c0) * (int64_t)sizeof(T);
+            const char* none = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(from.data) & ~(uintptr_t)15);
+            int64_t v = v0 + (int64_t)(tid / kRow) * apart;
             const T* p = base + (row_of(v) + shift) * from.token_stride;
-            for (int r = ty; r < rows; r += kTy) {
+#pragma unroll
+            for (int r = 0; r < rows; r += kThreads / kRow) {
                 const char* row = reinterpret_cast<const char*>(p);
-                const int64_t odd = reinterpret_cast<uintptr_t>(row) & 3;
-                const int64_t bytes = v < end ? n * (int64_t)sizeof(T) + odd : 0;
-                for (int w = lane; w < kPitch * (int)sizeof(T) / 4; w += kWarp) {
-                    const int size = (int)max((int64_t)0, min((int64_t)4, bytes - 4 * w));
-                    copy4(reinterpret_cast<char*>(to + r * kPitch) + 4 * w, size ? row - odd + 4 * w : none, size);
-                }
-                v += kTy * apart;
-                p += way * (kTy * apart);
+                const int64_t lead = reinterpret_cast<uintptr_t>(row) & 15;
+                const int size = v < end ? (int)max((int64_t)0, min((int64_t)16, n + lead - 16 * piece)) : 0;
+                if (piece < kUsed && r + tid / kRow < rows)
+                    copy16(to + (r + tid / kRow) * kPitch + piece * kPer, size ? row - lead + 16 * piece : none, size);
+                v += (kThreads / kRow) * apart;
+                p += way * ((kThreads / kRow) * apart);
             }
         }
     };
@@ -403,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_recurrence(const Recurrenc
     // value of this thread's channel in row r of a copied array whose row 0 is virtual token v0
     auto value = [&](const T* rows, const ak_rows& from, int r, int apart, int64_t v0, int shift) {
         int at = lane;
-        if constexpr (!WIDE && sizeof(T) == 2) {
-            const uint32_t first = (uint32_t)(reinterpret_cast<uintptr_t>(from.data) >> 1) + (uint32_t)c0;
+        if constexpr (!WIDE) {
+            const uint32_t first = (uint32_t)(reinterpret_cast<uintptr_t>(from.data) / sizeof(T)) + (uint32_t)c0;
             const uint32_t row = (uint32_t)row_of(v0) + (uint32_t)shift + (uint32_t)((REV ? -1 : 1) * r * apart);
-            at += (first + row * (uint32_t)from.token_stride) & 1;
+            at += (first + row * (uint32_t)from.token_stride) & (16 / sizeof(T) - 1);
         }
         return as_float(rows[r * kPitch + at]);
     };
