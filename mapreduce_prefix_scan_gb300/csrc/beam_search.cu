@@ -13,7 +13,7 @@
 // answer is among them. A cluster of blocks takes a request, a block a row
 // or a slice of one at a time:
 //  - pass: each thread folds its columns (16 bytes of them, then those kThreads
-//    times as far on, four such groups in flight) to a maximum, its column and a
+//    times as far on, three or four such groups in flight) to a maximum, its column and a
 //    sum of exponentials; no list is kept beside it, so an element costs a
 //    conversion, a maximum, an exponential and three halves of packed pairs;
 //  - the `keep`-th best of the threads' maxima is a bound below which nothing
@@ -34,9 +34,10 @@
 // Bound by HBM and the exponentials while rows are folded (0.78 of the copy
 // bandwidth with four rows an SM) and by a chain of latencies after them (about 10 us:
 // the block's sort, the candidates' loads, the cluster's exchange, the logarithms,
-// the ranks, the merge). Back to back: 64 x 8 rows of 128000 bf16 44 to 46 us, 32 x 8
-// float32 35 us (0.55), 4 rows of 32003 float32 11.4 us. Blocks of 128 threads: 52, 53
-// and 13 us; rows in twice as many slices: 58, 35 and 12.
+// the ranks, the merge). Back to back: 64 x 8 rows of 128000 bf16 42 to 46 us, 32 x 8
+// float32 35 us (0.55), 4 rows of 32003 float32 11.2 us. Blocks of 128 threads: 52, 53
+// and 13 us, of 512: 51, 34 and 12; rows in twice as many slices: 58, 35 and 12; three
+// blocks an SM with eight groups in flight: 87, 37 and 11.
 // The reordering of 8 x 64 x 8 states of 2048 float32 takes 6.9 us.
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -52,7 +53,6 @@ namespace bs {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kMaxBeams = 32;     // of a request, before and after: a list is a warp
-constexpr int kAhead = 4;         // groups of 16 bytes that a thread has in flight
 constexpr int kFound = kThreads * 4;  // candidates held at a time
 
 // Orders floats as unsigned integers; -0 and 0 are one value.
@@ -224,6 +224,7 @@ template <class T>
 __device__ void fold_row(const T* row, uint32_t first, uint32_t last, int keep, Shared& s, Share* out, bool& waited) {
     constexpr int G = Group<T>::kSize;
     constexpr uint64_t kStep = (uint64_t)kThreads * G;
+    constexpr int kAhead = sizeof(T) == 2 ? 3 : 4;  // groups in flight: the registers that four blocks an SM leave
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
     const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
     float top = -INFINITY, ref = 0.0f, sum = 0.0f, lost = 0.0f;
