@@ -53,7 +53,8 @@ namespace bs {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kMaxBeams = 32;     // of a request, before and after: a list is a warp
-constexpr int kFound = kThreads * 4;  // candidates held at a time
+// candidates held at a time: all of a group (16 bytes, 8 bf16) a thread, which may be candidates every one
+constexpr int kFound = kThreads * 8;
 
 // Orders floats as unsigned integers; -0 and 0 are one value.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -299,7 +300,10 @@ __device__ void fold_row(const T* row, uint32_t first, uint32_t last, int keep, 
     if (mine && mine >= bound) s.chosen[atomicAdd(&s.nchosen, 1)] = tid;
     __syncthreads();
     // ---- the chosen threads' columns again, 16 of them a thread at a time; where
-    // more are candidates than there is room for, a group
+    // more are candidates than there is room for, a group, for which there always is
+    // (how many lie in few threads is the logits' affair: the bound leaves out
+    // threads, not columns)
+    static_assert(kThreads * G <= kFound, "a group of every thread has to fit");
     constexpr int kSome = 16 / G;
     const int chosen = s.nchosen;
     const uint32_t groups = (last - first + G - 1) / G, per = (groups + kThreads - 1) / kThreads;  // of a thread, at most
