@@ -124,7 +124,7 @@ __device__ __forceinline__ void warp_take(K& list, K v, int lane) {
 }
 
 // Warp 0's list becomes the best 32 of the first `warps` warps' lists (a power of
-// two). Ends in sync.
+// two). Ends in the block's sync, but for one warp: that has nothing to wait for here.
 template <class K>
 __device__ __forceinline__ void block_merge(K& list, K (*s_lists)[kWarp], int lane, int warp, int warps = kWarps) {
     for (int half = warps / 2; half > 0; half >>= 1) {
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
     int warps = 1;
     while (warps < kWarps && warps < n) warps *= 2;
     block_merge(list, s.picks, lane, warp, warps);
+    __syncwarp();  // (one beam: the block has not met, and lanes read below what others wrote to s.totals, s.tokens)
     if (warp == 0 && lane < keep) {
         const int64_t o = r * keep + lane;
         int token = -1, parent = -1, length = 0;
