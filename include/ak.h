@@ -592,7 +592,7 @@ ak_status ak_linear_attention_step(const ak_linattn* shape, const ak_heads* q, c
  * ak_gated_recurrence_step: one token for each of `tokens` requests (seqs and
  * offsets unused), the state updated in place. Request b uses row slots[b] of
  * nslots in `state` (slots NULL: b). An index outside [0, nslots) marks padding: its
- * output is 0. Indices must not repeat.
+ * output is 0. Indices must not repeat. An infinite state is what a h + b x makes of it.
  *
  * opts->check also reports a bounded device-side wait that ran out
  * (AK_ERR_TIMEOUT; the results are then undefined). The waits are for the maps of

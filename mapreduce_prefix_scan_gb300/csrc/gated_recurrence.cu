@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kThreads) k_step(const RecurrenceCall c, float
         for (int q = 0; q < kStepVec; ++q) {
             float a, b;
             weights<float, FORM>(g[q], a, b);  // (states are float32)
-            const bool near = a > 0.5f;
+            const bool near = a > 0.5f && fabsf(h[q]) < INFINITY;  // ((a - 1) h + h of an infinity is none)
             const float less = FORM == AK_RECURRENCE_GATE ? -b : less_one(g[q], a), in = FORM == AK_RECURRENCE_GATE ? b * x[q] : x[q];
             h[q] = fmaf(near ? less : a, h[q], in) + (near ? h[q] : 0.0f);
         }
