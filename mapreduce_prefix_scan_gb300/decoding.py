@@ -61,6 +61,11 @@ def ak_beam_select(logits: torch.Tensor, scores: torch.Tensor, *, done: torch.Te
     token. Beams that are ``done`` (bool) go on as they are, by ``end_token``. ``lengths``
     (int32) are the beams' tokens so far. ``out`` reuses an earlier step's tensors, which may be this
     step's inputs. It has no gradient."""
+    if (logits.requires_grad or scores.requires_grad) and torch.is_grad_enabled():
+        with torch.no_grad():
+            step = ak_beam_select(logits, scores, done=done, lengths=lengths, end_token=end_token, length_penalty=length_penalty,
+                                  keep=keep, out=out, opts=opts, stream=stream)
+        return BeamStep(*_s._Untracked.apply(step, "ak_beam_select has no gradient", logits, scores))
     if logits.dim() != 3:
         raise ValueError("logits are [requests, beams, vocab]")
     n, k, vocab = logits.shape
