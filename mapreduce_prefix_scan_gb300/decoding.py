@@ -47,6 +47,13 @@ def _shaped(t, shape, dtype, name, on):
     return None if t is None else _given(t, shape, dtype, name, on, None, None).data_ptr()
 
 
+def _int32(v, name):
+    """A number that the entry point takes as an int32: ctypes would hand over its low bits."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name}: {v} is out of range")
+    return v
+
+
 # ---------------------------------------------------------------------------
 # beam search
 # ---------------------------------------------------------------------------
@@ -73,7 +80,8 @@ def ak_beam_select(logits: torch.Tensor, scores: torch.Tensor, *, done: torch.Te
     kind = _s._FLOAT.get(dt)
     if kind is None or on < 0 or not _s._dense_rows(logits):
         raise ValueError("logits: a float32 or bfloat16 CUDA tensor with contiguous rows is needed")
-    m = k if keep is None else int(keep)
+    m = k if keep is None else _int32(int(keep), "keep")
+    _int32(end_token, "end_token")
     if out is None:  # (allocations are half of a small call's time, views of a larger one more)
         e, shape, i32 = _s._empty, (n, m), torch.int32
         step = BeamStep(e(shape, torch.float32, dev, stream), e(shape, i32, dev, stream), e(shape, i32, dev, stream),
@@ -147,8 +155,9 @@ def ak_beam_reorder(state: torch.Tensor, parents: torch.Tensor, *, dim: int = 0,
 # blocks of a paged cache
 # ---------------------------------------------------------------------------
 
-def _table(block_table, lens, on):
+def _table(block_table, lens, block_size, on):
     """Arguments of a block table and its requests' lengths."""
+    _int32(block_size, "block_size")
     if not (block_table.dim() == 2 and block_table.dtype is torch.int32 and block_table.get_device() == on >= 0 and
             _s._dense_rows(block_table)):
         raise ValueError("block_table: a [requests, width] int32 tensor with contiguous rows on the call's CUDA device is needed")
@@ -161,7 +170,7 @@ def ak_blocks_count(block_table: torch.Tensor, lens: torch.Tensor, *, block_size
     """How many requests hold each of the pool's ``blocks`` ([blocks] int32): the
     first ceil(len / block_size) entries of each request's row of ``block_table``."""
     on = block_table.get_device()
-    a = _table(block_table, lens, on)
+    a = _table(block_table, lens, block_size, on)
     if out is None:
         refs = _s._empty(blocks, torch.int32, block_table.device, stream)
     else:
@@ -180,7 +189,7 @@ def ak_blocks_fork(block_table: torch.Tensor, lens: torch.Tensor, parents: torch
     ``pairs`` lists what ak_blocks_copy has to copy. ``refs`` are the counts of the result.
     ``out`` reuses an earlier fork's tensors, not those of the input."""
     on, dev = block_table.get_device(), block_table.device
-    a = _table(block_table, lens, on)
+    a = _table(block_table, lens, block_size, on)
     n, nfree = parents.numel(), free_blocks.numel()
     p, fb = _s._flat(parents, torch.int32, n, "parents", on), _s._flat(free_blocks, torch.int32, nfree, "free_blocks", on)
     width = block_table.shape[1]
@@ -223,7 +232,7 @@ def ak_blocks_compact(block_table: torch.Tensor, lens: torch.Tensor, refs: torch
     ``block_table``), the (from, to) that ak_blocks_copy has to copy, then (-1, -1), and [moves, blocks in
     use]."""
     on, dev = block_table.get_device(), block_table.device
-    a = _table(block_table, lens, on)
+    a = _table(block_table, lens, block_size, on)
     blocks = refs.numel()
     rp = _s._flat(refs, torch.int32, blocks, "refs", on)
     if out is block_table:

@@ -29,3 +29,18 @@ def test_a_beam_step_does_not_pass_for_differentiable(host, asks, given):  # noq
     with torch.no_grad():
         assert not ak.ak_beam_select(**tensors).scores.requires_grad
     assert not ak.ak_beam_select(**{n: t.detach() for n, t in tensors.items()}).scores.requires_grad
+
+
+@pytest.mark.parametrize("call,name,value", [("ak_beam_select", "end_token", 3), ("ak_beam_select", "keep", 2), ("ak_blocks_count", "block_size", 4),
+                                             ("ak_blocks_fork", "block_size", 4), ("ak_blocks_compact", "block_size", 4)])
+def test_numbers_past_32_bits_are_refused(host, call, name, value):  # noqa: F811
+    """ctypes hands over their low bits: 2^32 + 4 tokens a block would pass for 4."""
+    library = host(_Library())
+    tensors, rest = _calls()[call]
+    tensors = {n: _cuda(t) for n, t in tensors.items()}
+    getattr(ak, call)(**tensors, **dict(rest, **{name: value}))
+    assert library.calls.pop(call)
+    for far in (1 << 32, -(1 << 32), 1 << 63):
+        with pytest.raises(ValueError, match=name):
+            getattr(ak, call)(**tensors, **dict(rest, **{name: value + far}))
+    assert not library.calls
