@@ -67,6 +67,8 @@ extern "C" ak_status ak_gated_recurrence(const ak_recurrence* a, const ak_rows* 
     const ak_status s = check_shape(a);
     if (s != AK_OK) return s;
     if (!good(a, x, false) || !good(a, gate, false) || !good(a, h, true)) return AK_ERR_INVALID_ARG;
+    // in place the rows lie where they lay: others would be written before they are read
+    if (a->tokens > 1 && h->data == x->data && h->token_stride != x->token_stride) return AK_ERR_INVALID_ARG;
     if (!word_ptr(offsets, a->seqs != 1) || !word_ptr(state_in, false) || !word_ptr(state_out, false))
         return AK_ERR_INVALID_ARG;
     if (a->tokens == 0 && (a->seqs == 0 || !state_out)) return AK_OK;
