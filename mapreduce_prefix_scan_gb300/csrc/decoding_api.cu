@@ -135,6 +135,9 @@ extern "C" ak_status ak_beam_select(const void* logits, int64_t batch_stride, in
     if (!word_ptr(scores, true) || !word_ptr(lengths, false) || !word_ptr(out_scores, true) || !word_ptr(out_tokens, true) ||
         !word_ptr(out_parents, true) || !word_ptr(out_lengths, false))
         return AK_ERR_INVALID_ARG;
+    // one request's outputs would lie in another's inputs, which are read at another time
+    if (batch > 1 && keep != beams && (out_scores == scores || (done && out_done == done) || (lengths && out_lengths == lengths)))
+        return AK_ERR_INVALID_ARG;
     BeamCall c = {};
     c.logits = logits, c.batch_stride = batch_stride, c.beam_stride = beam_stride, c.dtype = dtype;
     c.batch = batch, c.vocab = vocab, c.beams = beams, c.keep = keep, c.end = end_token, c.penalty = penalty;
