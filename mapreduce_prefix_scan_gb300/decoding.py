@@ -94,6 +94,8 @@ def ak_beam_select(logits: torch.Tensor, scores: torch.Tensor, *, done: torch.Te
         logits.data_ptr(), ls[0], ls[1], kind, n, k, vocab, m, _shaped(scores, (n, k), torch.float32, "scores", on),
         _shaped(done, (n, k), torch.bool, "done", on), _shaped(lengths, (n, k), torch.int32, "lengths", on), end_token,
         length_penalty, *(t.data_ptr() for t in step), _s._opts(opts), _s._stream_of(stream, logits)), "ak_beam_select")
+    if out is not None:
+        _s._written(*step)
     return step
 
 
@@ -148,6 +150,7 @@ def ak_beam_reorder(state: torch.Tensor, parents: torch.Tensor, *, dim: int = 0,
     _s._check(_abi.load().ak_beam_reorder(state.data_ptr(), outer, outer_stride, n, state.stride(dim) * e, k,
                                           state.stride(dim + 1) * e, inner, p, _s._opts(opts),
                                           _s._stream_of(stream, state)), "ak_beam_reorder")
+    _s._written(state)
     return state
 
 
@@ -177,6 +180,7 @@ def ak_blocks_count(block_table: torch.Tensor, lens: torch.Tensor, *, block_size
         refs = _given(out, (blocks,), torch.int32, "out", on, None, None)
     _s._check(_abi.load().ak_blocks_count(*a, block_size, blocks, refs.data_ptr(), _s._opts(opts),
                                           _s._stream_of(stream, block_table)), "ak_blocks_count")
+    _s._written(out)
     return refs
 
 
@@ -207,6 +211,8 @@ def ak_blocks_fork(block_table: torch.Tensor, lens: torch.Tensor, parents: torch
     _s._check(L.ak_blocks_fork(*a, p, n, fb, nfree, block_size, blocks, f.table.data_ptr(), width, f.lens.data_ptr(),
                                f.refs.data_ptr(), f.pairs.data_ptr(), f.counts.data_ptr(), wp, wb, _s._opts(opts),
                                _s._stream_of(stream, block_table)), "ak_blocks_fork")
+    if out is not None:
+        _s._written(*f)
     return f
 
 
@@ -216,11 +222,12 @@ def ak_blocks_free(refs: torch.Tensor, *, out: torch.Tensor | None = None, count
     order, then -1 ([blocks] int32), and how many they are ([1] int32)."""
     on, n = refs.get_device(), refs.numel()
     p = _s._flat(refs, torch.int32, n, "refs", on)
-    dev = refs.device
+    dev, given = refs.device, (out, counts)
     free = _s._empty(n, torch.int32, dev, stream) if out is None else _given(out, (n,), torch.int32, "out", on, dev, stream)
     counts = _s._empty(1, torch.int32, dev, stream) if counts is None else _given(counts, (1,), torch.int32, "counts", on, dev, stream)
     _s._check(_abi.load().ak_blocks_free(p, n, free.data_ptr(), counts.data_ptr(), _s._opts(opts), _s._stream_of(stream, refs)),
               "ak_blocks_free")
+    _s._written(*given)
     return free, counts
 
 
@@ -231,7 +238,7 @@ def ak_blocks_compact(block_table: torch.Tensor, lens: torch.Tensor, refs: torch
     ``(table, pairs, counts)``, the table with its blocks renamed (``out`` may be
     ``block_table``), the (from, to) that ak_blocks_copy has to copy, then (-1, -1), and [moves, blocks in
     use]."""
-    on, dev = block_table.get_device(), block_table.device
+    on, dev, given = block_table.get_device(), block_table.device, (out, pairs, counts)
     a = _table(block_table, lens, block_size, on)
     blocks = refs.numel()
     rp = _s._flat(refs, torch.int32, blocks, "refs", on)
@@ -247,6 +254,7 @@ def ak_blocks_compact(block_table: torch.Tensor, lens: torch.Tensor, refs: torch
     wp, wb, _keep = _s._workspace_ptr(b.value, dev, workspace, stream, on)
     _s._check(L.ak_blocks_compact(*a, rp, block_size, blocks, table.data_ptr(), stride, pairs.data_ptr(), counts.data_ptr(),
                                   wp, wb, _s._opts(opts), _s._stream_of(stream, block_table)), "ak_blocks_compact")
+    _s._written(*given)
     return table, pairs, counts
 
 
@@ -271,4 +279,5 @@ def ak_blocks_copy(cache: torch.Tensor, pairs: torch.Tensor, *, counts: torch.Te
     inner = _inner(cache, dim + 1, "cache") if cache.dim() > dim + 1 else e
     _s._check(_abi.load().ak_blocks_copy(cache.data_ptr(), outer, outer_stride, cache.shape[dim], cache.stride(dim) * e, inner, p,
                                          n, c, _s._opts(opts), _s._stream_of(stream, cache)), "ak_blocks_copy")
+    _s._written(cache)
     return cache

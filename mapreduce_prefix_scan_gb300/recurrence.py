@@ -96,6 +96,7 @@ def ak_gated_recurrence(x: torch.Tensor, gate: torch.Tensor, *, form: str = "dec
         return _s._Untracked.apply(results, "ak_gated_recurrence into given memory or on a given stream is not recorded: "
                                    "no gradient", x, gate, state)
     a, ss, off, on = _geometry(x, offsets, form)
+    given = out, state_out
     if out is None:
         out = _s._empty(x.shape, x.dtype, x.device, stream)
     if state_out is None and final_state:
@@ -105,6 +106,7 @@ def ak_gated_recurrence(x: torch.Tensor, gate: torch.Tensor, *, form: str = "dec
     _s._check(_abi.load().ak_gated_recurrence(a, rx, rg, off, _state(state, ss, "state", on), ro,
                                               _state(state_out, ss, "state_out", on), _s._opts(opts),
                                               _s._stream_of(stream, x)), "ak_gated_recurrence")
+    _s._written(*given)
     return out, state_out
 
 
@@ -118,6 +120,7 @@ def ak_gated_recurrence_backward(dh: torch.Tensor, x: torch.Tensor, gate: torch.
     ``dstate_out`` (or None). Returns ``(dx, dgate, dstate)``; ``dstate`` is None
     where the forward call had no ``state`` and none is given."""
     a, ss, off, on = _geometry(x, offsets, form)
+    given = dx, dgate, dstate
     dx = _s._empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
     dgate = _s._empty(x.shape, x.dtype, x.device, stream) if dgate is None else dgate
     if dstate is None and state is not None:
@@ -128,6 +131,7 @@ def ak_gated_recurrence_backward(dh: torch.Tensor, x: torch.Tensor, gate: torch.
     _s._check(_abi.load().ak_gated_recurrence_backward(
         a, rd, rx, rg, rh, off, _state(state, ss, "state", on), _state(dstate_out, ss, "dstate_out", on), rdx, rdg,
         _state(dstate, ss, "dstate", on), _s._opts(opts), _s._stream_of(stream, x)), "ak_gated_recurrence_backward")
+    _s._written(*given)
     return dx, dgate, dstate
 
 
@@ -143,6 +147,7 @@ def ak_gated_recurrence_step(x: torch.Tensor, gate: torch.Tensor, state: torch.T
             out = ak_gated_recurrence_step(x, gate, state, form=form, slots=slots, out=out, opts=opts, stream=stream)
         return _s._Untracked.apply((out,), "ak_gated_recurrence_step has no gradient", x, gate, state)[0]
     a, (_, c), _, on = _geometry(x, None, form)
+    given = out
     if out is None:
         out = _s._empty(x.shape, x.dtype, x.device, stream)
     shape, dt = x.shape, x.dtype
@@ -154,4 +159,5 @@ def ak_gated_recurrence_step(x: torch.Tensor, gate: torch.Tensor, state: torch.T
         raise ValueError("state: a row for each request is needed")
     _s._check(_abi.load().ak_gated_recurrence_step(a, rx, rg, sp, at, pool, ro, _s._opts(opts), _s._stream_of(stream, x)),
               "ak_gated_recurrence_step")
+    _s._written(state, given)
     return out

@@ -95,6 +95,14 @@ def _dense_rows(t):
     return t.stride(-1) == 1 or t.shape[-1] <= 1 or t.numel() == 0
 
 
+def _written(*tensors):
+    """Tells autograd that a call has changed these (None: none). What it recorded on their values as they were raises in
+    its backward pass, as after PyTorch's own changes in place."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _workspace_ptr(nbytes, device, workspace, stream, on):
     """Pointer and size of a call's workspace, and the tensor that holds it: the caller keeps that until the entry
     point has returned, or the allocator may hand the memory out before the last launch is queued."""

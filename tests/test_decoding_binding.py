@@ -44,3 +44,45 @@ def test_numbers_past_32_bits_are_refused(host, call, name, value):  # noqa: F81
         with pytest.raises(ValueError, match=name):
             getattr(ak, call)(**tensors, **dict(rest, **{name: value + far}))
     assert not library.calls
+
+
+WRITTEN = {
+    "ak_gated_recurrence": {"out", "state_out"}, "ak_gated_recurrence_backward": {"dx", "dgate", "dstate"},
+    "ak_gated_recurrence_step": {"state", "out"}, "ak_beam_select": {"out"}, "ak_beam_reorder": {"state"}, "ak_blocks_count": {"out"},
+    "ak_blocks_fork": {"out"}, "ak_blocks_free": {"out", "counts"}, "ak_blocks_compact": {"out", "pairs", "counts"},
+    "ak_blocks_copy": {"cache"},
+}
+
+
+@pytest.mark.parametrize("call", WRITTEN)
+def test_autograd_learns_of_what_a_call_changes(host, call):  # noqa: F811
+    """A tensor's version counts its changes, and counts no reading."""
+    library = host(_Library())
+    tensors, rest = _calls()[call]
+    tensors = {n: _cuda(t) for n, t in tensors.items() if n != "workspace"}
+    i32 = lambda *s: _cuda(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    if call == "ak_beam_select":
+        tensors["out"] = ak.BeamStep(_cuda(torch.zeros(2, 3)), i32(2, 3), i32(2, 3), _cuda(torch.zeros(2, 3, dtype=torch.bool)), i32(2, 3))
+    if call == "ak_blocks_fork":
+        tensors["out"] = ak.BlockFork(i32(5, 4), i32(5), i32(9), i32(5, 2), i32(1))
+    before = {n: [u._version for u in (t if isinstance(t, tuple) else (t,))] for n, t in tensors.items()}
+    getattr(ak, call)(**tensors, **rest)
+    assert library.calls.pop(call)
+    for n, t in tensors.items():
+        for u, was in zip(t if isinstance(t, tuple) else (t,), before[n]):
+            assert (u._version > was) == (n in WRITTEN[call]), n
+
+
+@pytest.mark.parametrize("change", [
+    lambda s: ak.ak_gated_recurrence_step(_cuda(torch.zeros(4, 3)), _cuda(torch.zeros(4, 3)), s),
+    lambda s: ak.ak_gated_recurrence(_cuda(torch.zeros(4, 3)), _cuda(torch.zeros(4, 3)), out=s),
+    lambda s: ak.ak_beam_reorder(s.view(2, 2, 3), _cuda(torch.zeros(2, 2, dtype=torch.int32))),
+    lambda s: ak.ak_blocks_copy(s, _cuda(torch.zeros(2, 2, dtype=torch.int32))),
+])
+def test_a_backward_pass_over_what_has_changed_since_raises(host, change):  # noqa: F811
+    host(_Library())
+    state, w = _cuda(torch.ones(4, 3)), torch.ones(4, 3, requires_grad=True)
+    loss = (w * state).sum()
+    change(state)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
