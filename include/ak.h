@@ -652,7 +652,8 @@ ak_status ak_gated_recurrence_step(const ak_recurrence* shape, const ak_rows* x,
  * Sums of exponentials are float32 with compensation; logarithms, totals and
  * their comparison are 64-bit, out_scores rounded from them. A
  * logit of -infinity, and what has no finite rank, is no candidate; a row
- * that holds a NaN or +infinity, or a beam whose score is not finite, has none.
+ * that holds a NaN or +infinity, or a beam whose score is not finite or whose length^penalty
+ * is below 0 (a negative length), has none.
  * Where a request has fewer than `keep` candidates the rest of its beams get score
  * -infinity, token and parent -1, length 0 and done 1. No workspace.
  *

@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const BeamCall c) {
                 total += (double)value_of((uint32_t)(key >> 32)) + s.base[k];
             }
             const double q = c.penalty == 0.0 ? total : total / s.norm[k];
+            any = any && (c.penalty == 0.0 || s.norm[k] >= 0.0);  // (below 0 it would turn the order of the logits round)
             if (any && q > -INFINITY && q < INFINITY) v.rank = ordered(q);
             s.totals[k][lane] = (float)total;
             s.tokens[k][lane] = token;
