@@ -573,10 +573,12 @@ ak_status ak_linear_attention_step(const ak_linattn* shape, const ak_heads* q, c
  * token on (in gradients backwards in time).
  * Precision: a state is rounded where a token's run of up to 32, its tile of 8
  * runs and its cluster's step of up to 16 tiles meet, a few dozen times and not at
- * each token between, and factors near one are applied less one: relative and in
- * norm 1e-6 at memories of 10^4 tokens and equal gates (2e-7 at the gates of
- * ordinary models). In bf16 calls factors within a run are 2^-22 exact each, which
- * adds up to 4e-6 to states where every gate is the same; their outputs round to bf16.
+ * each token between, and factors near one are applied less one. Where every gate is
+ * the same, the worst for this, states were off by 2e-7 of their norm in the median
+ * over gates (memories of 1 to 10^5 tokens) and by 1.3e-6 at the worst gate. bf16 calls,
+ * whose factors within a run are rounded as they are, by 6e-7 and 3.5e-6 (1.4e-5 if each
+ * rounding pushed as far as it may); their outputs round to bf16. A gate's own factor is
+ * exact to 2^-21 + |gate| 2^-23 of itself, and below 2^-126 it is 0.
  * Range: factors of up to 256 tokens are multiplied before the state they meet, so
  * log decays above 0 that reach e^88 within a tile may give infinities or NaN where
  * the recurrence would not.
@@ -648,9 +650,13 @@ ak_status ak_gated_recurrence_step(const ak_recurrence* shape, const ak_rows* x,
  *              and the beam it extends
  *   out_done, out_lengths  device, likewise, or NULL
  * With keep = beams, out_scores, out_done and out_lengths may be scores, done and
- * lengths themselves.
- * Sums of exponentials are float32 with compensation; logarithms, totals and
- * their comparison are 64-bit, out_scores rounded from them. A
+ * lengths themselves (with another number of them, those of one request).
+ * Exponentials are float32, as are their sums, with compensation; logarithms, totals
+ * and their comparison are 64-bit, out_scores rounded from them. Within a beam logits
+ * decide, exactly. Between beams a logarithm that is off may: by 2e-7 at most where logits lie
+ * in any order, 2.3e-7 where they rise along the row (2^-21 + d 2^-22.8 + m 2^-21.6, d the mean
+ * distance of what is summed below the row's largest logit, m the larger logits
+ * that one thread meets). A
  * logit of -infinity, and what has no finite rank, is no candidate; a row
  * that holds a NaN or +infinity, or a beam whose score is not finite or whose length^penalty
  * is below 0 (a negative length), has none.

@@ -15,7 +15,7 @@
 //              i-th hole before it                             (two scans of one count)
 // The four that compute on tables are each one launch of one cluster of up to
 // 16 blocks of 1024 threads, whose phases the cluster's barrier separates: such
-// tables are some 100 KB, and a second launch would cost more than the rest of the
+// tables are some hundred KB, and a second launch would cost more than the rest of the
 // device could save. Histogram and ownership use integer atomics, whose order
 // does not show. Only the copies touch the pool's bytes; they take the whole device.
 //

@@ -35,7 +35,7 @@
 // run whose factors are all above 1/2 are applied so as well.
 //
 // Bound by the latency of a step (fold, maps, chain, outputs: 4000 cycles for two
-// tiles of 256 tokens x 32 channels bf16 an SM, 24 KB read and 16 written each),
+// tiles of 256 tokens x 32 channels bf16 an SM, 32 KB read and 16 written each),
 // not by its loads. Back to back: 16384 x 4096 bf16 95 us (0.63 of the copy
 // bandwidth), gradients of 8192 x 4096 bf16 93 us (0.53), 8192 x 4096 float32 77 to
 // 79 us (0.76), 32771 x 640 float32 65 us (0.57) and its gradients 102 us, 331 x 1000
@@ -125,8 +125,10 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// a and b of a gate, both to their own relative precision, 2^-21. Where results are
-// bf16 e stops at 2^126: a has long been nothing beside b there.
+// a and b of a gate, each to 2^-21 + |g| 2^-23 of itself (the exponential's instruction
+// 2^-22, its argument's product and constant |g| 2^-23.7, a sum, a reciprocal and a
+// product 2^-22); below 2^-126 they are 0. Where results are bf16 e stops at 2^126: a has
+// long been nothing beside b there.
 template <class T, int FORM>
 __device__ __forceinline__ void weights(float g, float& a, float& b) {
     constexpr bool kFast = sizeof(T) == 2;
