@@ -654,8 +654,8 @@ ak_status ak_gated_recurrence_step(const ak_recurrence* shape, const ak_rows* x,
  * Exponentials are float32, as are their sums, with compensation; logarithms, totals
  * and their comparison are 64-bit, out_scores rounded from them. Within a beam logits
  * decide, exactly. Between beams a logarithm that is off may: by 2e-7 at most where logits lie
- * in any order, 2.3e-7 where they rise along the row (2^-21 + d 2^-22.8 + m 2^-21.6, d the mean
- * distance of what is summed below the row's largest logit, m the larger logits
+ * in any order, 2.3e-7 where they rise along the row (2^-21 + d 2^-22.8 + (m + 2) 2^-21.6, d the
+ * mean distance of what is summed below the row's largest logit, m the larger logits
  * that one thread meets). A
  * logit of -infinity, and what has no finite rank, is no candidate; a row
  * that holds a NaN or +infinity, or a beam whose score is not finite or whose length^penalty
