@@ -71,6 +71,9 @@ __device__ __forceinline__ int64_t held(int32_t len, int32_t block, int64_t widt
     return len <= 0 ? 0 : min(((int64_t)len + block - 1) / block, width);
 }
 
+// Pieces of a row that a warp takes; at least one, as a row without entries has a length.
+__device__ __forceinline__ int64_t row_parts(int64_t width) { return max((int64_t)1, (width + kPart - 1) / kPart); }
+
 // Exclusive sum over the block's threads and the total. Ends in sync.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) k_blocks_count(const BlocksCall c) {
     for (int64_t i = team.thread(); i < c.blocks; i += team.threads()) c.refs[i] = 0;
     team.sync();
     const int lane = threadIdx.x % kWarp;
-    const int64_t parts = (c.width + kPart - 1) / kPart;
+    const int64_t parts = row_parts(c.width);
     for (int64_t w = team.warp(); w < c.rows * parts; w += team.warps()) {
         const int64_t r = div_fast(w, parts), col = (w - r * parts) * kPart;
         const int64_t end = min(held(c.lens[r], c.block_size, c.width), col + kPart);
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) k_blocks_fork(const BlocksCall c) {
     for (int64_t i = team.thread(); i < 2 * c.rows; i += team.threads()) c.pairs[i] = -1;
     team.sync();
 
-    const int64_t parts = max(1, (c.width + kPart - 1) / kPart);  // (a row without entries has a length)
+    const int64_t parts = row_parts(c.width);
     for (int64_t w = team.warp(); w < c.rows * parts; w += team.warps()) {
         const int64_t r = div_fast(w, parts), part = w - r * parts, col = part * kPart;
         const int32_t p = c.parents[r];
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) k_blocks_compact(const BlocksCall c)
     // ---- the table's entries
     const int lane = threadIdx.x % kWarp;
     const bool in_place = c.out_table == c.table;
-    const int64_t parts = (c.width + kPart - 1) / kPart;
+    const int64_t parts = row_parts(c.width);
     for (int64_t w = team.warp(); w < c.rows * parts; w += team.warps()) {
         const int64_t r = div_fast(w, parts), col = (w - r * parts) * kPart;
         const int64_t used = held(c.lens[r], c.block_size, c.width);
