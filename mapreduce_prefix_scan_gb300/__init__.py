@@ -20,8 +20,9 @@ import torch
 
 from . import _abi
 from ._abi import DTYPES, MAPS, MAPS2, OPS, SHAPES, STORES
-from .decoding import (BeamStep, BlockFork, ak_beam_reorder, ak_beam_select, ak_blocks_compact, ak_blocks_copy,
-                       ak_blocks_count, ak_blocks_fork, ak_blocks_free)
+from .decoding import (BeamStep, BlockFork, ak_beam_reorder, ak_beam_select, ak_blocks_compact,
+                       ak_blocks_compact_workspace_size, ak_blocks_copy, ak_blocks_count, ak_blocks_fork,
+                       ak_blocks_fork_workspace_size, ak_blocks_free)
 from .recurrence import ak_gated_recurrence, ak_gated_recurrence_backward, ak_gated_recurrence_step
 from .sequence import (BatchLayout, ak_batch_layout, ak_batch_layout_workspace_size, ak_linear_attention,
                        ak_linear_attention_backward, ak_linear_attention_step, ak_linear_attention_workspace_size,
@@ -35,7 +36,8 @@ __all__ = ["AkError", "ak_reduce", "ak_reduce2", "ak_reduce_dims", "ak_accumulat
            "ak_linear_attention_backward", "ak_linear_attention_step", "ak_linear_attention_workspace_size",
            "ak_gated_recurrence", "ak_gated_recurrence_backward", "ak_gated_recurrence_step", "BeamStep",
            "ak_beam_select", "ak_beam_reorder", "BlockFork", "ak_blocks_count", "ak_blocks_fork", "ak_blocks_free",
-           "ak_blocks_compact", "ak_blocks_copy"]
+           "ak_blocks_compact", "ak_blocks_copy", "ak_blocks_fork_workspace_size",
+           "ak_blocks_compact_workspace_size"]
 
 _TORCH = {torch.float32: "f32", torch.float64: "f64", torch.bfloat16: "bf16", torch.int32: "i32",
           torch.int64: "i64", torch.uint8: "u8", torch.bool: "u8"}

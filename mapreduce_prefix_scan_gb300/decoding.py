@@ -184,6 +184,22 @@ def ak_blocks_count(block_table: torch.Tensor, lens: torch.Tensor, *, block_size
     return refs
 
 
+def ak_blocks_fork_workspace_size(rows: int, blocks: int, opts=None) -> int:
+    """Bytes of the ``workspace`` of a fork into ``rows`` requests over a pool of ``blocks``."""
+    b = ctypes.c_size_t()
+    _s._check(_abi.load().ak_blocks_fork_workspace_size(int(rows), int(blocks), _s._opts(opts), ctypes.byref(b)),
+              "ak_blocks_fork_workspace_size")
+    return b.value
+
+
+def ak_blocks_compact_workspace_size(blocks: int, opts=None) -> int:
+    """Bytes of the ``workspace`` of a compaction of a pool of ``blocks``."""
+    b = ctypes.c_size_t()
+    _s._check(_abi.load().ak_blocks_compact_workspace_size(int(blocks), _s._opts(opts), ctypes.byref(b)),
+              "ak_blocks_compact_workspace_size")
+    return b.value
+
+
 def ak_blocks_fork(block_table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor, free_blocks: torch.Tensor, *,
                    block_size: int, blocks: int, out: BlockFork | None = None, workspace=None, opts=None,
                    stream=None) -> BlockFork:

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import mapreduce_prefix_scan_gb300 as ak
-from test_decoding_abi import _calls
+from test_decoding_abi import L, _calls  # noqa: F401
 from test_sequence_binding import _Library, _cuda, host  # noqa: F401
 
 
@@ -86,3 +86,22 @@ def test_a_backward_pass_over_what_has_changed_since_raises(host, change):  # no
     change(state)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_workspaces_can_be_sized(host, L):  # noqa: F811
+    """What the queries answer is what the calls take, to the byte."""
+    fork, compact = ak.ak_blocks_fork_workspace_size(5, 9), ak.ak_blocks_compact_workspace_size(9)
+    assert fork >= 4 * (2 * 9 + 5) and compact >= 4 * (2 * 4 + 9)
+    with pytest.raises(ak.AkError):
+        ak.ak_blocks_fork_workspace_size(-1, 9)
+    with pytest.raises(ak.AkError):
+        ak.ak_blocks_compact_workspace_size(-1)
+    for call, size in (("ak_blocks_fork", fork), ("ak_blocks_compact", compact)):
+        library = host(_Library(sizes=size))
+        tensors, rest = _calls()[call]
+        tensors = {n: _cuda(t) for n, t in tensors.items()}
+        getattr(ak, call)(**dict(tensors, workspace=_cuda(torch.zeros(size, dtype=torch.uint8))), **rest)
+        assert library.calls.pop(call)
+        with pytest.raises(ValueError, match="workspace"):
+            getattr(ak, call)(**dict(tensors, workspace=_cuda(torch.zeros(size - 1, dtype=torch.uint8))), **rest)
+        assert not library.calls
